@@ -478,6 +478,82 @@ fsdp_status fsdp_step_plan_launch_ex(fsdp_step_plan *plan, const fsdp_step_confi
 /* Free a plan (NULL is a no-op). Launches already enqueued complete. */
 fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
 
+/* Softmax cross entropy of a linear head (device): the loss of the last
+ * hidden states, and its gradients, without the tokens x vocab logits. Over
+ * rows t < tokens, columns v < vocab:
+ *   l[t,v]  = sum_k hidden[t,k] * weight[v,k]            (fp32 sums)
+ *   lse[t]  = log(sum_v exp(l[t,v]))
+ *   token_loss[t] = lse[t] - l[t, targets[t]]
+ *   loss    = sum_t token_loss[t] / n (MEAN; 0 when n is 0) or the sum (SUM)
+ *   d[t,v]  = exp(l[t,v] - lse[t]) - (v == targets[t])
+ *   d_hidden = g * d * weight,   d_weight = g * d^T * hidden
+ *   g       = grad_scale / n (MEAN) or grad_scale (SUM)
+ * n is the number of rows whose target is not ignore_index; the others have
+ * loss 0 and no gradient. A target outside [0, vocab) that is not
+ * ignore_index makes its row's loss and gradients NaN. Both gradients are
+ * overwritten, not added to; the pair (weight, d_weight) may be views of a
+ * unit's gathered buffer and of a rank's flat gradient buffer, whatever their
+ * alignment, so that the gradient lands where the reduce-scatter reads it
+ * ("Data Parallelism", "The Basic Protocol": each worker's backward pass
+ * gives the gradients that are then averaged).
+ * Precision: every sum and statistic is fp32 or wider. bf16 and fp16 heads:
+ * d is rounded once to the head's type (fp16: times 2^14) for the gradient
+ * products, the exponentials are held in fp16 relative to the largest of 128
+ * columns before that. fp32 heads: every operand as three bf16 parts, the
+ * products as exact as fp32's.
+ *   hidden       device, tokens rows of dim elements at stride ld_hidden.
+ *   weight       device, vocab rows of dim elements at stride ld_weight.
+ *                Rows that are not 16-byte aligned are packed into the
+ *                workspace first.
+ *   targets      device int64, tokens.
+ *   dtype        fsdp_dtype of hidden, weight and both gradients.
+ *   band         tokens worked on together; 0: as many as keep the 16-bit
+ *                exponentials within 2 GiB. A gradient call of more tokens
+ *                than that adds the bands' weight gradients in fp32 in the
+ *                workspace (4 * vocab * dim bytes).
+ *   loss         device fp32 scalar. token_loss: device fp32, tokens, or NULL.
+ *   d_hidden, d_weight   device, or NULL: that gradient is not formed; with
+ *                both NULL only the losses are.
+ *   wait_timeouts  device uint32 or NULL: incremented by each bounded wait of
+ *                this call that gave up (see "Bounded waits" above; this
+ *                call's waits show here only).
+ * No output may overlap an input or another output. tokens may be 0. */
+typedef enum { FSDP_LOSS_MEAN = 0, FSDP_LOSS_SUM = 1 } fsdp_loss_reduction;
+
+typedef struct {
+    const void *hidden;
+    int64_t ld_hidden;
+    const void *weight;
+    int64_t ld_weight;
+    const int64_t *targets;
+    int64_t tokens;
+    int64_t vocab;
+    int64_t dim;
+    int64_t ignore_index;
+    int64_t band;
+    int32_t dtype;        /* fsdp_dtype */
+    int32_t reduction;    /* fsdp_loss_reduction */
+    float grad_scale;     /* the loss scale the gradients carry; 1 if none */
+    int32_t reserved;     /* must be 0 */
+    float *loss;
+    float *token_loss;
+    void *d_hidden;
+    int64_t ld_d_hidden;
+    void *d_weight;
+    int64_t ld_d_weight;
+    uint32_t *wait_timeouts;
+} fsdp_head_loss_args;
+
+/* Bytes of workspace fsdp_head_loss needs for these arguments (host only;
+ * they depend on the sizes, the type, the band, which outputs are asked for
+ * and whether hidden and weight are 16-byte aligned). */
+fsdp_status fsdp_head_loss_workspace(const fsdp_head_loss_args *args, int64_t *bytes_out);
+
+/* Enqueue it. workspace: device, at least that many bytes, 1024-byte aligned,
+ * not overlapping any buffer of the call; its contents before the call do not
+ * matter and nothing is kept in it between calls. */
+fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char *fsdp_status_string(fsdp_status status);
 

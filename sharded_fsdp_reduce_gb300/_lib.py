@@ -24,6 +24,7 @@ FSDP_ERR_HOST_MEMORY = 5
 
 FSDP_F32, FSDP_BF16, FSDP_F16 = 0, 1, 2
 FSDP_OPT_ADAMW, FSDP_OPT_SGD, FSDP_OPT_ADAMAX, FSDP_OPT_ADADELTA = 0, 1, 2, 3
+FSDP_LOSS_MEAN, FSDP_LOSS_SUM = 0, 1
 
 # every symbol include/fsdp.h declares
 EXPORTS = (
@@ -52,6 +53,8 @@ EXPORTS = (
     "fsdp_step_plan_launch",
     "fsdp_step_plan_launch_ex",
     "fsdp_step_plan_destroy",
+    "fsdp_head_loss_workspace",
+    "fsdp_head_loss",
 )
 
 
@@ -86,6 +89,16 @@ class FsdpUnitEx(ctypes.Structure):
                 ("padded_numel", ctypes.c_int64), ("world", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
                 ("state_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("n_full", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class FsdpHeadLossArgs(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_void_p), ("ld_hidden", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("ld_weight", ctypes.c_int64), ("targets", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+                ("band", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reduction", ctypes.c_int32),
+                ("grad_scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("loss", ctypes.c_void_p),
+                ("token_loss", ctypes.c_void_p), ("d_hidden", ctypes.c_void_p), ("ld_d_hidden", ctypes.c_int64),
+                ("d_weight", ctypes.c_void_p), ("ld_d_weight", ctypes.c_int64), ("wait_timeouts", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -139,6 +152,8 @@ def load() -> ctypes.CDLL:
             "fsdp_step_plan_launch": (i32, [vp, ctypes.POINTER(FsdpAdamwHparams), vp]),
             "fsdp_step_plan_launch_ex": (i32, [vp, ctypes.POINTER(FsdpStepConfig), vp]),
             "fsdp_step_plan_destroy": (i32, [vp]),
+            "fsdp_head_loss_workspace": (i32, [ctypes.POINTER(FsdpHeadLossArgs), ctypes.POINTER(i64)]),
+            "fsdp_head_loss": (i32, [ctypes.POINTER(FsdpHeadLossArgs), vp, i64, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)

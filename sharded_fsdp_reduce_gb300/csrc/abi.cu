@@ -15,10 +15,6 @@
 #include "group.cuh"
 #include "host.cuh"
 
-// The library's exported symbols: the C ABI of include/fsdp.h and nothing else
-// (everything else is built with hidden visibility).
-#define FSDP_API __attribute__((visibility("default")))
-
 namespace fsdp {
 
 namespace {

@@ -8,6 +8,10 @@
 
 #include "common.cuh"
 
+// The library's exported symbols: the C ABI of include/fsdp.h and nothing else
+// (everything else is built with hidden visibility).
+#define FSDP_API __attribute__((visibility("default")))
+
 namespace fsdp {
 
 // SM count of the current device, cached per device.

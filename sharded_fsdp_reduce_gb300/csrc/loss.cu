@@ -1,0 +1,806 @@
+// loss.cu -- softmax cross entropy of a linear head: fsdp_head_loss.
+//
+//   l[t,v] = sum_k X[t,k] W[v,k]        lse[t] = log sum_v exp l[t,v]
+//   loss_t = lse[t] - l[t,y_t]          d[t,v] = exp(l[t,v] - lse[t]) - [v = y_t]
+//   dX = g d W                          dW = g d^T X
+//
+// The logits in fp32 live in tensor memory only. The logits product's epilogue
+// turns each span of 128 columns into exponentials against the span's own
+// maximum, and keeps their fp32 sum and that reference; a row kernel joins the
+// spans into lse. Without gradients that is all: X and W are read, a few bytes
+// per span are written. With gradients the exponentials of a band of tokens
+// are also stored, in 16 bits, and turned in place into d; the two gradient
+// products read d as it lies. That is three products of 2TVD operations
+// instead of the four that forming the logits again would take, for one pass
+// over the band (4 bytes an element): with D = 8192 a product's operations
+// take 8 times that pass, with D = 768 about as long.
+#include <math.h>
+#include <string.h>
+
+#include "loss.cuh"
+
+namespace fsdp {
+namespace loss {
+namespace {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+// fp16 gradients of the logits are held times 2^14: d is at most 1 in
+// magnitude, and a probability down to 2^-28 keeps all its bits.
+constexpr float kHalfGain = 16384.0f;
+
+// ---------------------------------------------------------------- rows
+
+struct RowArgs {
+    const float *off, *sum;  // [spans][ld_rows]
+    int64_t ld_rows;
+    int32_t spans;
+    const float *target_logit;
+    const int64_t *targets;
+    int64_t rows, vocab, ignore;
+    float *lse2;             // log2-sum of the row's exponentials
+    float *token_loss;       // or NULL
+    // the loss over all bands: block sums, joined by the last block
+    double *part_sum;
+    int64_t *part_count;
+    int64_t first_block, all_blocks;
+    uint32_t *ticket;
+    float *loss, *scale;
+    float grad_scale;
+    int32_t mean;
+};
+
+__device__ double warp_sum(double x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__device__ long long warp_sum(long long x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// 32 rows per block: lane = row, the warps share the row's spans. The
+// statistics lie span by span, so a warp's reads are contiguous. The loss
+// adds up per block, then over the blocks in one fixed order, in fp64.
+__global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowArgs a) {
+    __shared__ float tops[32][33], sums[32][33];
+    __shared__ double total[32];
+    __shared__ long long count[32];
+    __shared__ bool last;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t row = int64_t(blockIdx.x) * 32 + lane;
+    const bool live = row < a.rows;
+    float top = -INFINITY, sum = 0.0f;
+    if (live) {
+        for (int s = warp; s < a.spans; s += 32) {
+            const float o = a.off[s * a.ld_rows + row], x = a.sum[s * a.ld_rows + row];
+            if (o > top) {
+                sum = sum * exp2f(top - o) + x;
+                top = o;
+            } else {
+                sum += x * exp2f(o - top);
+            }
+        }
+    }
+    tops[warp][lane] = top;
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        double loss = 0.0;
+        long long valid = 0;
+        if (live) {
+            for (int w = 1; w < 32; ++w) top = fmaxf(top, tops[w][lane]);
+            float all = 0.0f;
+            for (int w = 0; w < 32; ++w)
+                if (w < a.spans) all += sums[w][lane] * exp2f(tops[w][lane] - top);
+            const float lse2 = top + log2f(all);
+            a.lse2[row] = lse2;
+            const int64_t y = a.targets[row];
+            float t = 0.0f;
+            if (y != a.ignore) {
+                valid = 1;
+                // a target outside the vocabulary has no loss: it shows as NaN
+                t = y >= 0 && y < a.vocab ? lse2 * kLn2 - a.target_logit[row] : NAN;
+            }
+            if (a.token_loss != nullptr) a.token_loss[row] = t;
+            loss = t;
+        }
+        loss = warp_sum(loss);
+        valid = warp_sum(valid);
+        if (lane == 0) {
+            a.part_sum[a.first_block + blockIdx.x] = loss;
+            a.part_count[a.first_block + blockIdx.x] = valid;
+            __threadfence();
+            last = atomicAdd(a.ticket, 1u) + 1 == static_cast<uint32_t>(a.all_blocks);
+        }
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double x = 0.0;
+    long long n = 0;
+    for (int64_t i = threadIdx.x; i < a.all_blocks; i += 1024) {
+        x += __ldcg(a.part_sum + i);
+        n += __ldcg(reinterpret_cast<const long long *>(a.part_count) + i);
+    }
+    x = warp_sum(x);
+    n = warp_sum(n);
+    if (lane == 0) {
+        total[warp] = x;
+        count[warp] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        x = warp_sum(total[lane]);
+        n = warp_sum(count[lane]);
+        if (lane == 0) {
+            const double by = a.mean && n > 0 ? static_cast<double>(n) : 1.0;
+            *a.loss = static_cast<float>(x / by);
+            *a.scale = static_cast<float>(a.grad_scale / by);
+        }
+    }
+}
+
+// The gradients' common factor before the last band's loss is known: the
+// valid rows of every band (only when there are several).
+__global__ void __launch_bounds__(1024)
+    count_kernel(const int64_t *targets, int64_t rows, int64_t ignore, float grad_scale, int mean, float *scale) {
+    __shared__ long long count[32];
+    long long n = 0;
+    for (int64_t i = threadIdx.x; i < rows; i += 1024) n += targets[i] != ignore;
+    n = warp_sum(n);
+    if (threadIdx.x % 32 == 0) count[threadIdx.x / 32] = n;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        n = warp_sum(count[threadIdx.x]);
+        if (threadIdx.x == 0) *scale = static_cast<float>(grad_scale / (mean && n > 0 ? static_cast<double>(n) : 1.0));
+    }
+}
+
+// ---------------------------------------------------------------- d from the exponentials
+
+struct GradArgs {
+    void *e;                 // [rows][ld] exponentials; 16-bit types: d in place
+    uint16_t *planes[3];     // an fp32 head: d as three bf16 planes
+    int64_t ld, rows, vocab;
+    const float *off;        // [spans][ld_rows]
+    int64_t ld_rows;
+    const float *lse2;
+    const int64_t *targets;
+    int64_t ignore;
+    uint32_t col_blocks;
+};
+
+// x in three bf16 parts: each takes the next 8 bits.
+__device__ __forceinline__ void split3(float x, float &hi, float &mid, float &lo) {
+    hi = __bfloat162float(__float2bfloat16_rn(x));
+    const float r = x - hi;
+    mid = __bfloat162float(__float2bfloat16_rn(r));
+    lo = r - mid;
+}
+
+constexpr int kGradCols = 512, kGradRows = 64;
+
+// 64 rows x 512 columns per block, 8 columns per thread and row. Bound by HBM
+// (or L2, where the band fits): 4 bytes moved per element in 16-bit types.
+template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __grid_constant__ GradArgs a) {
+    __shared__ float factor[kGradCols / kSpan][kGradRows];
+    __shared__ int32_t hit[kGradRows];  // the target's column in this block, or -1; -2: no gradient
+    const int64_t row0 = int64_t(blockIdx.x / a.col_blocks) * kGradRows;
+    const int64_t col0 = int64_t(blockIdx.x % a.col_blocks) * kGradCols;
+    constexpr float kGain = DT == FSDP_F16 ? kHalfGain : 1.0f;
+    {
+        const int r = threadIdx.x % kGradRows, s = threadIdx.x / kGradRows;
+        const int64_t row = row0 + r, span = col0 / kSpan + s;
+        if (row < a.rows) {
+            // e * 2^(off - lse2) is the probability; a target outside the
+            // vocabulary makes the row's gradient NaN, as its loss is
+            const int64_t y = a.targets[row], at = y - col0;
+            const bool bad = y != a.ignore && (y < 0 || y >= a.vocab);
+            if (span * kSpan < a.vocab)
+                factor[s][r] = bad ? NAN : kGain * exp2f(a.off[span * a.ld_rows + row] - a.lse2[row]);
+            if (s == 0) hit[r] = y == a.ignore ? -2 : at >= 0 && at < kGradCols ? static_cast<int32_t>(at) : -1;
+        }
+    }
+    __syncthreads();
+    const int c = threadIdx.x % (kGradCols / 8) * 8;
+    const int64_t col = col0 + c;
+    if (col >= a.vocab) return;
+    const int rows = static_cast<int>(min(int64_t(kGradRows), a.rows - row0));
+#pragma unroll 4
+    for (int r = threadIdx.x / (kGradCols / 8); r < rows; r += 256 / (kGradCols / 8)) {
+        const int64_t at = (row0 + r) * a.ld + col;
+        const float f = factor[c / kSpan][r];
+        const int h = hit[r] - c;
+        float v[8];
+        if constexpr (DT == FSDP_F32) {
+            const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.e) + at);
+            const float4 y = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.e) + at + 4);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+        } else {
+            unpack8<FSDP_F16>(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.e) + at), v);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] *= f;
+            if (h == j) v[j] -= kGain;
+        }
+        if (hit[r] == -2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        }
+        if constexpr (DT == FSDP_F32) {
+            float p[3][8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) split3(v[j], p[0][j], p[1][j], p[2][j]);
+#pragma unroll
+            for (int z = 0; z < 3; ++z)
+                *reinterpret_cast<uint4 *>(a.planes[z] + at) =
+                    make_uint4(pack2<FSDP_BF16>(p[z][0], p[z][1]), pack2<FSDP_BF16>(p[z][2], p[z][3]),
+                               pack2<FSDP_BF16>(p[z][4], p[z][5]), pack2<FSDP_BF16>(p[z][6], p[z][7]));
+        } else {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.e) + at) =
+                make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- operands TMA cannot address
+
+// rows x cols at stride ld into 16-bit rows padded to ldp (a multiple of 8):
+// a copy for 16-bit types, three bf16 planes for fp32.
+template <bool F32>
+__global__ void __launch_bounds__(256) pack_kernel(const void *src, int64_t rows, int64_t cols, int64_t ld,
+                                                   uint16_t *dst, int64_t ldp, int64_t plane) {
+    const int64_t words = ldp / 8, total = rows * words;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+        const int64_t r = i / words, c = (i - r * words) * 8;
+        const int n = static_cast<int>(min(int64_t(8), cols - c));
+        if constexpr (F32) {
+            const float *s = static_cast<const float *>(src) + r * ld + c;
+            float p[3][8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) split3(j < n ? s[j] : 0.0f, p[0][j], p[1][j], p[2][j]);
+#pragma unroll
+            for (int z = 0; z < 3; ++z)
+                *reinterpret_cast<uint4 *>(dst + z * plane + r * ldp + c) =
+                    make_uint4(pack2<FSDP_BF16>(p[z][0], p[z][1]), pack2<FSDP_BF16>(p[z][2], p[z][3]),
+                               pack2<FSDP_BF16>(p[z][4], p[z][5]), pack2<FSDP_BF16>(p[z][6], p[z][7]));
+        } else {
+            const uint16_t *s = static_cast<const uint16_t *>(src) + r * ld + c;
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t lo = 2 * j < n ? s[2 * j] : 0u, hi = 2 * j + 1 < n ? s[2 * j + 1] : 0u;
+                w[j] = lo | (hi << 16);
+            }
+            *reinterpret_cast<uint4 *>(dst + r * ldp + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- split products
+
+// out = scale * sum over the splits, in their order.
+template <int DT>
+__global__ void __launch_bounds__(256) join_kernel(const float *part, int splits, int64_t split_stride, int64_t rows,
+                                                   int64_t cols, int64_t ldp, const float *scale, float scale_const,
+                                                   void *out, int64_t ld) {
+    const float f = scale_const * *scale;
+    const int64_t words = ldp / 4, total = rows * words;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+        const int64_t r = i / words, c = (i - r * words) * 4;
+        float4 x = *reinterpret_cast<const float4 *>(part + r * ldp + c);
+        for (int s = 1; s < splits; ++s) {
+            const float4 y = *reinterpret_cast<const float4 *>(part + s * split_stride + r * ldp + c);
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        const float v[4] = {x.x * f, x.y * f, x.z * f, x.w * f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j < cols) Dtype<DT>::store(out, r * ld + c + j, v[j]);
+    }
+}
+
+// ---------------------------------------------------------------- host: the plan
+
+constexpr int64_t kDefaultBandBytes = int64_t(2) << 30;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+struct Plan {
+    bool f32, grad, pack_x, pack_w;
+    int64_t band, bands, spans, ldv, ldd, blocks;
+    int splits_x, splits_w;
+    // byte offsets into the workspace
+    int64_t scale, ticket, part_sum, part_count, lse2, target_logit, off, sum, x, w, e, d, part, sum_w, bytes;
+};
+
+// How many pieces a product's K is cut into: with few tiles most pairs would
+// idle, and with little more than a multiple of the pairs the last round is
+// nearly empty. Takes the least of rounds of K blocks (about 0.3 us each)
+// plus the fp32 partial results written and read (about 6 TB/s).
+int choose_splits(int64_t tiles, int64_t kblocks, int64_t m, int64_t n) {
+    const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= 32 && (s == 1 || kblocks / s >= 8); ++s) {
+        const double rounds = static_cast<double>(ceil_div(tiles * s, pairs));
+        double us = rounds * (static_cast<double>(ceil_div(kblocks, s)) * 0.3 + 2.0);
+        if (s > 1) us += 4.0 + static_cast<double>(m) * n * 8.0 * s / 6.0e6;
+        if (s == 1 || us < least) {
+            least = us;
+            best = s;
+        }
+    }
+    return best;
+}
+
+bool direct(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+Plan make_plan(const fsdp_head_loss_args &a) {
+    Plan p;
+    memset(&p, 0, sizeof(p));
+    p.f32 = a.dtype == FSDP_F32;
+    p.grad = a.d_hidden != nullptr || a.d_weight != nullptr;
+    p.pack_x = p.f32 || !direct(a.hidden, a.ld_hidden);
+    p.pack_w = p.f32 || !direct(a.weight, a.ld_weight);
+    p.ldv = round_up(a.vocab, 64);
+    p.ldd = round_up(a.dim, 64);
+    p.spans = ceil_div(a.vocab, kSpan);
+    const int64_t planes = p.f32 ? 3 : 1;
+    const int64_t per_row = p.ldv * (p.f32 ? 10 : 2);  // exponentials, and the planes of an fp32 head
+    int64_t band = a.band;
+    if (band == 0) {
+        // gradients: what fits the default budget; losses alone: the statistics
+        // (8 bytes a span and row) stay below it for any band this size
+        band = p.grad ? kDefaultBandBytes / per_row : kDefaultBandBytes / (8 * p.spans);
+        band = band / kTileM * kTileM;
+        if (band < kTileM) band = kTileM;
+    }
+    p.band = band < a.tokens ? band : a.tokens;
+    p.bands = ceil_div(a.tokens, p.band);
+    p.blocks = 0;
+    for (int64_t b = 0; b < p.bands; ++b) {
+        const int64_t rows = a.tokens - b * p.band < p.band ? a.tokens - b * p.band : p.band;
+        p.blocks += ceil_div(rows, 32);
+    }
+    p.splits_x = p.splits_w = 1;
+    const int64_t pairs = p.f32 ? 6 : 1;
+    if (a.d_hidden)
+        p.splits_x = choose_splits(ceil_div(p.band, kTileM) * ceil_div(a.dim, kTileN),
+                                   ceil_div(a.vocab, kBlockK) * pairs, p.band, p.ldd);
+    if (a.d_weight && p.bands == 1)
+        p.splits_w = choose_splits(ceil_div(a.vocab, kTileM) * ceil_div(a.dim, kTileN),
+                                   ceil_div(p.band, kBlockK) * pairs, a.vocab, p.ldd);
+    int64_t at = 0;
+    auto take = [&at](int64_t bytes) {
+        const int64_t here = at;
+        at = round_up(at + bytes, 1024);
+        return here;
+    };
+    p.scale = take(8);
+    p.ticket = p.scale + 4;
+    p.part_sum = take(8 * p.blocks);
+    p.part_count = take(8 * p.blocks);
+    p.lse2 = take(4 * p.band);
+    p.target_logit = take(4 * p.band);
+    p.off = take(4 * p.spans * p.band);
+    p.sum = take(4 * p.spans * p.band);
+    if (p.pack_x) p.x = take(2 * planes * a.tokens * p.ldd);
+    if (p.pack_w) p.w = take(2 * planes * a.vocab * p.ldd);
+    if (p.grad) {
+        p.e = take(p.band * p.ldv * (p.f32 ? 4 : 2));
+        p.d = p.f32 ? take(p.band * p.ldv * 6) : p.e;
+        const int64_t part_x = p.splits_x > 1 ? 4 * p.splits_x * p.band * p.ldd : 0;
+        const int64_t part_w = p.splits_w > 1 ? 4 * p.splits_w * a.vocab * p.ldd : 0;
+        p.part = take(part_x > part_w ? part_x : part_w);
+        if (a.d_weight && p.bands > 1) p.sum_w = take(4 * a.vocab * p.ldd);
+    }
+    p.bytes = at;
+    return p;
+}
+
+// ---------------------------------------------------------------- host: tensor maps
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled through the runtime's lookup (the library links no
+// driver library of its own); null if the driver has none.
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !f) {
+            (void)cudaGetLastError();
+            return static_cast<EncodeFn>(nullptr);
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// Rows of `cols` elements at stride ld, `planes` of them; boxes of 128 bytes
+// by box_rows, 128-byte swizzle, zeros outside.
+fsdp_status make_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, int64_t cols,
+                     int64_t rows, int64_t planes, int64_t ld, int64_t plane, int box_rows) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return cuda_status(cudaErrorNotSupported);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(planes)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * size), static_cast<cuuint64_t>(plane * size)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t unit[3] = {1, 1, 1};
+    const CUresult r = fn(map, type, 3, const_cast<void *>(base), dims, strides, box, unit,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FSDP_OK : cuda_status(cudaErrorInvalidValue);
+}
+
+CUtensorMapDataType map_type(int dtype) {
+    return dtype == FSDP_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+           : dtype == FSDP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+int grid_of(int64_t items) {
+    const int64_t want = ceil_div(items, 256), most = static_cast<int64_t>(sm_count()) * 16;
+    return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+}
+
+// ---------------------------------------------------------------- host: one call
+
+// A 16-bit operand as its products see it.
+struct Operand {
+    const uint8_t *base;
+    int64_t ld, plane;
+    int planes;
+};
+
+fsdp_status pack(const void *src, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t *dst, int64_t ldp,
+                 cudaStream_t s) {
+    const int grid = grid_of(rows * ldp / 8);
+    uint16_t *d = reinterpret_cast<uint16_t *>(dst);
+    if (f32)
+        pack_kernel<true><<<grid, 256, 0, s>>>(src, rows, cols, ld, d, ldp, rows * ldp);
+    else
+        pack_kernel<false><<<grid, 256, 0, s>>>(src, rows, cols, ld, d, ldp, rows * ldp);
+    return check_launch();
+}
+
+fsdp_status launch_grad(int dtype, Orders o, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
+                        const GemmArgs &g, cudaStream_t s) {
+    switch (dtype) {
+        case FSDP_BF16: return launch_grad_bf16(o, a, b, out, g, s);
+        case FSDP_F16: return launch_grad_f16(o, a, b, out, g, s);
+        default: return launch_grad_f32(o, a, b, out, g, s);
+    }
+}
+
+// One gradient product: out [M,N] of dtype at stride ld = scale * (A B + earlier), K split as planned.
+struct Product {
+    Orders orders;
+    int64_t M, N, K;
+    int splits;
+    const float *earlier;
+    int64_t ld_earlier;
+    void *out;
+    int64_t ld_out;
+    int out_dtype;
+    bool scaled;  // false: a band's fp32 sum, scaled with the last band
+};
+
+fsdp_status run_product(const Product &q, const Plan &p, const fsdp_head_loss_args &a, uint8_t *ws,
+                        const CUtensorMap &ma, const CUtensorMap &mb, cudaStream_t s) {
+    GemmArgs g;
+    memset(&g, 0, sizeof(g));
+    g.M = q.M;
+    g.N = q.N;
+    g.kblocks = static_cast<int32_t>(ceil_div(q.K, kBlockK));
+    g.pairs = p.f32 ? 6 : 1;
+    g.tiles_m = static_cast<int32_t>(ceil_div(q.M, kTileM));
+    g.tiles_n = static_cast<int32_t>(ceil_div(q.N, kTileN));
+    g.splits = q.splits;
+    // dW: all column tiles of a row tile together (d is read once, X stays in
+    // L2); dX: squares of tiles, both operands being long in K
+    g.m_fast = q.orders == kHiddenGrad;
+    g.group = q.orders == kHiddenGrad ? 8 : 32;
+    g.operand_type = a.dtype == FSDP_F16 ? 0 : 1;
+    const float *scale = reinterpret_cast<const float *>(ws + p.scale);
+    const float gain = a.dtype == FSDP_F16 ? 1.0f / kHalfGain : 1.0f;
+    g.timeouts = a.wait_timeouts;
+    CUtensorMap mo = ma;  // unused without TMA stores
+    if (q.splits > 1) {
+        g.scale_const = 1.0f;
+        g.tma_store = 1;
+        float *part = reinterpret_cast<float *>(ws + p.part);
+        fsdp_status st = make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, part, q.N, q.M, q.splits, p.ldd,
+                                  q.M * p.ldd, 32);
+        if (st == FSDP_OK) st = launch_grad_f32(q.orders, ma, mb, mo, g, s);
+        if (st != FSDP_OK) return st;
+        const int grid = grid_of(q.M * p.ldd / 4);
+        switch (q.out_dtype) {
+            case FSDP_BF16:
+                join_kernel<FSDP_BF16><<<grid, 256, 0, s>>>(part, q.splits, q.M * p.ldd, q.M, q.N, p.ldd, scale, gain,
+                                                            q.out, q.ld_out);
+                break;
+            case FSDP_F16:
+                join_kernel<FSDP_F16><<<grid, 256, 0, s>>>(part, q.splits, q.M * p.ldd, q.M, q.N, p.ldd, scale, gain,
+                                                           q.out, q.ld_out);
+                break;
+            default:
+                join_kernel<FSDP_F32><<<grid, 256, 0, s>>>(part, q.splits, q.M * p.ldd, q.M, q.N, p.ldd, scale, gain,
+                                                           q.out, q.ld_out);
+        }
+        return check_launch();
+    }
+    g.scale = q.scaled ? scale : nullptr;
+    g.scale_const = q.scaled ? gain : 1.0f;
+    g.earlier = q.earlier;
+    g.ld_earlier = q.ld_earlier;
+    g.out = q.out;
+    g.ld_out = q.ld_out;
+    const int size = dtype_size(q.out_dtype);
+    g.tma_store = aligned(q.out, 16) && q.ld_out * size % 16 == 0;
+    if (g.tma_store) {
+        const fsdp_status st =
+            make_map(&mo, map_type(q.out_dtype), size, q.out, q.N, q.M, 1, q.ld_out, q.M * q.ld_out, 32);
+        if (st != FSDP_OK) return st;
+    }
+    return launch_grad(q.out_dtype, q.orders, ma, mb, mo, g, s);
+}
+
+fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaStream_t s) {
+    const int64_t D = a.dim, V = a.vocab;
+    const int size = dtype_size(a.dtype);
+    const int planes = p.f32 ? 3 : 1;
+    Operand x{static_cast<const uint8_t *>(a.hidden), a.ld_hidden, a.tokens * a.ld_hidden, 1};
+    Operand w{static_cast<const uint8_t *>(a.weight), a.ld_weight, V * a.ld_weight, 1};
+    fsdp_status st = FSDP_OK;
+    if (p.pack_x) {
+        st = pack(a.hidden, p.f32, a.tokens, D, a.ld_hidden, ws + p.x, p.ldd, s);
+        x = Operand{ws + p.x, p.ldd, a.tokens * p.ldd, planes};
+    }
+    if (st == FSDP_OK && p.pack_w) {
+        st = pack(a.weight, p.f32, V, D, a.ld_weight, ws + p.w, p.ldd, s);
+        w = Operand{ws + p.w, p.ldd, V * p.ldd, planes};
+    }
+    if (st != FSDP_OK) return st;
+    float *scale = reinterpret_cast<float *>(ws + p.scale);
+    if (p.grad && p.bands > 1) {
+        count_kernel<<<1, 1024, 0, s>>>(a.targets, a.tokens, a.ignore_index, a.grad_scale,
+                                        a.reduction == FSDP_LOSS_MEAN, scale);
+        if ((st = check_launch()) != FSDP_OK) return st;
+    }
+    const CUtensorMapDataType t16 =
+        a.dtype == FSDP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap w_k, w_n;
+    st = make_map(&w_k, t16, 2, w.base, D, V, w.planes, w.ld, w.plane, 128);
+    if (st == FSDP_OK) st = make_map(&w_n, t16, 2, w.base, D, V, w.planes, w.ld, w.plane, 64);
+    if (st != FSDP_OK) return st;
+    int64_t block = 0;
+    for (int64_t b = 0; b < p.bands; ++b) {
+        const int64_t row0 = b * p.band;
+        const int64_t rows = a.tokens - row0 < p.band ? a.tokens - row0 : p.band;
+        const uint8_t *xb = x.base + 2 * row0 * x.ld;
+        CUtensorMap x_k, x_n, e_out;
+        st = make_map(&x_k, t16, 2, xb, D, rows, x.planes, x.ld, x.plane, 128);
+        if (st != FSDP_OK) return st;
+        // the logits, as statistics and exponentials
+        GemmArgs g;
+        memset(&g, 0, sizeof(g));
+        g.M = rows;
+        g.N = V;
+        g.kblocks = static_cast<int32_t>(ceil_div(D, kBlockK));
+        g.pairs = p.f32 ? 6 : 1;
+        g.tiles_m = static_cast<int32_t>(ceil_div(rows, kTileM));
+        g.tiles_n = static_cast<int32_t>(ceil_div(V, kTileN));
+        g.splits = 1;
+        g.m_fast = 1;  // W is the long operand: read once, X stays in L2
+        g.group = 16;
+        g.operand_type = a.dtype == FSDP_F16 ? 0 : 1;
+        g.targets = a.targets + row0;
+        g.off = reinterpret_cast<float *>(ws + p.off);
+        g.sum = reinterpret_cast<float *>(ws + p.sum);
+        g.target_logit = reinterpret_cast<float *>(ws + p.target_logit);
+        g.ld_rows = p.band;
+        g.tma_store = 1;
+        g.ticket = b == 0 ? reinterpret_cast<uint32_t *>(ws + p.ticket) : nullptr;
+        g.timeouts = a.wait_timeouts;
+        if (p.grad) {
+            st = p.f32 ? make_map(&e_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ws + p.e, V, rows, 1, p.ldv,
+                                  rows * p.ldv, 32)
+                       : make_map(&e_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ws + p.e, V, rows, 1, p.ldv,
+                                  rows * p.ldv, 32);
+            if (st != FSDP_OK) return st;
+        } else {
+            e_out = x_k;
+        }
+        st = launch_logits(p.grad ? kExp : kStats, p.f32, x_k, w_k, e_out, g, s);
+        if (st != FSDP_OK) return st;
+        // the rows' sums and losses
+        RowArgs r;
+        r.off = g.off;
+        r.sum = g.sum;
+        r.ld_rows = p.band;
+        r.spans = static_cast<int32_t>(p.spans);
+        r.target_logit = g.target_logit;
+        r.targets = g.targets;
+        r.rows = rows;
+        r.vocab = V;
+        r.ignore = a.ignore_index;
+        r.lse2 = reinterpret_cast<float *>(ws + p.lse2);
+        r.token_loss = a.token_loss ? a.token_loss + row0 : nullptr;
+        r.part_sum = reinterpret_cast<double *>(ws + p.part_sum);
+        r.part_count = reinterpret_cast<int64_t *>(ws + p.part_count);
+        r.first_block = block;
+        r.all_blocks = p.blocks;
+        r.ticket = reinterpret_cast<uint32_t *>(ws + p.ticket);
+        r.loss = a.loss;
+        r.scale = scale;
+        r.grad_scale = a.grad_scale;
+        r.mean = a.reduction == FSDP_LOSS_MEAN;
+        const unsigned nblocks = static_cast<unsigned>(ceil_div(rows, 32));
+        rows_kernel<<<nblocks, 1024, 0, s>>>(r);
+        block += nblocks;
+        if ((st = check_launch()) != FSDP_OK) return st;
+        if (!p.grad) continue;
+        // d, then the two products
+        GradArgs d;
+        memset(&d, 0, sizeof(d));
+        d.e = ws + p.e;
+        const int64_t plane = rows * p.ldv;
+        if (p.f32)
+            for (int z = 0; z < 3; ++z) d.planes[z] = reinterpret_cast<uint16_t *>(ws + p.d) + z * plane;
+        d.ld = p.ldv;
+        d.rows = rows;
+        d.vocab = V;
+        d.off = g.off;
+        d.ld_rows = p.band;
+        d.lse2 = r.lse2;
+        d.targets = g.targets;
+        d.ignore = a.ignore_index;
+        d.col_blocks = static_cast<uint32_t>(ceil_div(V, kGradCols));
+        const int64_t all = ceil_div(rows, kGradRows) * d.col_blocks;
+        if (all > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
+        const unsigned dgrid = static_cast<unsigned>(all);
+        switch (a.dtype) {
+            case FSDP_BF16: grad_kernel<FSDP_BF16><<<dgrid, 256, 0, s>>>(d); break;
+            case FSDP_F16: grad_kernel<FSDP_F16><<<dgrid, 256, 0, s>>>(d); break;
+            default: grad_kernel<FSDP_F32><<<dgrid, 256, 0, s>>>(d);
+        }
+        if ((st = check_launch()) != FSDP_OK) return st;
+        if (a.d_hidden) {
+            CUtensorMap d_k;
+            st = make_map(&d_k, t16, 2, ws + p.d, V, rows, planes, p.ldv, plane, 128);
+            if (st != FSDP_OK) return st;
+            const Product q{kHiddenGrad, rows, D, V, p.splits_x, nullptr, 0,
+                            static_cast<uint8_t *>(a.d_hidden) + row0 * a.ld_d_hidden * size, a.ld_d_hidden,
+                            static_cast<int>(a.dtype), true};
+            if ((st = run_product(q, p, a, ws, d_k, w_n, s)) != FSDP_OK) return st;
+        }
+        if (a.d_weight) {
+            CUtensorMap d_m;
+            st = make_map(&d_m, t16, 2, ws + p.d, V, rows, planes, p.ldv, plane, 64);
+            if (st == FSDP_OK) st = make_map(&x_n, t16, 2, xb, D, rows, x.planes, x.ld, x.plane, 64);
+            if (st != FSDP_OK) return st;
+            float *sum_w = reinterpret_cast<float *>(ws + p.sum_w);
+            const bool last = b + 1 == p.bands;
+            const Product q{kWeightGrad, V, D, rows, p.splits_w, b > 0 ? sum_w : nullptr, p.ldd,
+                            last ? a.d_weight : sum_w, last ? a.ld_d_weight : p.ldd,
+                            last ? static_cast<int>(a.dtype) : static_cast<int>(FSDP_F32), last};
+            if ((st = run_product(q, p, a, ws, d_m, x_n, s)) != FSDP_OK) return st;
+        }
+    }
+    return FSDP_OK;
+}
+
+// ---------------------------------------------------------------- host: checks
+
+size_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int size) {
+    return rows > 0 ? static_cast<size_t>(((rows - 1) * ld + cols) * size) : 0;
+}
+
+fsdp_status check(const fsdp_head_loss_args *a) {
+    if (!a) return FSDP_ERR_INVALID_ARG;
+    if (!dtype_valid(a->dtype)) return FSDP_ERR_UNSUPPORTED_DTYPE;
+    constexpr int64_t kMost = int64_t(1) << 30;  // tile coordinates are 32-bit
+    if (a->tokens < 0 || a->tokens > kMost || a->vocab < 1 || a->vocab > kMost || a->dim < 1 || a->dim > kMost)
+        return FSDP_ERR_INVALID_ARG;
+    if (a->reserved != 0 || a->band < 0 || (a->reduction != FSDP_LOSS_MEAN && a->reduction != FSDP_LOSS_SUM) || !isfinite(a->grad_scale))
+        return FSDP_ERR_INVALID_ARG;
+    // products of sizes stay far inside 64 bits
+    constexpr int64_t kMostLd = int64_t(1) << 34, kMostArea = int64_t(1) << 50;
+    if (a->tokens > kMostArea / a->vocab) return FSDP_ERR_INVALID_ARG;
+    const int size = dtype_size(a->dtype);
+    struct Matrix {
+        const void *p;
+        int64_t rows, ld;
+        bool needed;
+    } m[4] = {{a->hidden, a->tokens, a->ld_hidden, a->tokens > 0},
+              {a->weight, a->vocab, a->ld_weight, true},
+              {a->d_hidden, a->tokens, a->ld_d_hidden, false},
+              {a->d_weight, a->vocab, a->ld_d_weight, false}};
+    for (const Matrix &x : m) {
+        if (!x.p) {
+            if (x.needed) return FSDP_ERR_INVALID_ARG;
+            continue;
+        }
+        if (x.ld < a->dim || x.ld > kMostLd || x.rows > kMostArea / x.ld) return FSDP_ERR_INVALID_ARG;
+        if (!aligned(x.p, size)) return FSDP_ERR_ALIGNMENT;
+    }
+    if (!a->loss || (a->tokens > 0 && !a->targets)) return FSDP_ERR_INVALID_ARG;
+    if (!aligned(a->loss, 4) || !aligned(a->token_loss, 4) || !aligned(a->targets, 8) || !aligned(a->wait_timeouts, 4))
+        return FSDP_ERR_ALIGNMENT;
+    // no output overlaps an input or another output
+    const void *in[3] = {a->hidden, a->weight, a->targets};
+    const size_t nin[3] = {span_bytes(a->tokens, a->dim, a->ld_hidden, size),
+                           span_bytes(a->vocab, a->dim, a->ld_weight, size), static_cast<size_t>(a->tokens) * 8};
+    const void *out[4] = {a->loss, a->token_loss, a->d_hidden, a->d_weight};
+    const size_t nout[4] = {4, a->token_loss ? static_cast<size_t>(a->tokens) * 4 : 0,
+                            a->d_hidden ? span_bytes(a->tokens, a->dim, a->ld_d_hidden, size) : 0,
+                            a->d_weight ? span_bytes(a->vocab, a->dim, a->ld_d_weight, size) : 0};
+    for (int i = 0; i < 4; ++i) {
+        for (int k = 0; k < 3; ++k)
+            if (overlaps(out[i], nout[i], in[k], nin[k])) return FSDP_ERR_INVALID_ARG;
+        for (int k = i + 1; k < 4; ++k)
+            if (overlaps(out[i], nout[i], out[k], nout[k])) return FSDP_ERR_INVALID_ARG;
+    }
+    return FSDP_OK;
+}
+
+}  // namespace
+}  // namespace loss
+}  // namespace fsdp
+
+using namespace fsdp;
+
+extern "C" {
+
+FSDP_API fsdp_status fsdp_head_loss_workspace(const fsdp_head_loss_args *args, int64_t *bytes_out) {
+    const fsdp_status st = loss::check(args);
+    if (st != FSDP_OK) return st;
+    if (!bytes_out) return FSDP_ERR_INVALID_ARG;
+    *bytes_out = args->tokens == 0 ? 0 : loss::make_plan(*args).bytes;
+    return FSDP_OK;
+}
+
+FSDP_API fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *workspace, int64_t workspace_bytes,
+                                    void *stream) {
+    const fsdp_status st = loss::check(args);
+    if (st != FSDP_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const fsdp_head_loss_args &a = *args;
+    if (a.tokens == 0) {
+        // no rows: a loss of 0 and a zero weight gradient
+        cudaError_t e = cudaMemsetAsync(a.loss, 0, 4, s);
+        if (e == cudaSuccess && a.d_weight) {
+            const size_t size = static_cast<size_t>(dtype_size(a.dtype));
+            e = cudaMemset2DAsync(a.d_weight, a.ld_d_weight * size, 0, a.dim * size, a.vocab, s);
+        }
+        return cuda_status(e);
+    }
+    const loss::Plan p = loss::make_plan(a);
+    if (!workspace || workspace_bytes < p.bytes) return FSDP_ERR_INVALID_ARG;
+    if (!aligned(workspace, 1024)) return FSDP_ERR_ALIGNMENT;
+    const void *used[7] = {a.hidden, a.weight, a.targets, a.loss, a.token_loss, a.d_hidden, a.d_weight};
+    const size_t size = static_cast<size_t>(dtype_size(a.dtype));
+    const size_t bytes[7] = {((a.tokens - 1) * a.ld_hidden + a.dim) * size,
+                             ((a.vocab - 1) * a.ld_weight + a.dim) * size,
+                             static_cast<size_t>(a.tokens) * 8,
+                             4,
+                             a.token_loss ? static_cast<size_t>(a.tokens) * 4 : 0,
+                             a.d_hidden ? ((a.tokens - 1) * a.ld_d_hidden + a.dim) * size : 0,
+                             a.d_weight ? ((a.vocab - 1) * a.ld_d_weight + a.dim) * size : 0};
+    for (int i = 0; i < 7; ++i)
+        if (overlaps(used[i], bytes[i], workspace, static_cast<size_t>(p.bytes))) return FSDP_ERR_INVALID_ARG;
+    return loss::run(a, p, static_cast<uint8_t *>(workspace), s);
+}
+
+}  // extern "C"

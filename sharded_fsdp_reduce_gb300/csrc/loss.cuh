@@ -1,0 +1,66 @@
+// loss.cuh -- internal arguments of the head loss: the three matrix products
+// (logits, hidden gradient, weight gradient) and the row kernels between them.
+#pragma once
+
+#include <cuda.h>  // CUtensorMap
+
+#include "host.cuh"
+
+namespace fsdp {
+namespace loss {
+
+// Tile of one CTA pair: 256 rows (128 per CTA) by 256 columns, 64 K at a time.
+constexpr int kTileM = 256;
+constexpr int kTileN = 256;
+constexpr int kBlockK = 64;
+// Columns whose exponentials share one reference (one epilogue warp's).
+constexpr int kSpan = 128;
+
+// What a product's epilogue does with the accumulator.
+enum Epilogue {
+    kStats = 0,   // per row and span: exponent reference and sum (nothing stored)
+    kExp = 1,     // kStats, and the exponentials stored (fp16, or fp32 for an fp32 head)
+    kScale = 2,   // store scale * (accumulator + earlier bands)
+};
+
+// Operand orders of the three products: whether A and B are MN-major.
+enum Orders { kLogits, kHiddenGrad, kWeightGrad };
+
+struct GemmArgs {
+    int64_t M, N;          // valid rows and columns
+    int32_t kblocks;       // K blocks per operand pair
+    int32_t pairs;         // 1, or 6 plane pairs of an fp32 head
+    int32_t tiles_m, tiles_n, splits;
+    int32_t group;         // tiles of the fast dimension visited together
+    int32_t m_fast;        // 1: rows are the fast dimension
+    int32_t operand_type;  // 0 fp16, 1 bf16
+    // kStats, kExp
+    const int64_t *targets;
+    float *off, *sum;      // [spans][ld_rows]
+    float *target_logit;   // [rows]
+    int64_t ld_rows;
+    // kScale
+    const float *scale;    // device scalar, or NULL for 1
+    float scale_const;     // and this constant factor
+    const float *earlier;  // fp32 [M][ld_earlier] added to the accumulator, or NULL
+    int64_t ld_earlier;
+    int32_t tma_store;     // 1: through the output map, 0: element stores to out
+    void *out;
+    int64_t ld_out;
+    uint32_t *ticket;      // kStats, kExp: cleared for the row kernel that follows (or NULL)
+    uint32_t *timeouts;
+};
+
+
+// One translation unit per output dtype of the gradients, and one for the logits.
+fsdp_status launch_logits(Epilogue ep, bool f32, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
+                          const GemmArgs &g, cudaStream_t s);
+fsdp_status launch_grad_bf16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
+                             const GemmArgs &g, cudaStream_t s);
+fsdp_status launch_grad_f16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
+                            const GemmArgs &g, cudaStream_t s);
+fsdp_status launch_grad_f32(Orders o, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
+                            const GemmArgs &g, cudaStream_t s);
+
+}  // namespace loss
+}  // namespace fsdp

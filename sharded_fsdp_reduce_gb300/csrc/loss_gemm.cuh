@@ -1,0 +1,468 @@
+// loss_gemm.cuh -- the matrix product of the head loss on CTA pairs.
+//
+// One kernel text for three products, by the operands' orders:
+//   logits  L = X W^T        A = X  [T,D] K-major,  B = W [V,D] K-major
+//   dX      = d W            A = d  [T,V] K-major,  B = W [V,D] N-major (K = V)
+//   dW      = d^T X          A = d  [T,V] M-major,  B = X [T,D] N-major (K = T)
+// so none of the operands is ever transposed in memory.
+//
+// A pair of CTAs (one cluster) works on a 256 x 256 tile of the result: each
+// loads 128 rows of A and 128 of B per 64-wide K block by TMA (32 KB a stage,
+// six stages), the even CTA issues the tcgen05 products for both (M = N = 256,
+// K = 16), and each CTA's tensor memory holds 128 rows of the accumulator in
+// fp32, twice (2 x 256 columns): the epilogue of one tile runs while the next
+// one's products are issued. The pair shape halves the operand bytes that
+// shared memory and L2 must deliver per product against single CTAs of
+// 128 x 256. Persistent: one CTA per SM, tiles taken in a fixed order that
+// keeps the reused operand in L2.
+//
+// Roles by warp: 0 loads, 1 issues the products, 2 owns tensor memory, 4-11
+// are the epilogue: warp w reads lanes 32 (w % 4) .. + 31 (one row per
+// thread), columns 128 ((w - 4) / 4) .. + 127.
+//
+// An fp32 operand is held as three bf16 planes (its leading, middle and last
+// 8 bits); the K loop then runs over the six plane pairs whose products reach
+// 2^-16 of the leading one, smallest first, into the same accumulator. What it
+// leaves out is below 2^-23 of the product of the operands' magnitudes.
+//
+// Every wait gives up after about a second, records itself and makes the pair
+// leave; the result is then incomplete and the counter says so.
+#pragma once
+
+#include <float.h>
+
+#include <type_traits>
+
+#include "loss.cuh"
+#include "tcgen.cuh"
+
+namespace fsdp {
+namespace loss {
+
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr int kStages = 6;
+constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // one operand's half tile: 16 KB
+constexpr uint32_t kStageBytes = 2 * kHalfBytes;         // per CTA
+constexpr uint32_t kStoreBytes = 32 * 128;               // one warp's store box: 32 rows of 128 bytes
+constexpr uint32_t kTensorCols = 512;                    // two accumulators of 256 columns
+constexpr long long kWaitCycles = 2000000000ll;          // about one second of SM clocks
+
+struct Barriers {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tensor_base;
+    int32_t gave_up;
+};
+
+constexpr size_t kSmemBytes =
+    1024 + kStages * kStageBytes + kEpilogueWarps * kStoreBytes + sizeof(Barriers);
+
+// The (A, B) planes of the six pairs, low nibble first, smallest products first.
+constexpr uint32_t kPlanesA = 0x001021, kPlanesB = 0x010201;
+
+struct Tile {
+    int m, n, split;
+};
+
+__device__ __forceinline__ Tile tile_at(const GemmArgs &g, int t) {
+    const int per = g.tiles_m * g.tiles_n;
+    Tile r;
+    r.split = t / per;
+    t -= r.split * per;
+    const int fast = g.m_fast ? g.tiles_m : g.tiles_n, slow = g.m_fast ? g.tiles_n : g.tiles_m;
+    const int first = t / (g.group * slow) * g.group;
+    t -= first * slow;
+    const int width = min(g.group, fast - first);
+    const int f = first + t % width, s = t / width;
+    r.m = g.m_fast ? f : s;
+    r.n = g.m_fast ? s : f;
+    return r;
+}
+
+__device__ __forceinline__ void k_range(const GemmArgs &g, int split, int &begin, int &end) {
+    const int64_t total = int64_t(g.kblocks) * g.pairs;
+    begin = static_cast<int>(total * split / g.splits);
+    end = static_cast<int>(total * (split + 1) / g.splits);
+}
+
+// Bounded wait; false once any wait of this CTA has given up.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Barriers *b, uint32_t *timeouts) {
+    if (tc::try_wait_cluster(bar, parity)) return true;
+    const long long t0 = clock64();
+    volatile int32_t *gave_up = &b->gave_up;
+    while (!tc::try_wait_cluster(bar, parity)) {
+        if (*gave_up) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *gave_up = 1;
+            if (timeouts) atomicAdd(timeouts, 1u);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One warp's 32 x (128 bytes) store box in swizzled shared memory.
+struct StoreBox {
+    uint8_t *smem;
+    int lane;
+
+    // before writing: the last store has read the box
+    __device__ __forceinline__ void open(bool tma_store) const {
+        if (tma_store && lane == 0) tma::bulk_wait_read<0>();
+        __syncwarp();
+    }
+    // 16 bytes at chunk c (0..7) of this lane's row
+    __device__ __forceinline__ void put(int c, uint4 v) const {
+        *reinterpret_cast<uint4 *>(smem + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+    }
+    template <class T> __device__ __forceinline__ T get(int row, int e) const {
+        const int byte = e * static_cast<int>(sizeof(T));
+        return *reinterpret_cast<const T *>(smem + row * 128 + ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 15)));
+    }
+};
+
+// 32 values of a row as packed words: 16-bit types fill half a box row.
+template <int DT> __device__ __forceinline__ void put32(const StoreBox &box, int chunk, const float *v) {
+    if constexpr (DT == FSDP_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            box.put(i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                  __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            box.put(4 * (chunk & 1) + i, make_uint4(pack2<DT>(v[8 * i], v[8 * i + 1]), pack2<DT>(v[8 * i + 2], v[8 * i + 3]),
+                                                    pack2<DT>(v[8 * i + 4], v[8 * i + 5]),
+                                                    pack2<DT>(v[8 * i + 6], v[8 * i + 7])));
+    }
+}
+
+// Store the filled box: its first row and column, and the plane or split.
+template <int DT>
+__device__ __forceinline__ void flush(const StoreBox &box, const CUtensorMap *map, const GemmArgs &g, int64_t row0,
+                                      int64_t col0, int z) {
+    constexpr int kCols = 128 / Dtype<DT>::kSize;
+    if (g.tma_store) {
+        tma::fence_proxy_async_smem();
+        __syncwarp();
+        if (box.lane == 0) {
+            tc::store_tile(map, static_cast<int>(col0), static_cast<int>(row0), z, box.smem);
+            tma::bulk_commit();
+        }
+    } else {
+        // outputs whose rows TMA cannot address (base or stride off 16 bytes)
+        __syncwarp();
+        using T = typename std::conditional<DT == FSDP_F32, uint32_t, uint16_t>::type;
+        const int rows = static_cast<int>(min(int64_t(32), g.M - row0));
+        for (int r = 0; r < rows; ++r) {
+            T *out = static_cast<T *>(g.out) + (row0 + r) * g.ld_out + col0;
+#pragma unroll
+            for (int e = box.lane; e < kCols; e += 32)
+                if (col0 + e < g.N) out[e] = box.get<T>(r, e);
+        }
+    }
+}
+
+// Softmax statistics (and exponentials) of one warp's 32 rows x 128 columns.
+// With l2 = logit * log2(e), a span's exponentials are e = 2^(l2 - off), off =
+// max(l2) - 15: at most 2^15, so that fp16 holds them with 11 bits down to
+// 2^-29 of the span's largest (what is smaller is below 2^-40 of it).
+template <int EP, int DT>
+__device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMap *map, const StoreBox &box,
+                                             uint32_t acc, int64_t row0, int64_t col0) {
+    constexpr float kLog2e = 1.44269504088896340736f;
+    const int64_t row = row0 + box.lane;
+    const bool live = row < g.M;
+    const int64_t y = live ? g.targets[row] : -1;
+    const int cols = static_cast<int>(min(int64_t(kSpan), g.N - col0));
+    float top = -FLT_MAX;
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+        float v[32];
+        __syncwarp();
+        tc::load_cols32(acc + c, v);
+        if (c + 32 <= cols) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j < cols) top = fmaxf(top, v[j]);
+        }
+        const int64_t at = y - (col0 + c);
+        if (at >= 0 && at < 32) {
+            float t = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (at == j) t = v[j];
+            g.target_logit[row] = t;
+        }
+    }
+    const float off = fmaxf(top * kLog2e, -FLT_MAX) - 15.0f;
+    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+        float v[32];
+        __syncwarp();
+        tc::load_cols32(acc + c, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], kLog2e, -off));
+        if (c + 32 > cols) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j >= cols) v[j] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            s0 += v[j];
+            s1 += v[j + 1];
+            s2 += v[j + 2];
+            s3 += v[j + 3];
+        }
+        if constexpr (EP == kExp) {
+            constexpr int kCols = 128 / Dtype<DT>::kSize;
+            if (c % kCols == 0) box.open(true);
+            put32<DT>(box, c / 32, v);
+            if ((c + 32) % kCols == 0 || c + 32 >= cols)
+                flush<DT>(box, map, g, row0, col0 + c / kCols * kCols, 0);
+        }
+    }
+    if (live) {
+        const int64_t at = col0 / kSpan * g.ld_rows + row;
+        g.off[at] = off;
+        g.sum[at] = (s0 + s1) + (s2 + s3);
+    }
+}
+
+// scale * (accumulator + earlier) of one warp's 32 rows x 128 columns.
+template <int DT>
+__device__ __forceinline__ void scaled_span(const GemmArgs &g, const CUtensorMap *map, const StoreBox &box,
+                                            uint32_t acc, int64_t row0, int64_t col0, int split, float scale) {
+    constexpr int kCols = 128 / Dtype<DT>::kSize;
+    const int64_t row = row0 + box.lane;
+    const int cols = static_cast<int>(min(int64_t(kSpan), g.N - col0));
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+        float v[32];
+        __syncwarp();
+        tc::load_cols32(acc + c, v);
+        if (g.earlier != nullptr && row < g.M) {
+            const float *e = g.earlier + row * g.ld_earlier + col0 + c;  // 16-byte aligned, padded to 32 columns
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(e + j);
+                v[j] += x.x;
+                v[j + 1] += x.y;
+                v[j + 2] += x.z;
+                v[j + 3] += x.w;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= scale;
+        if (c % kCols == 0) box.open(g.tma_store != 0);
+        put32<DT>(box, c / 32, v);
+        if ((c + 32) % kCols == 0 || c + 32 >= cols)
+            flush<DT>(box, map, g, row0, col0 + c / kCols * kCols, split);
+    }
+}
+
+template <int AMN, int BMN, int EP, int DT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                const __grid_constant__ CUtensorMap map_out, const __grid_constant__ GemmArgs g) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *boxes = smem + kStages * kStageBytes;
+    Barriers *b = reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * kStoreBytes);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = tc::cluster_rank();
+    const int total = g.tiles_m * g.tiles_n * g.splits;
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tma::mbar_init(&b->full[s], 1);
+            tma::mbar_init(&b->empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tma::mbar_init(&b->acc_full[s], 1);
+            tma::mbar_init(&b->acc_empty[s], 2 * kEpilogueWarps);
+        }
+        b->gave_up = 0;
+        tma::fence_mbar_init();
+        tc::prefetch_map(&map_a);
+        tc::prefetch_map(&map_b);
+    }
+    __syncwarp();
+    if (warp == 2) tc::alloc_pair(&b->tensor_base, kTensorCols);
+    if constexpr (EP != kScale) {
+        if (blockIdx.x == 0 && threadIdx.x == 96 && g.ticket != nullptr) *g.ticket = 0;
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();  // both CTAs' barriers exist before either signals the other's
+    tc::fence_after();
+    const uint32_t tensor = b->tensor_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += step) {
+                const Tile x = tile_at(g, t);
+                int k0, k1;
+                k_range(g, x.split, k0, k1);
+                const int row = x.m * kTileM + static_cast<int>(rank) * 128;
+                const int col = x.n * kTileN + static_cast<int>(rank) * 128;
+                for (int k = k0; k < k1; ++k) {
+                    if (!wait(&b->empty[stage], phase ^ 1, b, g.timeouts)) {
+                        ok = false;
+                        break;
+                    }
+                    const int pair = k / g.kblocks, kk = (k - pair * g.kblocks) * kBlockK;
+                    int za = 0, zb = 0;
+                    if (g.pairs > 1) {
+                        za = (kPlanesA >> (4 * pair)) & 15;
+                        zb = (kPlanesB >> (4 * pair)) & 15;
+                    }
+                    if (rank == 0) tma::mbar_arrive_expect_tx(&b->full[stage], 2 * kStageBytes);
+                    const uint32_t bar = tc::peer_addr(tc::smem_addr(&b->full[stage]), 0);
+                    uint8_t *sa = smem + stage * kStageBytes, *sb = sa + kHalfBytes;
+                    if constexpr (AMN) {
+                        tc::load_tile(sa, &map_a, row, kk, za, bar);
+                        tc::load_tile(sa + kHalfBytes / 2, &map_a, row + 64, kk, za, bar);
+                    } else {
+                        tc::load_tile(sa, &map_a, kk, row, za, bar);
+                    }
+                    if constexpr (BMN) {
+                        tc::load_tile(sb, &map_b, col, kk, zb, bar);
+                        tc::load_tile(sb + kHalfBytes / 2, &map_b, col + 64, kk, zb, bar);
+                    } else {
+                        tc::load_tile(sb, &map_b, kk, col, zb, bar);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // the last use of every stage has been consumed: no copy of this
+            // CTA is in flight and no product still signals its barriers
+            for (int s = 0; s < kStages && ok; ++s) {
+                ok = wait(&b->empty[stage], phase ^ 1, b, g.timeouts);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = tc::instruction(0, AMN, BMN, kTileM, kTileN) |
+                                   (static_cast<uint32_t>(g.operand_type) << 7) |
+                                   (static_cast<uint32_t>(g.operand_type) << 10);
+            // per K = 16: 32 bytes along a K-major row, two groups of eight K otherwise
+            constexpr uint32_t kStepA = (AMN ? 2048 : 32) >> 4, kStepB = (BMN ? 2048 : 32) >> 4;
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += step) {
+                const Tile x = tile_at(g, t);
+                int k0, k1;
+                k_range(g, x.split, k0, k1);
+                ok = wait(&b->acc_empty[buf], acc_phase ^ 1, b, g.timeouts);
+                tc::fence_after();
+                for (int k = k0; k < k1 && ok; ++k) {
+                    ok = wait(&b->full[stage], phase, b, g.timeouts);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t sa = tc::smem_addr(smem + stage * kStageBytes);
+                    const uint64_t da = tc::operand(sa, AMN ? kHalfBytes / 2 : 16, 1024);
+                    const uint64_t db = tc::operand(sa + kHalfBytes, BMN ? kHalfBytes / 2 : 16, 1024);
+#pragma unroll
+                    for (int j = 0; j < kBlockK / 16; ++j)
+                        tc::mma_pair(tensor + buf * kTileN, da + j * kStepA, db + j * kStepB, idesc, k > k0 || j > 0);
+                    tc::commit_pair(&b->empty[stage]);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                tc::commit_pair(&b->acc_full[buf]);
+                buf ^= 1;
+                acc_phase ^= buf == 0;
+            }
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp % 4, half = (warp - 4) / 4;
+        const StoreBox box{boxes + (warp - 4) * kStoreBytes, lane};
+        float scale = 1.0f;
+        if constexpr (EP == kScale) scale = g.scale_const * (g.scale != nullptr ? *g.scale : 1.0f);
+        int buf = 0;
+        uint32_t acc_phase = 0;
+        for (int t = first; t < total; t += step) {
+            const Tile x = tile_at(g, t);
+            if (!wait(&b->acc_full[buf], acc_phase, b, g.timeouts)) break;
+            tc::fence_after();
+            const int64_t row0 = int64_t(x.m) * kTileM + rank * 128 + quarter * 32;
+            const int64_t col0 = int64_t(x.n) * kTileN + half * kSpan;
+            const uint32_t acc = tensor + buf * kTileN + half * kSpan + (static_cast<uint32_t>(quarter * 32) << 16);
+            if (row0 < g.M && col0 < g.N) {
+                if constexpr (EP == kScale)
+                    scaled_span<DT>(g, &map_out, box, acc, row0, col0, x.split, scale);
+                else
+                    softmax_span<EP, DT>(g, &map_out, box, acc, row0, col0);
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::arrive_cluster(tc::peer_addr(tc::smem_addr(&b->acc_empty[buf]), 0));
+            buf ^= 1;
+            acc_phase ^= buf == 0;
+        }
+        if (lane == 0) tma::bulk_wait<0>();
+    }
+    // a wait gave up: let copies and products that are only slow land before
+    // the shared and tensor memory go
+    __syncwarp();
+    if (*static_cast<volatile int32_t *>(&b->gave_up)) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < kWaitCycles) __nanosleep(1000);
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    __syncwarp();
+    if (warp == 2) tc::free_pair(tensor, kTensorCols);
+}
+
+template <int AMN, int BMN, int EP, int DT>
+fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const GemmArgs &g,
+                          cudaStream_t s) {
+    static PerDeviceOnce once;
+    const int dev = current_device();
+    if (!once.is_done(dev)) {
+        const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<AMN, BMN, EP, DT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(kSmemBytes));
+        if (e != cudaSuccess) return cuda_status(e);
+        once.mark(dev);
+    }
+    const int64_t total = int64_t(g.tiles_m) * g.tiles_n * g.splits;
+    if (total < 1 || total > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
+    const int64_t pairs = sm_count() / 2;
+    const unsigned grid = static_cast<unsigned>(2 * (total < pairs ? total : (pairs > 0 ? pairs : 1)));
+    gemm_kernel<AMN, BMN, EP, DT><<<grid, kThreads, kSmemBytes, s>>>(a, b, out, g);
+    return check_launch();
+}
+
+}  // namespace loss
+}  // namespace fsdp

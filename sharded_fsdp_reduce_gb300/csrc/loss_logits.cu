@@ -1,0 +1,15 @@
+// The head loss's logits product (see loss_gemm.cuh).
+#include "loss_gemm.cuh"
+
+namespace fsdp {
+namespace loss {
+
+fsdp_status launch_logits(Epilogue ep, bool f32, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
+                          const GemmArgs &g, cudaStream_t s) {
+    if (ep == kStats) return launch_kernel<0, 0, kStats, FSDP_F16>(a, b, out, g, s);
+    return f32 ? launch_kernel<0, 0, kExp, FSDP_F32>(a, b, out, g, s)
+               : launch_kernel<0, 0, kExp, FSDP_F16>(a, b, out, g, s);
+}
+
+}  // namespace loss
+}  // namespace fsdp

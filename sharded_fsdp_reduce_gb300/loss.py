@@ -1,0 +1,186 @@
+"""The loss of a linear head over a large vocabulary, and its gradients.
+
+Softmax cross entropy of logits = hidden @ weight.T against target tokens,
+with the logits formed tile by tile and never stored in fp32 (the kernels:
+csrc/loss.cu, csrc/loss_gemm.cuh). In a training step of sharded units the
+weight is a view of a unit's gathered buffer and d_weight a view of a rank's
+flat gradient buffer, so the gradient lands where the reduce-scatter reads it
+("Data Parallelism", "The Basic Protocol").
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from .fsdp import _check, _counter, _on_current_device, _stream, dtype_code
+
+__all__ = ["HeadLoss", "fsdp_head_loss"]
+
+_REDUCTIONS = {"mean": _lib.FSDP_LOSS_MEAN, "sum": _lib.FSDP_LOSS_SUM}
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype) -> Tuple[int, int]:
+    """Address and row stride of a [rows, cols] CUDA matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}] of {dtype}")
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and rows > 0 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    _on_current_device(t, name)
+    return t.data_ptr(), ld
+
+
+def _vector(t: torch.Tensor, name: str, numel: int, dtype: torch.dtype) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype != dtype or t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} elements of {dtype}")
+    _on_current_device(t, name)
+    return t.data_ptr()
+
+
+def _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, ignore_index, reduction, grad_scale, band,
+          wait_timeouts) -> _lib.FsdpHeadLossArgs:
+    if not isinstance(hidden, torch.Tensor) or hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError("hidden and weight must be matrices")
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
+    T, D = hidden.shape
+    V = weight.shape[0]
+    dt = hidden.dtype
+    a = _lib.FsdpHeadLossArgs()
+    a.dtype = dtype_code(dt)
+    a.tokens, a.vocab, a.dim = T, V, D
+    a.hidden, a.ld_hidden = _matrix(hidden, "hidden", T, D, dt)
+    a.weight, a.ld_weight = _matrix(weight, "weight", V, D, dt)
+    a.targets = _vector(targets, "targets", T, torch.int64)
+    a.loss = _vector(loss, "loss", 1, torch.float32)
+    if token_loss is not None:
+        a.token_loss = _vector(token_loss, "token_loss", T, torch.float32)
+    if d_hidden is not None:
+        a.d_hidden, a.ld_d_hidden = _matrix(d_hidden, "d_hidden", T, D, dt)
+    if d_weight is not None:
+        a.d_weight, a.ld_d_weight = _matrix(d_weight, "d_weight", V, D, dt)
+    a.ignore_index = int(ignore_index)
+    a.reduction = _REDUCTIONS[reduction]
+    a.grad_scale = float(grad_scale)
+    a.band = int(band)
+    a.wait_timeouts = _counter(wait_timeouts, "wait_timeouts")
+    return a
+
+
+def _workspace_bytes(a: _lib.FsdpHeadLossArgs) -> int:
+    n = ctypes.c_int64(0)
+    _check(_lib.load().fsdp_head_loss_workspace(ctypes.byref(a), ctypes.byref(n)), "fsdp_head_loss_workspace")
+    return int(n.value)
+
+
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    # torch aligns allocations to 512 bytes: one kilobyte more, cut to the alignment
+    buf = torch.empty(nbytes + 1024, dtype=torch.uint8, device=device)
+    return buf.narrow(0, -buf.data_ptr() % 1024, nbytes)
+
+
+def _launch(a: _lib.FsdpHeadLossArgs, workspace: torch.Tensor, stream) -> None:
+    _check(_lib.load().fsdp_head_loss(ctypes.byref(a), workspace.data_ptr(), workspace.numel(), _stream(stream)),
+           "fsdp_head_loss")
+
+
+def fsdp_head_loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, loss: torch.Tensor,
+                   token_loss: Optional[torch.Tensor] = None, d_hidden: Optional[torch.Tensor] = None,
+                   d_weight: Optional[torch.Tensor] = None, ignore_index: int = -100, reduction: str = "mean",
+                   grad_scale: float = 1.0, band: int = 0, wait_timeouts: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> None:
+    """The C entry point with a workspace of its own for this one call.
+
+    hidden [T, D], weight [V, D] (rows contiguous, any stride and alignment),
+    targets int64 [T]; loss fp32 scalar, token_loss fp32 [T], d_hidden [T, D]
+    and d_weight [V, D] of hidden's dtype are written (d_* None: not formed)."""
+    a = _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, ignore_index, reduction, grad_scale,
+              band, wait_timeouts)
+    ws = _workspace(_workspace_bytes(a), hidden.device)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    _launch(a, ws, s)
+    ws.record_stream(s)
+
+
+class HeadLoss:
+    """A head's loss with the workspace its calls share.
+
+    vocab, dim, dtype: the weight's shape and the dtype of hidden, weight and
+    gradients. max_tokens: the most rows of a call. grad: whether gradients
+    will be asked for (the workspace is sized for it). band: rows worked on
+    together (0: as many as keep the 16-bit exponentials within 2 GiB).
+    ignore_index, reduction ("mean" over the rows that count, or "sum") as in
+    fsdp_head_loss. The workspace grows by itself, once, when a call needs
+    more (rows that are not 16-byte aligned are packed into it). Calls on one
+    stream, or ordered between streams, may share it; calls that run at the
+    same time need a HeadLoss each."""
+
+    def __init__(self, vocab: int, dim: int, dtype: torch.dtype, max_tokens: int, grad: bool = True, band: int = 0,
+                 ignore_index: int = -100, reduction: str = "mean", device="cuda"):
+        if reduction not in _REDUCTIONS:
+            raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
+        self.vocab, self.dim, self.dtype = int(vocab), int(dim), dtype
+        self.max_tokens, self.grad, self.band = int(max_tokens), bool(grad), int(band)
+        self.ignore_index, self.reduction = int(ignore_index), reduction
+        self.device = torch.device(device)
+        # sized as a call with aligned operands needs it (addresses are not read)
+        a = _lib.FsdpHeadLossArgs()
+        a.dtype = dtype_code(dtype)
+        a.tokens, a.vocab, a.dim, a.band = self.max_tokens, self.vocab, self.dim, self.band
+        pad = -(-self.dim // 8) * 8
+        step = 1 << 56
+        a.hidden, a.weight, a.targets, a.loss = step, 2 * step, 3 * step, 4 * step
+        a.ld_hidden = a.ld_weight = a.ld_d_hidden = a.ld_d_weight = pad
+        if grad:
+            a.d_hidden, a.d_weight = 5 * step, 6 * step
+        a.grad_scale = 1.0
+        self._ws = _workspace(_workspace_bytes(a), self.device)
+        self._ws_stream = torch.cuda.current_stream(self.device).cuda_stream
+
+    def forward(self, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                loss: Optional[torch.Tensor] = None, token_loss: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None,
+                wait_timeouts: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """The loss (fp32 scalar) and the tokens' losses (fp32 [T], 0 where
+        ignored). loss / token_loss: where to write them (new ones otherwise)."""
+        return self._run(hidden, weight, targets, None, None, 1.0, loss, token_loss, stream, wait_timeouts)
+
+    def forward_backward(self, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                         d_hidden: Optional[torch.Tensor], d_weight: Optional[torch.Tensor], grad_scale: float = 1.0,
+                         loss: Optional[torch.Tensor] = None, token_loss: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None,
+                         wait_timeouts: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """forward(), and the gradients of grad_scale * loss written to
+        d_hidden [T, D] and d_weight [V, D] (None: not formed)."""
+        return self._run(hidden, weight, targets, d_hidden, d_weight, grad_scale, loss, token_loss, stream,
+                         wait_timeouts)
+
+    def _run(self, hidden, weight, targets, d_hidden, d_weight, grad_scale, loss, token_loss, stream, wait_timeouts):
+        if hidden.dim() != 2 or hidden.shape[0] > self.max_tokens or hidden.shape[1] != self.dim:
+            raise ValueError(f"hidden must be [at most {self.max_tokens}, {self.dim}]")
+        if hidden.dtype != self.dtype or tuple(weight.shape) != (self.vocab, self.dim):
+            raise ValueError(f"hidden must be {self.dtype} and weight [{self.vocab}, {self.dim}]")
+        s = stream if stream is not None else torch.cuda.current_stream()
+        if loss is None or token_loss is None:
+            with torch.cuda.stream(s):  # new results belong to the call's stream
+                if loss is None:
+                    loss = torch.empty((), dtype=torch.float32, device=hidden.device)
+                if token_loss is None:
+                    token_loss = torch.empty(hidden.shape[0], dtype=torch.float32, device=hidden.device)
+        a = _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, self.ignore_index, self.reduction,
+                  grad_scale, self.band, wait_timeouts)
+        need = _workspace_bytes(a)
+        if need > self._ws.numel():
+            self._ws = _workspace(need, self.device)
+            self._ws_stream = torch.cuda.current_stream(self.device).cuda_stream
+        if s.cuda_stream != self._ws_stream:
+            self._ws.record_stream(s)  # freed only after this call's work
+        _launch(a, self._ws, s)
+        return loss, token_loss
