@@ -42,6 +42,11 @@ namespace loss {
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
 constexpr int kStages = 6;
+// K blocks summed in tensor memory before the sum moves to registers. The
+// tensor cores' own sum loses bits at every K = 16 (a chain of 5120 / 16 adds
+// left a loss 2.4e-6 off, 64 bits against it); chains of 512 / 16 joined by
+// rounded fp32 adds do not show.
+constexpr int kChunk = 8;
 constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // one operand's half tile: 16 KB
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;         // per CTA
 constexpr uint32_t kStoreBytes = 32 * 128;               // one warp's store box: 32 rows of 128 bytes
@@ -128,8 +133,8 @@ struct StoreBox {
     }
 };
 
-// 32 values of a row as packed words: 16-bit types fill half a box row.
-template <int DT> __device__ __forceinline__ void put32(const StoreBox &box, int chunk, const float *v) {
+// The columns from c0 of a box: 64 (16-bit types) or 32 (fp32) of a row's values.
+template <int DT> __device__ __forceinline__ void put_row(const StoreBox &box, const float *v) {
     if constexpr (DT == FSDP_F32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -137,35 +142,40 @@ template <int DT> __device__ __forceinline__ void put32(const StoreBox &box, int
                                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            box.put(4 * (chunk & 1) + i, make_uint4(pack2<DT>(v[8 * i], v[8 * i + 1]), pack2<DT>(v[8 * i + 2], v[8 * i + 3]),
-                                                    pack2<DT>(v[8 * i + 4], v[8 * i + 5]),
-                                                    pack2<DT>(v[8 * i + 6], v[8 * i + 7])));
+        for (int i = 0; i < 8; ++i)
+            box.put(i, make_uint4(pack2<DT>(v[8 * i], v[8 * i + 1]), pack2<DT>(v[8 * i + 2], v[8 * i + 3]),
+                                  pack2<DT>(v[8 * i + 4], v[8 * i + 5]), pack2<DT>(v[8 * i + 6], v[8 * i + 7])));
     }
 }
 
-// Store the filled box: its first row and column, and the plane or split.
+// Store one warp's 32 rows x 128 columns, box by box; z: the plane or split.
 template <int DT>
-__device__ __forceinline__ void flush(const StoreBox &box, const CUtensorMap *map, const GemmArgs &g, int64_t row0,
-                                      int64_t col0, int z) {
+__device__ __forceinline__ void store_span(const StoreBox &box, const CUtensorMap *map, const GemmArgs &g,
+                                           bool tma_store, int64_t row0, int64_t col0, int z, const float *v) {
     constexpr int kCols = 128 / Dtype<DT>::kSize;
-    if (g.tma_store) {
-        tma::fence_proxy_async_smem();
-        __syncwarp();
-        if (box.lane == 0) {
-            tc::store_tile(map, static_cast<int>(col0), static_cast<int>(row0), z, box.smem);
-            tma::bulk_commit();
-        }
-    } else {
-        // outputs whose rows TMA cannot address (base or stride off 16 bytes)
-        __syncwarp();
-        using T = typename std::conditional<DT == FSDP_F32, uint32_t, uint16_t>::type;
-        const int rows = static_cast<int>(min(int64_t(32), g.M - row0));
-        for (int r = 0; r < rows; ++r) {
-            T *out = static_cast<T *>(g.out) + (row0 + r) * g.ld_out + col0;
 #pragma unroll
-            for (int e = box.lane; e < kCols; e += 32)
-                if (col0 + e < g.N) out[e] = box.get<T>(r, e);
+    for (int c = 0; c < kSpan; c += kCols) {
+        if (col0 + c >= g.N) break;
+        box.open(tma_store);
+        put_row<DT>(box, v + c);
+        if (tma_store) {
+            tma::fence_proxy_async_smem();
+            __syncwarp();
+            if (box.lane == 0) {
+                tc::store_tile(map, static_cast<int>(col0 + c), static_cast<int>(row0), z, box.smem);
+                tma::bulk_commit();
+            }
+        } else {
+            // outputs whose rows TMA cannot address (base or stride off 16 bytes)
+            __syncwarp();
+            using T = typename std::conditional<DT == FSDP_F32, uint32_t, uint16_t>::type;
+            const int rows = static_cast<int>(min(int64_t(32), g.M - row0));
+            for (int r = 0; r < rows; ++r) {
+                T *out = static_cast<T *>(g.out) + (row0 + r) * g.ld_out + col0 + c;
+#pragma unroll
+                for (int e = box.lane; e < kCols; e += 32)
+                    if (col0 + c + e < g.N) out[e] = box.get<T>(r, e);
+            }
         }
     }
 }
@@ -176,87 +186,59 @@ __device__ __forceinline__ void flush(const StoreBox &box, const CUtensorMap *ma
 // 2^-29 of the span's largest (what is smaller is below 2^-40 of it).
 template <int EP, int DT>
 __device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMap *map, const StoreBox &box,
-                                             uint32_t acc, int64_t row0, int64_t col0) {
+                                             float *v, int64_t row0, int64_t col0) {
     constexpr float kLog2e = 1.44269504088896340736f;
     const int64_t row = row0 + box.lane;
     const bool live = row < g.M;
-    const int64_t y = live ? g.targets[row] : -1;
-    const int cols = static_cast<int>(min(int64_t(kSpan), g.N - col0));
-    float top = -FLT_MAX;
-#pragma unroll 1
-    for (int c = 0; c < cols; c += 32) {
-        float v[32];
-        __syncwarp();
-        tc::load_cols32(acc + c, v);
-        if (c + 32 <= cols) {
+    const int64_t at = (live ? g.targets[row] : -1) - col0;
+    if (at >= 0 && at < kSpan && at + col0 < g.N) {
+        float t = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (c + j < cols) top = fmaxf(top, v[j]);
-        }
-        const int64_t at = y - (col0 + c);
-        if (at >= 0 && at < 32) {
-            float t = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (at == j) t = v[j];
-            g.target_logit[row] = t;
-        }
+        for (int j = 0; j < kSpan; ++j)
+            if (at == j) t = v[j];
+        g.target_logit[row] = t;
     }
-    const float off = fmaxf(top * kLog2e, -FLT_MAX) - 15.0f;
+    if (col0 + kSpan > g.N) {
+        const int cols = static_cast<int>(g.N - col0);
+#pragma unroll
+        for (int j = 0; j < kSpan; ++j)
+            if (j >= cols) v[j] = -INFINITY;
+    }
+    float t0 = -FLT_MAX, t1 = -FLT_MAX;
+#pragma unroll
+    for (int j = 0; j < kSpan; j += 2) {
+        t0 = fmaxf(t0, v[j]);
+        t1 = fmaxf(t1, v[j + 1]);
+    }
+    const float off = fmaxf(fmaxf(t0, t1) * kLog2e, -FLT_MAX) - 15.0f;
     float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-#pragma unroll 1
-    for (int c = 0; c < cols; c += 32) {
-        float v[32];
-        __syncwarp();
-        tc::load_cols32(acc + c, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = exp2_fast(fmaf(v[j], kLog2e, -off));
-        if (c + 32 > cols) {
+    for (int j = 0; j < kSpan; ++j) v[j] = exp2_fast(fmaf(v[j], kLog2e, -off));
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (c + j >= cols) v[j] = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            s0 += v[j];
-            s1 += v[j + 1];
-            s2 += v[j + 2];
-            s3 += v[j + 3];
-        }
-        if constexpr (EP == kExp) {
-            constexpr int kCols = 128 / Dtype<DT>::kSize;
-            if (c % kCols == 0) box.open(true);
-            put32<DT>(box, c / 32, v);
-            if ((c + 32) % kCols == 0 || c + 32 >= cols)
-                flush<DT>(box, map, g, row0, col0 + c / kCols * kCols, 0);
-        }
+    for (int j = 0; j < kSpan; j += 4) {
+        s0 += v[j];
+        s1 += v[j + 1];
+        s2 += v[j + 2];
+        s3 += v[j + 3];
     }
     if (live) {
-        const int64_t at = col0 / kSpan * g.ld_rows + row;
-        g.off[at] = off;
-        g.sum[at] = (s0 + s1) + (s2 + s3);
+        const int64_t to = col0 / kSpan * g.ld_rows + row;
+        g.off[to] = off;
+        g.sum[to] = (s0 + s1) + (s2 + s3);
     }
+    if constexpr (EP == kExp) store_span<DT>(box, map, g, true, row0, col0, 0, v);
 }
 
 // scale * (accumulator + earlier) of one warp's 32 rows x 128 columns.
 template <int DT>
 __device__ __forceinline__ void scaled_span(const GemmArgs &g, const CUtensorMap *map, const StoreBox &box,
-                                            uint32_t acc, int64_t row0, int64_t col0, int split, float scale) {
-    constexpr int kCols = 128 / Dtype<DT>::kSize;
+                                            float *v, int64_t row0, int64_t col0, int split, float scale) {
     const int64_t row = row0 + box.lane;
-    const int cols = static_cast<int>(min(int64_t(kSpan), g.N - col0));
-#pragma unroll 1
-    for (int c = 0; c < cols; c += 32) {
-        float v[32];
-        __syncwarp();
-        tc::load_cols32(acc + c, v);
-        if (g.earlier != nullptr && row < g.M) {
-            const float *e = g.earlier + row * g.ld_earlier + col0 + c;  // 16-byte aligned, padded to 32 columns
+    if (g.earlier != nullptr && row < g.M) {
+        const float *e = g.earlier + row * g.ld_earlier + col0;  // 16-byte aligned, padded to 64 columns
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < kSpan; j += 4) {
+            if (col0 + j < g.N) {
                 const float4 x = *reinterpret_cast<const float4 *>(e + j);
                 v[j] += x.x;
                 v[j + 1] += x.y;
@@ -264,13 +246,10 @@ __device__ __forceinline__ void scaled_span(const GemmArgs &g, const CUtensorMap
                 v[j + 3] += x.w;
             }
         }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= scale;
-        if (c % kCols == 0) box.open(g.tma_store != 0);
-        put32<DT>(box, c / 32, v);
-        if ((c + 32) % kCols == 0 || c + 32 >= cols)
-            flush<DT>(box, map, g, row0, col0 + c / kCols * kCols, split);
     }
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) v[j] *= scale;
+    store_span<DT>(box, map, g, g.tma_store != 0, row0, col0, split, v);
 }
 
 template <int AMN, int BMN, int EP, int DT>
@@ -311,8 +290,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::fence_after();
     const uint32_t tensor = b->tensor_base;
 
-    if (warp == 0) {
-        if (lane == 0) {
+    // registers: 64 a thread for the first four warps, 208 for the epilogue's
+    // eight (a row of 128 values each): 128 * 64 + 256 * 208 = 61,440 of the
+    // 384 * 168 = 64,512 the block was launched with
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 0 && lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -364,8 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (warp == 1 && lane == 0 && rank == 0) {
             const uint32_t idesc = tc::instruction(0, AMN, BMN, kTileM, kTileN) |
                                    (static_cast<uint32_t>(g.operand_type) << 7) |
                                    (static_cast<uint32_t>(g.operand_type) << 10);
@@ -378,55 +360,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const Tile x = tile_at(g, t);
                 int k0, k1;
                 k_range(g, x.split, k0, k1);
-                ok = wait(&b->acc_empty[buf], acc_phase ^ 1, b, g.timeouts);
-                tc::fence_after();
-                for (int k = k0; k < k1 && ok; ++k) {
-                    ok = wait(&b->full[stage], phase, b, g.timeouts);
-                    if (!ok) break;
+                for (int c = k0; c < k1 && ok; c += kChunk) {
+                    const int end = min(c + kChunk, k1);
+                    ok = wait(&b->acc_empty[buf], acc_phase ^ 1, b, g.timeouts);
                     tc::fence_after();
-                    const uint32_t sa = tc::smem_addr(smem + stage * kStageBytes);
-                    const uint64_t da = tc::operand(sa, AMN ? kHalfBytes / 2 : 16, 1024);
-                    const uint64_t db = tc::operand(sa + kHalfBytes, BMN ? kHalfBytes / 2 : 16, 1024);
+                    for (int k = c; k < end && ok; ++k) {
+                        ok = wait(&b->full[stage], phase, b, g.timeouts);
+                        if (!ok) break;
+                        tc::fence_after();
+                        const uint32_t sa = tc::smem_addr(smem + stage * kStageBytes);
+                        const uint64_t da = tc::operand(sa, AMN ? kHalfBytes / 2 : 16, 1024);
+                        const uint64_t db = tc::operand(sa + kHalfBytes, BMN ? kHalfBytes / 2 : 16, 1024);
 #pragma unroll
-                    for (int j = 0; j < kBlockK / 16; ++j)
-                        tc::mma_pair(tensor + buf * kTileN, da + j * kStepA, db + j * kStepB, idesc, k > k0 || j > 0);
-                    tc::commit_pair(&b->empty[stage]);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
+                        for (int j = 0; j < kBlockK / 16; ++j)
+                            tc::mma_pair(tensor + buf * kTileN, da + j * kStepA, db + j * kStepB, idesc,
+                                         k > c || j > 0);
+                        tc::commit_pair(&b->empty[stage]);
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
                     }
+                    if (!ok) break;
+                    tc::commit_pair(&b->acc_full[buf]);
+                    buf ^= 1;
+                    acc_phase ^= buf == 0;
                 }
-                if (!ok) break;
-                tc::commit_pair(&b->acc_full[buf]);
-                buf ^= 1;
-                acc_phase ^= buf == 0;
             }
         }
-    } else if (warp >= 4) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int quarter = warp % 4, half = (warp - 4) / 4;
         const StoreBox box{boxes + (warp - 4) * kStoreBytes, lane};
         float scale = 1.0f;
         if constexpr (EP == kScale) scale = g.scale_const * (g.scale != nullptr ? *g.scale : 1.0f);
         int buf = 0;
         uint32_t acc_phase = 0;
-        for (int t = first; t < total; t += step) {
+        bool ok = true;
+        for (int t = first; t < total && ok; t += step) {
             const Tile x = tile_at(g, t);
-            if (!wait(&b->acc_full[buf], acc_phase, b, g.timeouts)) break;
-            tc::fence_after();
+            int k0, k1;
+            k_range(g, x.split, k0, k1);
             const int64_t row0 = int64_t(x.m) * kTileM + rank * 128 + quarter * 32;
             const int64_t col0 = int64_t(x.n) * kTileN + half * kSpan;
-            const uint32_t acc = tensor + buf * kTileN + half * kSpan + (static_cast<uint32_t>(quarter * 32) << 16);
-            if (row0 < g.M && col0 < g.N) {
-                if constexpr (EP == kScale)
-                    scaled_span<DT>(g, &map_out, box, acc, row0, col0, x.split, scale);
-                else
-                    softmax_span<EP, DT>(g, &map_out, box, acc, row0, col0);
+            float v[kSpan];
+#pragma unroll
+            for (int j = 0; j < kSpan; ++j) v[j] = 0.0f;
+            for (int k = k0; k < k1; k += kChunk) {
+                if (!(ok = wait(&b->acc_full[buf], acc_phase, b, g.timeouts))) break;
+                tc::fence_after();
+                const uint32_t acc =
+                    tensor + buf * kTileN + half * kSpan + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+                for (int c = 0; c < kSpan; c += 32) {
+                    float r[32];
+                    __syncwarp();
+                    tc::load_cols32(acc + c, r);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[c + j] += r[j];
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::arrive_cluster(tc::peer_addr(tc::smem_addr(&b->acc_empty[buf]), 0));
+                buf ^= 1;
+                acc_phase ^= buf == 0;
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::arrive_cluster(tc::peer_addr(tc::smem_addr(&b->acc_empty[buf]), 0));
-            buf ^= 1;
-            acc_phase ^= buf == 0;
+            if (ok && row0 < g.M && col0 < g.N) {
+                if constexpr (EP == kScale)
+                    scaled_span<DT>(g, &map_out, box, v, row0, col0, x.split, scale);
+                else
+                    softmax_span<EP, DT>(g, &map_out, box, v, row0, col0);
+            }
         }
         if (lane == 0) tma::bulk_wait<0>();
     }
