@@ -554,6 +554,68 @@ fsdp_status fsdp_head_loss_workspace(const fsdp_head_loss_args *args, int64_t *b
  * matter and nothing is kept in it between calls. */
 fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* The global L2 norm of many tensors (device), in one pass:
+ *   norm = |scale| * sqrt(sum over tensors and elements of x^2)
+ * to *norm_out (device fp32). Squares are added in fp32 eight at a time and
+ * in fp64 from there, in an order the sizes fix: the same bits every time,
+ * and no overflow or underflow while the norm itself is a finite fp32. A
+ * NaN element makes it NaN, an infinite one infinite. Empty tensors and an
+ * empty list (norm 0) are fine.
+ *   tensors, numels, dtypes  host arrays: device (or mapped host) addresses,
+ *                element counts and fsdp_dtype values; any alignment.
+ *   scale        what the gradients are multiplied by before they count (the
+ *                inverse of a loss scale they carry; 1 if none).
+ *   workspace    device, fsdp_grad_norm_workspace's bytes, 16-byte aligned,
+ *                zeroed once by the caller before its first call; a call
+ *                leaves it ready for the next one in stream order. */
+fsdp_status fsdp_grad_norm_workspace(const int64_t *numels, const int32_t *dtypes, int n_tensors, int64_t *bytes_out);
+fsdp_status fsdp_grad_norm(const void *const *tensors, const int64_t *numels, const int32_t *dtypes, int n_tensors,
+                           float scale, float *norm_out, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Scale many tensors to a largest norm (device), without the host seeing it:
+ *   outs[k][i] = tensors[k][i] * (scale * min(1, max_norm / (*norm + 1e-6)))
+ * rounded once to the tensor's dtype. norm is what fsdp_grad_norm wrote for
+ * the same scale. outs[k] may be tensors[k] (in place; nothing is written
+ * when every tensor is in place and the factor is 1) or another buffer at any
+ * alignment, such as a parameter's view of a flat gradient buffer; written
+ * buffers overlap nothing else of the call. max_norm > 0. A norm of NaN makes
+ * everything NaN, an infinite one makes finite elements 0. */
+fsdp_status fsdp_clip_grads(const void *const *tensors, void *const *outs, const int64_t *numels,
+                            const int32_t *dtypes, int n_tensors, const float *norm, float max_norm, float scale,
+                            void *stream);
+
+/* The model step of fsdp_step_units with the averaged gradient clipped by
+ * its global norm between the reduce-scatter and AdamW (device):
+ *   g     = c * (G_0 + ... + G_{N-1})   per unit, as the fused step forms it
+ *   norm  = sqrt(sum over all units and elements of g^2)  -> *norm_out
+ *   coef  = min(1, max_norm / (norm + 1e-6))
+ *   AdamW, cast and all-gathers with g * coef in g's place.
+ * The norm is of what one replica's averaged gradient would have ("Fully
+ * Sharded Data Parallel: ...", "From all-reduce to sharded parameters": the
+ * shards together are the all-reduced gradient), not of any rank's own. With
+ * coef 1 the step's bits are fsdp_step_units'. A model is validated once
+ * (plan_create, with fsdp_step_units' checks) and launched per step; the
+ * first all-gather of a unit with at most 8 gathered buffers is written by
+ * its update.
+ *   workspace    device, fsdp_clip_plan_workspace's bytes (units of more than
+ *                8 gradient bytes an element, or offloaded, keep the fp32
+ *                average there: 4 bytes an element), 256-byte aligned, zeroed
+ *                once by the caller before the first launch; it must stay
+ *                allocated, like the units' buffers, and belongs to this plan.
+ *   nonfinite_count  device uint32 or NULL: incremented by the number of
+ *                averaged elements that are not finite (reported, never
+ *                skipped: the norm is then not finite either).
+ *   max_norm     > 0; infinity clips nothing. norm_out: device fp32.
+ * Other arguments, statuses and rules as fsdp_step_plan_create / _launch. */
+typedef struct fsdp_clip_plan fsdp_clip_plan;
+fsdp_status fsdp_clip_plan_workspace(const fsdp_unit *units, int n_units, int64_t *bytes_out);
+fsdp_status fsdp_clip_plan_create(const fsdp_unit *units, int n_units, int gathers, void *workspace,
+                                  int64_t workspace_bytes, uint32_t *nonfinite_count, uint32_t *wait_timeouts,
+                                  fsdp_clip_plan **plan_out);
+fsdp_status fsdp_clip_plan_launch(fsdp_clip_plan *plan, const fsdp_adamw_hparams *hp, float max_norm,
+                                  float *norm_out, void *stream);
+fsdp_status fsdp_clip_plan_destroy(fsdp_clip_plan *plan);
+
 /* Human-readable name of a status. Never NULL. */
 const char *fsdp_status_string(fsdp_status status);
 

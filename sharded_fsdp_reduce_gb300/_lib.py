@@ -55,6 +55,13 @@ EXPORTS = (
     "fsdp_step_plan_destroy",
     "fsdp_head_loss_workspace",
     "fsdp_head_loss",
+    "fsdp_grad_norm_workspace",
+    "fsdp_grad_norm",
+    "fsdp_clip_grads",
+    "fsdp_clip_plan_workspace",
+    "fsdp_clip_plan_create",
+    "fsdp_clip_plan_launch",
+    "fsdp_clip_plan_destroy",
 )
 
 
@@ -154,6 +161,14 @@ def load() -> ctypes.CDLL:
             "fsdp_step_plan_destroy": (i32, [vp]),
             "fsdp_head_loss_workspace": (i32, [ctypes.POINTER(FsdpHeadLossArgs), ctypes.POINTER(i64)]),
             "fsdp_head_loss": (i32, [ctypes.POINTER(FsdpHeadLossArgs), vp, i64, vp]),
+            "fsdp_grad_norm_workspace": (i32, [vp, vp, i32, ctypes.POINTER(i64)]),
+            "fsdp_grad_norm": (i32, [vp, vp, vp, i32, ctypes.c_float, vp, vp, i64, vp]),
+            "fsdp_clip_grads": (i32, [vp, vp, vp, vp, i32, vp, ctypes.c_float, ctypes.c_float, vp]),
+            "fsdp_clip_plan_workspace": (i32, [ctypes.POINTER(FsdpUnit), i32, ctypes.POINTER(i64)]),
+            "fsdp_clip_plan_create": (i32, [ctypes.POINTER(FsdpUnit), i32, i32, vp, i64, vp, vp,
+                                            ctypes.POINTER(vp)]),
+            "fsdp_clip_plan_launch": (i32, [vp, ctypes.POINTER(FsdpAdamwHparams), ctypes.c_float, vp, vp]),
+            "fsdp_clip_plan_destroy": (i32, [vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)

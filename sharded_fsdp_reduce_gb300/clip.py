@@ -1,0 +1,142 @@
+"""The global gradient norm and clipping: over a list of tensors, and inside a
+model's step (the kernels: csrc/clip_norm.cu, csrc/clip_scale.cu,
+csrc/clip_update.cuh)."""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence
+
+import torch
+
+from . import _lib
+from .fsdp import AdamWHParams, UnitDescs, _check, _counter, _dev, _stream, dtype_code
+
+__all__ = ["GradClip", "ClipPlan"]
+
+
+def _scalar(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() != 1:
+        raise ValueError(f"{name} must be a float32 CUDA scalar")
+    return _dev(t, name)
+
+
+class _Workspace:
+    """Zeroed device memory that calls on any stream may use, in order."""
+
+    def __init__(self, nbytes: int, device):
+        self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        made_on = torch.cuda.current_stream(self.buf.device)
+        self._made_on = made_on.cuda_stream
+        self._zeroed = made_on.record_event()
+
+    def on(self, stream: Optional[torch.cuda.Stream]) -> torch.cuda.Stream:
+        """The stream of a call (the current one by default), ordered after
+        the zeroing and holding the memory until its work is done."""
+        s = stream if stream is not None else torch.cuda.current_stream()
+        if s.cuda_stream != self._made_on:
+            # (a capture starts after the device is idle and cannot wait for work outside it)
+            if not torch.cuda.is_current_stream_capturing():
+                s.wait_event(self._zeroed)
+            self.buf.record_stream(s)
+        return s
+
+
+class GradClip:
+    """The L2 norm over gradient tensors and their scaling to a largest norm.
+
+    tensors: contiguous CUDA tensors of fp32, bf16 or fp16 (mixed is fine).
+    out: where clip() writes (same sizes and dtypes, any alignment, e.g. the
+    parameters' views of a rank's flat gradient buffer); default: in place.
+    scale: what the gradients are multiplied by, the inverse of a loss scale
+    they carry. Holds the tensors and their addresses: build a new one when
+    a tensor is replaced. Calls on one stream, or ordered between streams."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None,
+                 scale: float = 1.0):
+        self.tensors = list(tensors)
+        self.out = self.tensors if out is None else list(out)
+        self.scale = float(scale)
+        n = len(self.tensors)
+        if len(self.out) != n:
+            raise ValueError(f"out must hold {n} tensors")
+        for i, (t, o) in enumerate(zip(self.tensors, self.out)):
+            if o.dtype != t.dtype or o.numel() != t.numel():
+                raise ValueError(f"out[{i}] must hold {t.numel()} elements of {t.dtype}")
+        self._src = (ctypes.c_void_p * max(n, 1))(*[_dev(t, f"tensors[{i}]") for i, t in enumerate(self.tensors)])
+        self._dst = (ctypes.c_void_p * max(n, 1))(*[_dev(t, f"out[{i}]") for i, t in enumerate(self.out)])
+        self._numels = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in self.tensors])
+        self._dtypes = (ctypes.c_int32 * max(n, 1))(*[dtype_code(t.dtype) for t in self.tensors])
+        self._n = n
+        size = ctypes.c_int64(0)
+        _check(_lib.load().fsdp_grad_norm_workspace(self._numels, self._dtypes, n, ctypes.byref(size)),
+               "fsdp_grad_norm_workspace")
+        device = self.tensors[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        self._ws = _Workspace(size.value, device)
+        self._norm = torch.zeros((), dtype=torch.float32, device=device)
+
+    def norm(self, out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """The norm of scale * tensors, an fp32 CUDA scalar: out, or one this
+        object keeps and overwrites with every call."""
+        norm = self._norm if out is None else out
+        s = self._ws.on(stream)
+        _check(_lib.load().fsdp_grad_norm(self._src, self._numels, self._dtypes, self._n, self.scale,
+                                          _scalar(norm, "out"), self._ws.buf.data_ptr(), self._ws.buf.numel(),
+                                          s.cuda_stream), "fsdp_grad_norm")
+        return norm
+
+    def clip(self, max_norm: float, norm: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """out = tensors * scale * min(1, max_norm / (norm + 1e-6)). norm: the
+        norm to use (a CUDA scalar, e.g. one taken over more tensors than
+        these); default: these tensors', taken first. Returns the norm."""
+        if norm is None:
+            norm = self.norm(stream=stream)
+        _check(_lib.load().fsdp_clip_grads(self._src, self._dst, self._numels, self._dtypes, self._n,
+                                           _scalar(norm, "norm"), float(max_norm), self.scale, _stream(stream)),
+               "fsdp_clip_grads")
+        return norm
+
+
+class ClipPlan:
+    """A model's clipped step, validated once (fsdp_clip_plan_create): launch()
+    takes the averaged gradient's norm over all units, then each unit's AdamW
+    step with the clipped gradient and its all-gathers. The units' buffers
+    must stay allocated (the units are kept alive here)."""
+
+    def __init__(self, units, gathers: int = 1, nonfinite_count: Optional[torch.Tensor] = None,
+                 wait_timeouts: Optional[torch.Tensor] = None):
+        self.descs = units if isinstance(units, UnitDescs) else UnitDescs(units)
+        if not self.descs.adamw:
+            raise ValueError("a clipped model step needs fp32 master and AdamW state in every unit")
+        self._counters = (nonfinite_count, wait_timeouts)
+        self._handle = ctypes.c_void_p(None)
+        lib = _lib.load()
+        size = ctypes.c_int64(0)
+        _check(lib.fsdp_clip_plan_workspace(self.descs.array, self.descs.n, ctypes.byref(size)),
+               "fsdp_clip_plan_workspace")
+        self._ws = _Workspace(size.value, torch.device("cuda", torch.cuda.current_device()))
+        _check(lib.fsdp_clip_plan_create(self.descs.array, self.descs.n, int(gathers),
+                                         self._ws.buf.data_ptr(), self._ws.buf.numel(), _counter(nonfinite_count),
+                                         _counter(wait_timeouts, "wait_timeouts"), ctypes.byref(self._handle)),
+               "fsdp_clip_plan_create")
+
+    def launch(self, hparams: AdamWHParams, max_norm: float, norm: torch.Tensor,
+               stream: Optional[torch.cuda.Stream] = None) -> None:
+        """One step; norm (fp32 CUDA scalar) receives the gradient's norm."""
+        if not self._handle:
+            raise RuntimeError("the model step was destroyed")
+        s = self._ws.on(stream)
+        c = hparams.to_c()
+        _check(_lib.load().fsdp_clip_plan_launch(self._handle, ctypes.byref(c), float(max_norm),
+                                                 _scalar(norm, "norm"), s.cuda_stream), "fsdp_clip_plan_launch")
+
+    def close(self) -> None:
+        if self._handle:
+            _check(_lib.load().fsdp_clip_plan_destroy(self._handle), "fsdp_clip_plan_destroy")
+            self._handle = ctypes.c_void_p(None)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

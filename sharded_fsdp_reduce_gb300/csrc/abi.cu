@@ -12,6 +12,7 @@
 #include <new>
 #include <vector>
 
+#include "clip.cuh"
 #include "group.cuh"
 #include "host.cuh"
 
@@ -1452,6 +1453,311 @@ FSDP_API fsdp_status fsdp_check_bounded_wait(int64_t limit_cycles, uint32_t *wai
     if (wait_timeouts && !aligned(wait_timeouts, 4)) return FSDP_ERR_ALIGNMENT;
     return launch_stalled_wait(static_cast<long long>(limit_cycles), wait_timeouts,
                                static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the clipped model step
+
+namespace {
+
+// One norm launch's arguments, by its descriptor width.
+struct NormLaunch {
+    int width = 0;  // 1, 2, 4, 8 or FSDP_MAX_WORLD
+    int world = 0, dtype = 0;
+    int64_t grid = 0;
+    std::unique_ptr<clip::NormArgs<1>> a1;
+    std::unique_ptr<clip::NormArgs<2>> a2;
+    std::unique_ptr<clip::NormArgs<4>> a4;
+    std::unique_ptr<clip::NormArgs<8>> a8;
+    std::unique_ptr<clip::NormArgs<FSDP_MAX_WORLD>> any;
+
+    // Run f on the arguments this launch has.
+    template <class F> auto with(F &&f) {
+        switch (width) {
+            case 1: return f(a1);
+            case 2: return f(a2);
+            case 4: return f(a4);
+            case 8: return f(a8);
+            default: return f(any);
+        }
+    }
+};
+
+struct UpdateLaunch {
+    int source_dtype = 0, out_dtype = 0, world = 0;  // world: ranks read; unit_world: of the average's factor
+    int unit_world = 0;
+    bool average = false, host_state = false;
+    int64_t grid = 0;
+    std::unique_ptr<clip::UpdateArgs> a;
+};
+
+constexpr int64_t kClipHeader = 256;  // the norm's counter
+
+}  // namespace
+
+// A validated clipped model step (fsdp_clip_plan_*).
+struct fsdp_clip_plan {
+    ModelPlan m;
+    std::vector<NormLaunch> norms;
+    std::vector<UpdateLaunch> updates;
+    int64_t blocks = 0;       // of all the norm launches
+    int64_t average_bytes = 0;
+    uint8_t *workspace = nullptr;
+    int device = -1;
+};
+
+namespace {
+
+int64_t clip_bytes(const fsdp_clip_plan &p) {
+    return kClipHeader + (8 * p.blocks + 255) / 256 * 256 + p.average_bytes;
+}
+
+// Whether the update reads the averaged gradient from the workspace rather
+// than the ranks' gradients again (clip_update.cuh): where that is fewer
+// bytes, or where anything it reads or writes lies behind the host link.
+bool keeps_average(const UnitPlan &u, bool host) {
+    return host || u.rsa.world * dtype_size(u.grad_dtype) > 8;
+}
+
+bool unit_vec(const UnitPlan &u) {
+    const RsaArgs &r = u.rsa;
+    bool vec = aligned(r.master, 16) && aligned(r.m, 16) && aligned(r.v, 16) && aligned(r.out, 16);
+    for (int q = 0; q < r.world; ++q) vec = vec && aligned(r.grads[q], 16);
+    return vec;
+}
+
+// The gathered buffers the update writes itself: a unit's first all-gather,
+// where its buffers fit the update's descriptor.
+int fused_full(const UnitPlan &u) {
+    return u.separate_gathers > 0 && u.gather.n_dst <= clip::kUpdateFull ? u.gather.n_dst : 0;
+}
+
+template <class Args>
+fsdp_status add_norm_unit(fsdp_clip_plan &p, std::unique_ptr<Args> NormLaunch::*which, int width, const UnitPlan &u,
+                          float *average, uint32_t *nonfinite, int per_thread) {
+    const RsaArgs &r = u.rsa;
+    NormLaunch *l = nullptr;
+    for (NormLaunch &x : p.norms)
+        if (x.width == width && x.world == r.world && x.dtype == u.grad_dtype && (x.*which)->n < Args::kUnits) l = &x;
+    if (!l) {
+        p.norms.emplace_back();
+        l = &p.norms.back();
+        l->width = width;
+        l->world = r.world;
+        l->dtype = u.grad_dtype;
+        (l->*which).reset(new Args);
+        memset((l->*which).get(), 0, sizeof(Args));
+        (l->*which)->world = r.world;
+        (l->*which)->per_thread = per_thread;
+        (l->*which)->out.nonfinite = nonfinite;
+        (l->*which)->out.scale = 1.0f;
+    }
+    Args &a = *(l->*which);
+    auto &d = a.u[a.n++];
+    for (int q = 0; q < r.world; ++q) d.grads[q] = r.grads[q];
+    d.average = average;
+    d.numel = r.end;
+    d.cta_begin = l->grid;
+    d.lead = 0;
+    d.vec = 1;
+    for (int q = 0; q < r.world; ++q) d.vec = d.vec && aligned(r.grads[q], 16);
+    l->grid += clip::norm_ctas(r.end, 0, per_thread);
+    return FSDP_OK;
+}
+
+void add_update_unit(fsdp_clip_plan &p, const UnitPlan &u, bool host, float *average, bool keep) {
+    const RsaArgs &r = u.rsa;
+    UpdateLaunch key;
+    key.average = keep;
+    key.host_state = host;
+    key.source_dtype = keep ? static_cast<int>(FSDP_F32) : static_cast<int>(u.grad_dtype);
+    key.out_dtype = u.out_dtype;
+    key.world = keep ? 1 : r.world;
+    key.unit_world = r.world;
+    UpdateLaunch *l = nullptr;
+    for (UpdateLaunch &x : p.updates)
+        if (x.average == key.average && x.host_state == key.host_state && x.source_dtype == key.source_dtype &&
+            x.out_dtype == key.out_dtype && x.world == key.world && (keep || x.unit_world == key.unit_world) &&
+            x.a->n < clip::UpdateArgs::kUnits)
+            l = &x;
+    if (!l) {
+        p.updates.push_back(std::move(key));
+        l = &p.updates.back();
+        l->a.reset(new clip::UpdateArgs);
+        memset(l->a.get(), 0, sizeof(clip::UpdateArgs));
+        l->a->world = l->world;
+    }
+    clip::UpdateUnit &d = l->a->u[l->a->n++];
+    if (keep) {
+        d.grads[0] = average;
+    } else {
+        for (int q = 0; q < r.world; ++q) d.grads[q] = r.grads[q];
+    }
+    d.n_full = fused_full(u);
+    d.vec = unit_vec(u);
+    for (int k = 0; k < d.n_full; ++k) {
+        d.full[k] = u.gather.dst[k];
+        d.vec = d.vec && aligned(d.full[k], 16);
+    }
+    d.master = r.master;
+    d.m = r.m;
+    d.v = r.v;
+    d.out = r.out;
+    d.numel = r.end;
+    d.cta_begin = l->grid;
+    l->grid += clip::update_ctas(r.end);
+}
+
+// The launches of a validated model; addresses in the workspace are filled
+// when `workspace` is known (sizes do not depend on it).
+fsdp_status plan_clip(fsdp_clip_plan &p, uint8_t *workspace, uint32_t *nonfinite) {
+    ResidencyMemo res;
+    int64_t total = 0;
+    for (const UnitPlan &u : p.m.units)
+        if (!u.empty) total += u.rsa.end;
+    const int per_thread = clip::norm_per_thread(total);
+    int64_t blocks = 0;
+    for (const UnitPlan &u : p.m.units)
+        if (!u.empty) blocks += clip::norm_ctas(u.rsa.end, 0, per_thread);
+    if (blocks > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
+    p.blocks = blocks;
+    const int64_t averages = kClipHeader + (8 * blocks + 255) / 256 * 256;
+    p.average_bytes = 0;
+    for (const UnitPlan &u : p.m.units) {
+        if (u.empty) continue;
+        bool host = res.host_resident(u.rsa.master) || res.host_resident(u.rsa.m) || res.host_resident(u.rsa.v);
+        bool host_grads = false;
+        for (int q = 0; q < u.rsa.world; ++q) host_grads = host_grads || res.host_resident(u.rsa.grads[q]);
+        const bool keep = keeps_average(u, host || host_grads);
+        float *average = nullptr;
+        if (keep) {
+            if (workspace) average = reinterpret_cast<float *>(workspace + averages + p.average_bytes);
+            p.average_bytes += (4 * u.rsa.end + 255) / 256 * 256;
+        }
+        if (!workspace) continue;
+        fsdp_status st = FSDP_OK;
+        switch (u.rsa.world) {
+            case 1: st = add_norm_unit(p, &NormLaunch::a1, 1, u, average, nonfinite, per_thread); break;
+            case 2: st = add_norm_unit(p, &NormLaunch::a2, 2, u, average, nonfinite, per_thread); break;
+            case 4: st = add_norm_unit(p, &NormLaunch::a4, 4, u, average, nonfinite, per_thread); break;
+            case 8: st = add_norm_unit(p, &NormLaunch::a8, 8, u, average, nonfinite, per_thread); break;
+            default: st = add_norm_unit(p, &NormLaunch::any, FSDP_MAX_WORLD, u, average, nonfinite, per_thread);
+        }
+        if (st != FSDP_OK) return st;
+        add_update_unit(p, u, host, average, keep);
+    }
+    p.workspace = workspace;
+    return FSDP_OK;
+}
+
+fsdp_status run_clip(fsdp_clip_plan &p, const fsdp_adamw_hparams &hp, float max_norm, float *norm, cudaStream_t s) {
+    if (p.blocks == 0) return cuda_status(cudaMemsetAsync(norm, 0, 4, s));
+    int64_t part = 0;
+    for (NormLaunch &l : p.norms) {
+        const fsdp_status st = l.with([&](auto &a) {
+            a->c = make_scalars(hp, l.world).c;
+            a->out.ticket = reinterpret_cast<uint32_t *>(p.workspace);
+            a->out.part = reinterpret_cast<double *>(p.workspace + kClipHeader);
+            a->out.part_begin = part;
+            a->out.part_count = p.blocks;
+            a->out.norm = norm;
+            return clip::launch_norm(*a, l.dtype, l.grid, s);
+        });
+        if (st != FSDP_OK) return st;
+        part += l.grid;
+    }
+    for (size_t i = p.updates.size(); i-- > 0;) {
+        UpdateLaunch &l = p.updates[i];
+        l.a->s = make_scalars(hp, l.unit_world);
+        if (l.average) l.a->s.c = 1.0f;
+        l.a->norm = norm;
+        l.a->max_norm = max_norm;
+        const fsdp_status st = l.source_dtype == FSDP_F32
+                                   ? clip::launch_update_f32(*l.a, l.out_dtype, l.host_state, l.grid, s)
+                               : l.source_dtype == FSDP_BF16 ? clip::launch_update_bf16(*l.a, l.out_dtype, l.grid, s)
+                                                             : clip::launch_update_f16(*l.a, l.out_dtype, l.grid, s);
+        if (st != FSDP_OK) return st;
+    }
+    // the all-gathers the updates have not written
+    for (const Work &w : p.m.work) {
+        if (w.group) {
+            const Group &g = *w.group;  // batched units have at most kGroupMaxWorld buffers: their first is done
+            for (int k = 1; k < g.gathers; ++k)
+                if (fsdp_status st = launch_gather_group(g.gather, g.gather_grid, s); st != FSDP_OK) return st;
+        } else {
+            const UnitPlan &u = p.m.units[static_cast<size_t>(w.unit)];
+            for (int k = fused_full(u) > 0 ? 1 : 0; k < u.separate_gathers; ++k)
+                if (fsdp_status st = launch_gather(u.gather, s); st != FSDP_OK) return st;
+        }
+    }
+    return FSDP_OK;
+}
+
+static_assert(kGroupMaxWorld <= clip::kUpdateFull, "a batched unit's first gather is written by its update");
+
+}  // namespace
+
+extern "C" {
+
+FSDP_API fsdp_status fsdp_clip_plan_workspace(const fsdp_unit *units, int n_units, int64_t *bytes_out) {
+    return guarded([&]() -> fsdp_status {
+        if (!bytes_out) return FSDP_ERR_INVALID_ARG;
+        fsdp_clip_plan p;
+        fsdp_status st = plan_units(units, n_units, &kPlaceholderHp, 0, 0, nullptr, nullptr, p.m);
+        if (st == FSDP_OK) st = plan_clip(p, nullptr, nullptr);
+        if (st != FSDP_OK) return st;
+        *bytes_out = clip_bytes(p);
+        return FSDP_OK;
+    });
+}
+
+FSDP_API fsdp_status fsdp_clip_plan_create(const fsdp_unit *units, int n_units, int gathers, void *workspace,
+                                           int64_t workspace_bytes, uint32_t *nonfinite_count,
+                                           uint32_t *wait_timeouts, fsdp_clip_plan **plan_out) {
+    return guarded([&]() -> fsdp_status {
+        if (!plan_out) return FSDP_ERR_INVALID_ARG;
+        *plan_out = nullptr;
+        std::unique_ptr<fsdp_clip_plan> p(new fsdp_clip_plan);
+        fsdp_status st = plan_units(units, n_units, &kPlaceholderHp, gathers, 0, nonfinite_count, wait_timeouts, p->m);
+        if (st != FSDP_OK) return st;
+        if (!workspace) return FSDP_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256)) return FSDP_ERR_ALIGNMENT;
+        if ((st = plan_clip(*p, static_cast<uint8_t *>(workspace), nonfinite_count)) != FSDP_OK) return st;
+        const int64_t bytes = clip_bytes(*p);
+        if (workspace_bytes < bytes) return FSDP_ERR_INVALID_ARG;
+        for (const std::vector<Span> *spans : {&p->m.writes, &p->m.reads})
+            for (const Span &x : *spans)
+                if (overlaps(reinterpret_cast<const void *>(x.lo), x.hi - x.lo, workspace, static_cast<size_t>(bytes)))
+                    return FSDP_ERR_INVALID_ARG;
+        if (cudaGetDevice(&p->device) != cudaSuccess) {
+            (void)cudaGetLastError();
+            p->device = -1;
+        }
+        *plan_out = p.release();
+        return FSDP_OK;
+    });
+}
+
+FSDP_API fsdp_status fsdp_clip_plan_launch(fsdp_clip_plan *plan, const fsdp_adamw_hparams *hp, float max_norm,
+                                           float *norm_out, void *stream) {
+    return guarded([&]() -> fsdp_status {
+        if (!plan || !hp || !norm_out || !(max_norm > 0.0f)) return FSDP_ERR_INVALID_ARG;
+        if (!adam_step_valid(*hp)) return FSDP_ERR_INVALID_ARG;
+        if (!aligned(norm_out, 4)) return FSDP_ERR_ALIGNMENT;
+        int dev = -1;
+        if (cudaGetDevice(&dev) != cudaSuccess) {
+            (void)cudaGetLastError();
+            dev = -1;
+        }
+        if (dev != plan->device) return FSDP_ERR_INVALID_ARG;
+        return run_clip(*plan, *hp, max_norm, norm_out, static_cast<cudaStream_t>(stream));
+    });
+}
+
+FSDP_API fsdp_status fsdp_clip_plan_destroy(fsdp_clip_plan *plan) {
+    delete plan;
+    return FSDP_OK;
 }
 
 }  // extern "C"
