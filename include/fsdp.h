@@ -498,7 +498,7 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  * gives the gradients that are then averaged).
  * Precision: every sum and statistic is fp32 or wider. bf16 and fp16 heads:
  * d is rounded once to the head's type (fp16: times 2^14) for the gradient
- * products, the exponentials are held in fp16 relative to the largest of 128
+ * products, the exponentials are held in fp16 relative to the largest of 64
  * columns before that. fp32 heads: every operand as three bf16 parts, the
  * products as exact as fp32's.
  *   hidden       device, tokens rows of dim elements at stride ld_hidden.

@@ -2,6 +2,9 @@
 // tensors to a largest norm, and the clipped model step.
 #pragma once
 
+#include <stddef.h>
+#include <string.h>
+
 #include "host.cuh"
 
 namespace fsdp {
@@ -17,10 +20,18 @@ __device__ __forceinline__ float coefficient(float norm, float max_norm) {
 }
 
 // Descriptors travel by value in the kernel's parameter space; a launch takes
-// as many as fit about 28 KB.
+// as many as fit about 28 KB. Up to kFew go in a struct of that size: a short
+// launch does not pay for copying the long one's.
 constexpr int capacity(size_t descriptor) {
     const size_t n = 28000 / descriptor;
     return static_cast<int>(n < 512 ? n : 512);
+}
+constexpr int kFew = 16;
+
+// The first a.n <= kFew descriptors of `a`, and all that lies before them.
+template <class Args, class Few> void few_of(const Args &a, Few &few) {
+    memcpy(static_cast<void *>(&few), &a, offsetof(Args, u));
+    memcpy(static_cast<void *>(few.u), a.u, sizeof(a.u[0]) * static_cast<size_t>(a.n));
 }
 
 // ---------------------------------------------------------------- norm
@@ -48,8 +59,8 @@ struct NormOut {
     uint32_t *nonfinite; // count of averaged values that are not finite, or NULL
 };
 
-template <int W> struct NormArgs {
-    static constexpr int kUnits = capacity(sizeof(NormUnit<W>));
+template <int W, int CAP = capacity(sizeof(NormUnit<W>))> struct NormArgs {
+    static constexpr int kUnits = CAP;
     NormOut out;
     float c;             // average = c * sum over the ranks
     int32_t n, world;
@@ -85,14 +96,15 @@ struct ScaleUnit {
     int32_t vec;     // src lies as dst does on 16 bytes
 };
 
-struct ScaleArgs {
-    static constexpr int kUnits = capacity(sizeof(ScaleUnit));
+template <int CAP> struct ScaleArgsOf {
+    static constexpr int kUnits = CAP;
     const float *norm;
     float max_norm, scale;
     int32_t n;
     int32_t in_place;  // every dst is its src: nothing to do for a factor of 1
     ScaleUnit u[kUnits];
 };
+using ScaleArgs = ScaleArgsOf<capacity(sizeof(ScaleUnit))>;
 
 constexpr int kScaleChunks = 4;  // chunks per thread
 inline int64_t scale_ctas(int64_t numel, int lead) { return norm_ctas(numel, lead, kScaleChunks); }
@@ -115,14 +127,15 @@ struct UpdateUnit {
     int32_t vec;
 };
 
-struct UpdateArgs {
-    static constexpr int kUnits = capacity(sizeof(UpdateUnit));
+template <int CAP> struct UpdateArgsOf {
+    static constexpr int kUnits = CAP;
     AdamScalars s;   // c: the average's factor, 1 for an average
     const float *norm;
     float max_norm;
     int32_t n, world;
     UpdateUnit u[kUnits];
 };
+using UpdateArgs = UpdateArgsOf<capacity(sizeof(UpdateUnit))>;
 
 inline int64_t update_ctas(int64_t numel) { return (numel + 8 * kThreads - 1) / (8 * kThreads); }
 

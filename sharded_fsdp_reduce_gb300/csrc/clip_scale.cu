@@ -33,7 +33,8 @@ template <int DT> __device__ __forceinline__ void load8(const void *base, int64_
     }
 }
 
-template <int DT> __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ ScaleArgs a) {
+template <int DT, int CAP>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ ScaleArgsOf<CAP> a) {
     const float f = __fmul_rn(a.scale, coefficient(*a.norm, a.max_norm));
     if (a.in_place && f == 1.0f) return;
     const int64_t cta = gridDim.x - 1 - blockIdx.x;
@@ -69,19 +70,28 @@ template <int DT> __global__ void __launch_bounds__(kThreads) scale_kernel(const
     }
 }
 
+template <int CAP>
+fsdp_status launch_capacity(const ScaleArgsOf<CAP> &a, int dtype, unsigned grid, cudaStream_t s) {
+    switch (dtype) {
+        case FSDP_BF16: scale_kernel<FSDP_BF16, CAP><<<grid, kThreads, 0, s>>>(a); break;
+        case FSDP_F16: scale_kernel<FSDP_F16, CAP><<<grid, kThreads, 0, s>>>(a); break;
+        default: scale_kernel<FSDP_F32, CAP><<<grid, kThreads, 0, s>>>(a);
+    }
+    return check_launch();
+}
+
 }  // namespace
 
 static_assert(sizeof(ScaleArgs) < 32764, "kernel parameter space");
 
 fsdp_status launch_scale(const ScaleArgs &a, int dtype, int64_t grid, cudaStream_t s) {
     if (a.n < 1 || a.n > ScaleArgs::kUnits || grid < 1 || grid > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
-    const unsigned n = static_cast<unsigned>(grid);
-    switch (dtype) {
-        case FSDP_BF16: scale_kernel<FSDP_BF16><<<n, kThreads, 0, s>>>(a); break;
-        case FSDP_F16: scale_kernel<FSDP_F16><<<n, kThreads, 0, s>>>(a); break;
-        default: scale_kernel<FSDP_F32><<<n, kThreads, 0, s>>>(a);
+    if (a.n <= kFew) {
+        ScaleArgsOf<kFew> few;
+        few_of(a, few);
+        return launch_capacity(few, dtype, static_cast<unsigned>(grid), s);
     }
-    return check_launch();
+    return launch_capacity(a, dtype, static_cast<unsigned>(grid), s);
 }
 
 }  // namespace clip

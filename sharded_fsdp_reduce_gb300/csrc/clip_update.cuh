@@ -22,8 +22,9 @@ namespace clip {
 
 // SPLIT: the lane-interleaved chunks of state in host memory (rsa_impl.cuh);
 // a CTA then has eight warp blocks of 256 elements, the same 2048 in all.
-template <int NW, int GD, int OD, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, SPLIT ? 1 : 3) update_kernel(const __grid_constant__ UpdateArgs a) {
+template <int NW, int GD, int OD, bool SPLIT, int CAP>
+__global__ void __launch_bounds__(kThreads, SPLIT ? 1 : 3)
+    update_kernel(const __grid_constant__ UpdateArgsOf<CAP> a) {
     const int64_t cta = gridDim.x - 1 - blockIdx.x;
     const UpdateUnit &u = a.u[unit_of(a.u, a.n, cta)];
     const int64_t first = (cta - u.cta_begin) * (8 * kThreads);
@@ -75,16 +76,25 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 1 : 3) update_kernel(const _
     }
 }
 
+template <int NW, int GD, bool SPLIT, int CAP>
+fsdp_status launch_capacity(const UpdateArgsOf<CAP> &a, int out_dtype, unsigned grid, cudaStream_t s) {
+    switch (out_dtype) {
+        case FSDP_BF16: update_kernel<NW, GD, FSDP_BF16, SPLIT, CAP><<<grid, kThreads, 0, s>>>(a); break;
+        case FSDP_F16: update_kernel<NW, GD, FSDP_F16, SPLIT, CAP><<<grid, kThreads, 0, s>>>(a); break;
+        default: update_kernel<NW, GD, FSDP_F32, SPLIT, CAP><<<grid, kThreads, 0, s>>>(a);
+    }
+    return check_launch();
+}
+
 template <int NW, int GD, bool SPLIT>
 fsdp_status launch_out(const UpdateArgs &a, int out_dtype, int64_t grid, cudaStream_t s) {
     if (a.n < 1 || a.n > UpdateArgs::kUnits || grid < 1 || grid > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
-    const unsigned n = static_cast<unsigned>(grid);
-    switch (out_dtype) {
-        case FSDP_BF16: update_kernel<NW, GD, FSDP_BF16, SPLIT><<<n, kThreads, 0, s>>>(a); break;
-        case FSDP_F16: update_kernel<NW, GD, FSDP_F16, SPLIT><<<n, kThreads, 0, s>>>(a); break;
-        default: update_kernel<NW, GD, FSDP_F32, SPLIT><<<n, kThreads, 0, s>>>(a);
+    if (a.n <= kFew) {
+        UpdateArgsOf<kFew> few;
+        few_of(a, few);
+        return launch_capacity<NW, GD, SPLIT>(few, out_dtype, static_cast<unsigned>(grid), s);
     }
-    return check_launch();
+    return launch_capacity<NW, GD, SPLIT>(a, out_dtype, static_cast<unsigned>(grid), s);
 }
 
 // 16-bit gradients of up to four ranks.

@@ -5,7 +5,7 @@
 //   dX = g d W                          dW = g d^T X
 //
 // The logits in fp32 live in tensor memory only. The logits product's epilogue
-// turns each span of 128 columns into exponentials against the span's own
+// turns each span of 64 columns into exponentials against the span's own
 // maximum, and keeps their fp32 sum and that reference; a row kernel joins the
 // spans into lse. Without gradients that is all: X and W are read, a few bytes
 // per span are written. With gradients the exponentials of a band of tokens
@@ -190,8 +190,8 @@ template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __gri
     const int64_t row0 = int64_t(blockIdx.x / a.col_blocks) * kGradRows;
     const int64_t col0 = int64_t(blockIdx.x % a.col_blocks) * kGradCols;
     constexpr float kGain = DT == FSDP_F16 ? kHalfGain : 1.0f;
-    {
-        const int r = threadIdx.x % kGradRows, s = threadIdx.x / kGradRows;
+    for (int i = threadIdx.x; i < kGradRows * (kGradCols / kSpan); i += 256) {
+        const int r = i % kGradRows, s = i / kGradRows;
         const int64_t row = row0 + r, span = col0 / kSpan + s;
         if (row < a.rows) {
             // e * 2^(off - lse2) is the probability; a target outside the

@@ -14,7 +14,7 @@ constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kBlockK = 64;
 // Columns whose exponentials share one reference (one epilogue warp's).
-constexpr int kSpan = 128;
+constexpr int kSpan = 64;
 
 // What a product's epilogue does with the accumulator.
 enum Epilogue {
@@ -31,6 +31,7 @@ struct GemmArgs {
     int32_t kblocks;       // K blocks per operand pair
     int32_t pairs;         // 1, or 6 plane pairs of an fp32 head
     int32_t tiles_m, tiles_n, splits;
+    int32_t k_each, k_more;  // K blocks of a split, and the splits that have one more
     int32_t group;         // tiles of the fast dimension visited together
     int32_t m_fast;        // 1: rows are the fast dimension
     int32_t operand_type;  // 0 fp16, 1 bf16

@@ -8,7 +8,7 @@
 //
 // A pair of CTAs (one cluster) works on a 256 x 256 tile of the result: each
 // loads 128 rows of A and 128 of B per 64-wide K block by TMA (32 KB a stage,
-// six stages), the even CTA issues the tcgen05 products for both (M = N = 256,
+// five stages), the even CTA issues the tcgen05 products for both (M = N = 256,
 // K = 16), and each CTA's tensor memory holds 128 rows of the accumulator in
 // fp32, twice (2 x 256 columns): the epilogue of one tile runs while the next
 // one's products are issued. The pair shape halves the operand bytes that
@@ -16,9 +16,10 @@
 // 128 x 256. Persistent: one CTA per SM, tiles taken in a fixed order that
 // keeps the reused operand in L2.
 //
-// Roles by warp: 0 loads, 1 issues the products, 2 owns tensor memory, 4-11
+// Roles by warp: 0 loads A and 3 loads B, 1 issues the products, 2 owns tensor
+// memory, 4-19
 // are the epilogue: warp w reads lanes 32 (w % 4) .. + 31 (one row per
-// thread), columns 128 ((w - 4) / 4) .. + 127.
+// thread), columns 64 ((w - 4) / 4) .. + 63.
 //
 // An fp32 operand is held as three bf16 planes (its leading, middle and last
 // 8 bits); the K loop then runs over the six plane pairs whose products reach
@@ -39,9 +40,9 @@
 namespace fsdp {
 namespace loss {
 
-constexpr int kThreads = 384;
-constexpr int kEpilogueWarps = 8;
-constexpr int kStages = 6;
+constexpr int kThreads = 640;
+constexpr int kEpilogueWarps = 16;
+constexpr int kStages = 5;
 // K blocks summed in tensor memory before the sum moves to registers. The
 // tensor cores' own sum loses bits at every K = 16 (a chain of 5120 / 16 adds
 // left a loss 2.4e-6 off, 64 bits against it); chains of 512 / 16 joined by
@@ -85,18 +86,18 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs &g, int t) {
     return r;
 }
 
+// The K blocks (of all operand pairs) of a split.
 __device__ __forceinline__ void k_range(const GemmArgs &g, int split, int &begin, int &end) {
-    const int64_t total = int64_t(g.kblocks) * g.pairs;
-    begin = static_cast<int>(total * split / g.splits);
-    end = static_cast<int>(total * (split + 1) / g.splits);
+    begin = split * g.k_each + min(split, g.k_more);
+    end = begin + g.k_each + (split < g.k_more ? 1 : 0);
 }
 
 // Bounded wait; false once any wait of this CTA has given up.
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Barriers *b, uint32_t *timeouts) {
-    if (tc::try_wait_cluster(bar, parity)) return true;
+    if (tma::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     volatile int32_t *gave_up = &b->gave_up;
-    while (!tc::try_wait_cluster(bar, parity)) {
+    while (!tma::mbar_try_wait(bar, parity)) {
         if (*gave_up) return false;
         if (clock64() - t0 > kWaitCycles) {
             *gave_up = 1;
@@ -148,7 +149,7 @@ template <int DT> __device__ __forceinline__ void put_row(const StoreBox &box, c
     }
 }
 
-// Store one warp's 32 rows x 128 columns, box by box; z: the plane or split.
+// Store one warp's 32 rows x 64 columns, box by box; z: the plane or split.
 template <int DT>
 __device__ __forceinline__ void store_span(const StoreBox &box, const CUtensorMap *map, const GemmArgs &g,
                                            bool tma_store, int64_t row0, int64_t col0, int z, const float *v) {
@@ -180,17 +181,17 @@ __device__ __forceinline__ void store_span(const StoreBox &box, const CUtensorMa
     }
 }
 
-// Softmax statistics (and exponentials) of one warp's 32 rows x 128 columns.
+// Softmax statistics (and exponentials) of one warp's 32 rows x 64 columns.
 // With l2 = logit * log2(e), a span's exponentials are e = 2^(l2 - off), off =
 // max(l2) - 15: at most 2^15, so that fp16 holds them with 11 bits down to
 // 2^-29 of the span's largest (what is smaller is below 2^-40 of it).
 template <int EP, int DT>
 __device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMap *map, const StoreBox &box,
-                                             float *v, int64_t row0, int64_t col0) {
+                                             float *v, int64_t row0, int64_t col0, int64_t target) {
     constexpr float kLog2e = 1.44269504088896340736f;
     const int64_t row = row0 + box.lane;
     const bool live = row < g.M;
-    const int64_t at = (live ? g.targets[row] : -1) - col0;
+    const int64_t at = target - col0;
     if (at >= 0 && at < kSpan && at + col0 < g.N) {
         float t = 0.0f;
 #pragma unroll
@@ -229,7 +230,7 @@ __device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMa
     if constexpr (EP == kExp) store_span<DT>(box, map, g, true, row0, col0, 0, v);
 }
 
-// scale * (accumulator + earlier) of one warp's 32 rows x 128 columns.
+// scale * (accumulator + earlier) of one warp's 32 rows x 64 columns.
 template <int DT>
 __device__ __forceinline__ void scaled_span(const GemmArgs &g, const CUtensorMap *map, const StoreBox &box,
                                             float *v, int64_t row0, int64_t col0, int split, float scale) {
@@ -252,6 +253,110 @@ __device__ __forceinline__ void scaled_span(const GemmArgs &g, const CUtensorMap
     store_span<DT>(box, map, g, g.tma_store != 0, row0, col0, split, v);
 }
 
+// One operand's loads, by one thread of each CTA: its 128 rows of every K
+// block of every tile, into the stages in turn. Each operand has a thread of
+// its own: one thread that issued both (and divided to find its place) took
+// 830 cycles a K block, the products 512.
+template <int MN, bool A>
+__device__ __forceinline__ void load_operand(const GemmArgs &g, const CUtensorMap *map, uint8_t *smem, Barriers *b,
+                                             uint32_t rank, int first, int total, int step) {
+    const uint32_t full = tc::peer_addr(tc::smem_addr(&b->full[0]), 0);
+    const int kblocks = g.kblocks;
+    const bool planes = g.pairs > 1;
+    uint32_t *timeouts = g.timeouts;
+    int stage = 0;
+    uint32_t phase = 1;
+    for (int t = first; t < total; t += step) {
+        const Tile x = tile_at(g, t);
+        int k0, k1;
+        k_range(g, x.split, k0, k1);
+        const int at = (A ? x.m * kTileM : x.n * kTileN) + static_cast<int>(rank) * 128;
+        int pair = planes ? k0 / kblocks : 0;
+        int kb = k0 - pair * kblocks;
+        for (int k = k0; k < k1; ++k) {
+            if (!wait(&b->empty[stage], phase, b, timeouts)) return;
+            const int z = planes ? ((A ? kPlanesA : kPlanesB) >> (4 * pair)) & 15 : 0;
+            if (A && rank == 0) tma::mbar_arrive_expect_tx(&b->full[stage], 2 * kStageBytes);
+            uint8_t *dst = smem + stage * kStageBytes;
+            const uint32_t bar = full + stage * static_cast<uint32_t>(sizeof(uint64_t));
+            if constexpr (MN) {
+                tc::load_tile(dst, map, at, kb * kBlockK, z, bar);
+                tc::load_tile(dst + kHalfBytes / 2, map, at + 64, kb * kBlockK, z, bar);
+            } else {
+                tc::load_tile(dst, map, kb * kBlockK, at, z, bar);
+            }
+            if (++kb == kblocks) {
+                kb = 0;
+                ++pair;
+            }
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    // the last use of every stage has been consumed: no copy of this CTA is in
+    // flight and no product still signals its barriers
+    for (int s = 0; s < kStages; ++s) {
+        if (!wait(&b->empty[stage], phase, b, g.timeouts)) return;
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+}
+
+// The products of every tile, by one warp of the even CTA for the pair. The
+// whole warp runs the loop and one elected thread issues: what it issues with
+// then stays in uniform registers (a single thread's loop moved every operand
+// there first, 560 cycles a K block against the products' 512).
+template <int AMN, int BMN>
+__device__ __forceinline__ void issue_products(const GemmArgs &g, uint8_t *smem, Barriers *b, uint32_t tensor,
+                                               int first, int total, int step) {
+    const uint32_t idesc = tc::instruction(0, AMN, BMN, kTileM, kTileN) |
+                           (static_cast<uint32_t>(g.operand_type) << 7) |
+                           (static_cast<uint32_t>(g.operand_type) << 10);
+    // per K = 16: 32 bytes along a K-major row, two groups of eight K otherwise
+    constexpr uint32_t kStepA = (AMN ? 2048 : 32) >> 4, kStepB = (BMN ? 2048 : 32) >> 4;
+    constexpr uint32_t kHigh = tc::operand_high(1024);
+    const uint32_t sa = tc::smem_addr(smem);
+    const uint32_t a0 = tc::operand_low(sa, AMN ? kHalfBytes / 2 : 16);
+    const uint32_t b0 = tc::operand_low(sa + kHalfBytes, BMN ? kHalfBytes / 2 : 16);
+    const int tiles = g.tiles_m * g.tiles_n, splits = g.splits;
+    uint32_t *timeouts = g.timeouts;
+    int k0, k1;
+    k_range(g, 0, k0, k1);
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, acc_phase = 1;
+    for (int t = first; t < total; t += step) {
+        if (splits > 1) k_range(g, t / tiles, k0, k1);
+        for (int c = k0; c < k1; c += kChunk) {
+            if (!wait(&b->acc_empty[buf], acc_phase, b, timeouts)) return;
+            tc::fence_after();
+            const int end = min(c + kChunk, k1);
+            const uint32_t d = tensor + buf * kTileN;
+            for (int k = c; k < end; ++k) {
+                if (!wait(&b->full[stage], phase, b, timeouts)) return;
+                tc::fence_after();
+                const uint32_t da = a0 + stage * (kStageBytes >> 4), db = b0 + stage * (kStageBytes >> 4);
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < kBlockK / 16; ++j)
+                        tc::mma_pair(d, da + j * kStepA, db + j * kStepB, kHigh, idesc, k > c || j > 0);
+                    tc::commit_pair(&b->empty[stage]);
+                    if (k + 1 == end) tc::commit_pair(&b->acc_full[buf]);
+                }
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            buf ^= 1;
+            acc_phase ^= buf == 0;
+        }
+    }
+}
+
 template <int AMN, int BMN, int EP, int DT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -260,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *boxes = smem + kStages * kStageBytes;
     Barriers *b = reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * kStoreBytes);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // (uniform)
     const uint32_t rank = tc::cluster_rank();
     const int total = g.tiles_m * g.tiles_n * g.splits;
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
@@ -290,107 +395,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::fence_after();
     const uint32_t tensor = b->tensor_base;
 
-    // registers: 64 a thread for the first four warps, 208 for the epilogue's
-    // eight (a row of 128 values each): 128 * 64 + 256 * 208 = 61,440 of the
-    // 384 * 168 = 64,512 the block was launched with
+    // registers: 56 a thread for the first four warps, 104 for the epilogue's
+    // sixteen (a row of 64 sums each): 128 * 56 + 512 * 104 = 60,416 of the
+    // 640 * 96 = 61,440 the block was launched with
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == 0 && lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = first; t < total && ok; t += step) {
-                const Tile x = tile_at(g, t);
-                int k0, k1;
-                k_range(g, x.split, k0, k1);
-                const int row = x.m * kTileM + static_cast<int>(rank) * 128;
-                const int col = x.n * kTileN + static_cast<int>(rank) * 128;
-                for (int k = k0; k < k1; ++k) {
-                    if (!wait(&b->empty[stage], phase ^ 1, b, g.timeouts)) {
-                        ok = false;
-                        break;
-                    }
-                    const int pair = k / g.kblocks, kk = (k - pair * g.kblocks) * kBlockK;
-                    int za = 0, zb = 0;
-                    if (g.pairs > 1) {
-                        za = (kPlanesA >> (4 * pair)) & 15;
-                        zb = (kPlanesB >> (4 * pair)) & 15;
-                    }
-                    if (rank == 0) tma::mbar_arrive_expect_tx(&b->full[stage], 2 * kStageBytes);
-                    const uint32_t bar = tc::peer_addr(tc::smem_addr(&b->full[stage]), 0);
-                    uint8_t *sa = smem + stage * kStageBytes, *sb = sa + kHalfBytes;
-                    if constexpr (AMN) {
-                        tc::load_tile(sa, &map_a, row, kk, za, bar);
-                        tc::load_tile(sa + kHalfBytes / 2, &map_a, row + 64, kk, za, bar);
-                    } else {
-                        tc::load_tile(sa, &map_a, kk, row, za, bar);
-                    }
-                    if constexpr (BMN) {
-                        tc::load_tile(sb, &map_b, col, kk, zb, bar);
-                        tc::load_tile(sb + kHalfBytes / 2, &map_b, col + 64, kk, zb, bar);
-                    } else {
-                        tc::load_tile(sb, &map_b, kk, col, zb, bar);
-                    }
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            // the last use of every stage has been consumed: no copy of this
-            // CTA is in flight and no product still signals its barriers
-            for (int s = 0; s < kStages && ok; ++s) {
-                ok = wait(&b->empty[stage], phase ^ 1, b, g.timeouts);
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        if (warp == 1 && lane == 0 && rank == 0) {
-            const uint32_t idesc = tc::instruction(0, AMN, BMN, kTileM, kTileN) |
-                                   (static_cast<uint32_t>(g.operand_type) << 7) |
-                                   (static_cast<uint32_t>(g.operand_type) << 10);
-            // per K = 16: 32 bytes along a K-major row, two groups of eight K otherwise
-            constexpr uint32_t kStepA = (AMN ? 2048 : 32) >> 4, kStepB = (BMN ? 2048 : 32) >> 4;
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, acc_phase = 0;
-            bool ok = true;
-            for (int t = first; t < total && ok; t += step) {
-                const Tile x = tile_at(g, t);
-                int k0, k1;
-                k_range(g, x.split, k0, k1);
-                for (int c = k0; c < k1 && ok; c += kChunk) {
-                    const int end = min(c + kChunk, k1);
-                    ok = wait(&b->acc_empty[buf], acc_phase ^ 1, b, g.timeouts);
-                    tc::fence_after();
-                    for (int k = c; k < end && ok; ++k) {
-                        ok = wait(&b->full[stage], phase, b, g.timeouts);
-                        if (!ok) break;
-                        tc::fence_after();
-                        const uint32_t sa = tc::smem_addr(smem + stage * kStageBytes);
-                        const uint64_t da = tc::operand(sa, AMN ? kHalfBytes / 2 : 16, 1024);
-                        const uint64_t db = tc::operand(sa + kHalfBytes, BMN ? kHalfBytes / 2 : 16, 1024);
-#pragma unroll
-                        for (int j = 0; j < kBlockK / 16; ++j)
-                            tc::mma_pair(tensor + buf * kTileN, da + j * kStepA, db + j * kStepB, idesc,
-                                         k > c || j > 0);
-                        tc::commit_pair(&b->empty[stage]);
-                        if (++stage == kStages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
-                    }
-                    if (!ok) break;
-                    tc::commit_pair(&b->acc_full[buf]);
-                    buf ^= 1;
-                    acc_phase ^= buf == 0;
-                }
-            }
-        }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0 && lane == 0)
+            load_operand<AMN, true>(g, &map_a, smem, b, rank, first, total, step);
+        else if (warp == 3 && lane == 0)
+            load_operand<BMN, false>(g, &map_b, smem + kHalfBytes, b, rank, first, total, step);
+        else if (warp == 1 && rank == 0)
+            issue_products<AMN, BMN>(g, smem, b, tensor, first, total, step);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int quarter = warp % 4, half = (warp - 4) / 4;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int quarter = warp % 4, part = (warp - 4) / 4;
         const StoreBox box{boxes + (warp - 4) * kStoreBytes, lane};
         float scale = 1.0f;
         if constexpr (EP == kScale) scale = g.scale_const * (g.scale != nullptr ? *g.scale : 1.0f);
@@ -402,7 +420,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int k0, k1;
             k_range(g, x.split, k0, k1);
             const int64_t row0 = int64_t(x.m) * kTileM + rank * 128 + quarter * 32;
-            const int64_t col0 = int64_t(x.n) * kTileN + half * kSpan;
+            const int64_t col0 = int64_t(x.n) * kTileN + part * kSpan;
+            int64_t target = -1;  // loaded while the products run
+            if constexpr (EP != kScale) {
+                if (row0 + lane < g.M) target = g.targets[row0 + lane];
+            }
             float v[kSpan];
 #pragma unroll
             for (int j = 0; j < kSpan; ++j) v[j] = 0.0f;
@@ -410,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!(ok = wait(&b->acc_full[buf], acc_phase, b, g.timeouts))) break;
                 tc::fence_after();
                 const uint32_t acc =
-                    tensor + buf * kTileN + half * kSpan + (static_cast<uint32_t>(quarter * 32) << 16);
+                    tensor + buf * kTileN + part * kSpan + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
                 for (int c = 0; c < kSpan; c += 32) {
                     float r[32];
@@ -429,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if constexpr (EP == kScale)
                     scaled_span<DT>(g, &map_out, box, v, row0, col0, x.split, scale);
                 else
-                    softmax_span<EP, DT>(g, &map_out, box, v, row0, col0);
+                    softmax_span<EP, DT>(g, &map_out, box, v, row0, col0, target);
             }
         }
         if (lane == 0) tma::bulk_wait<0>();
@@ -449,8 +471,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int AMN, int BMN, int EP, int DT>
-fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const GemmArgs &g,
+fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, GemmArgs g,
                           cudaStream_t s) {
+    const int32_t blocks = g.kblocks * g.pairs;
+    g.k_each = blocks / g.splits;
+    g.k_more = blocks % g.splits;
     static PerDeviceOnce once;
     const int dev = current_device();
     if (!once.is_done(dev)) {

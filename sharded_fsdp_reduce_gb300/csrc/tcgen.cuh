@@ -39,20 +39,12 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
     return r;
 }
 
+// Arrive on a barrier of either CTA (a shared::cluster address). What it
+// orders are tensor-memory reads that a tcgen05 fence has closed: the CTA
+// scope of the default form is enough, and a cluster-scope release would
+// wait for this thread's global stores.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ---------------------------------------------------------------- tiled TMA
@@ -118,11 +110,12 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 // eight 128-byte rows. `lead` and `stride` in bytes: K-major operands (rows of
 // 64 K elements) use stride between groups of eight rows; MN-major ones (rows
 // of 64 M or N elements) use stride between groups of eight K and lead
-// between blocks of 64 M or N.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
-           (static_cast<uint64_t>(stride >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// between blocks of 64 M or N. The address is in the low word, which is all
+// that changes from one product to the next.
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr, uint32_t lead) {
+    return ((addr & 0x3ffff) >> 4) | ((lead >> 4) << 16);
 }
+constexpr uint32_t operand_high(uint32_t stride) { return (stride >> 4) | (1u << 14) | (2u << 29); }
 
 // Instruction descriptor of kind::f16: fp32 accumulator, operand type 0 (fp16)
 // or 1 (bf16) for both, majorness per operand (1: MN-major).
@@ -133,12 +126,16 @@ constexpr uint32_t instruction(int type, int a_mn, int b_mn, int m, int n) {
 }
 
 // D (+)= A B over K = 16 by the pair; one thread of the even CTA issues it.
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// Operands as the low words of their descriptors; `high` is both's high word.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc,
+                                         bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 x, {%1, %3};\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
         : "memory");
 }
 
@@ -150,6 +147,17 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
             smem_addr(bar)),
         "h"(static_cast<uint16_t>(3))
         : "memory");
+}
+
+// True in one thread of the (whole) warp: always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 }  // namespace tc
