@@ -152,6 +152,8 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     const NormUnit<W> &u = a.u[unit_of(a.u, a.n, blockIdx.x)];
     const int64_t first = (blockIdx.x - u.cta_begin) * (int64_t(8) * kThreads * a.per_thread) - u.lead;
     constexpr int U = chunks_together<NW, GD>();
+    wait_previous();
+    allow_next();
     Pair sum;
     double out_of_range = 0.0;  // what was summed at another scale
     bool any_rare = false;
@@ -263,12 +265,10 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 
 template <int NW, int W, int CAP>
 fsdp_status launch_capacity(const NormArgs<W, CAP> &a, int dtype, unsigned grid, cudaStream_t s) {
-    switch (dtype) {
-        case FSDP_BF16: norm_kernel<NW, FSDP_BF16, W, CAP><<<grid, kThreads, 0, s>>>(a); break;
-        case FSDP_F16: norm_kernel<NW, FSDP_F16, W, CAP><<<grid, kThreads, 0, s>>>(a); break;
-        default: norm_kernel<NW, FSDP_F32, W, CAP><<<grid, kThreads, 0, s>>>(a);
-    }
-    return check_launch();
+    auto kernel = dtype == FSDP_BF16  ? norm_kernel<NW, FSDP_BF16, W, CAP>
+                  : dtype == FSDP_F16 ? norm_kernel<NW, FSDP_F16, W, CAP>
+                                      : norm_kernel<NW, FSDP_F32, W, CAP>;
+    return launch_chained(kernel, grid, kThreads, 0, s, a);
 }
 
 template <int NW, int W> fsdp_status launch(const NormArgs<W> &a, int dtype, int64_t grid, cudaStream_t s) {

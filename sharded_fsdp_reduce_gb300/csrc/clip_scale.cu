@@ -35,12 +35,14 @@ template <int DT> __device__ __forceinline__ void load8(const void *base, int64_
 
 template <int DT, int CAP>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ ScaleArgsOf<CAP> a) {
-    const float f = __fmul_rn(a.scale, coefficient(*a.norm, a.max_norm));
-    if (a.in_place && f == 1.0f) return;
     const int64_t cta = gridDim.x - 1 - blockIdx.x;
     const ScaleUnit &u = a.u[unit_of(a.u, a.n, cta)];
     const int64_t first = (cta - u.cta_begin) * (int64_t(8) * kThreads * kScaleChunks) - u.lead;
     constexpr int kWords = rsa::GradRegs<1, DT>::kWords;
+    wait_previous();
+    allow_next();
+    const float f = __fmul_rn(a.scale, coefficient(*a.norm, a.max_norm));
+    if (a.in_place && f == 1.0f) return;
     uint4 w[kScaleChunks][kWords];
 #pragma unroll
     for (int i = 0; i < kScaleChunks; ++i) {
@@ -72,12 +74,10 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
 
 template <int CAP>
 fsdp_status launch_capacity(const ScaleArgsOf<CAP> &a, int dtype, unsigned grid, cudaStream_t s) {
-    switch (dtype) {
-        case FSDP_BF16: scale_kernel<FSDP_BF16, CAP><<<grid, kThreads, 0, s>>>(a); break;
-        case FSDP_F16: scale_kernel<FSDP_F16, CAP><<<grid, kThreads, 0, s>>>(a); break;
-        default: scale_kernel<FSDP_F32, CAP><<<grid, kThreads, 0, s>>>(a);
-    }
-    return check_launch();
+    auto kernel = dtype == FSDP_BF16  ? scale_kernel<FSDP_BF16, CAP>
+                  : dtype == FSDP_F16 ? scale_kernel<FSDP_F16, CAP>
+                                      : scale_kernel<FSDP_F32, CAP>;
+    return launch_chained(kernel, grid, kThreads, 0, s, a);
 }
 
 }  // namespace

@@ -38,12 +38,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 1 : 3)
     r.out = u.out;
     r.s = a.s;
     if (u.vec && (SPLIT ? block + 256 : j_lo + 8) <= u.numel) {
-        rsa::GradRegs<NW, GD> w;
-#pragma unroll
-        for (int q = 0; q < NW; ++q) rsa::load_grad8<GD, SPLIT>(u.grads[q], j_lo, j_hi, w.w[q]);
+        // the norm pass before this kernel does not touch the state: its loads
+        // need not wait for it
         const float4 p0 = ld_state(u.master + j_lo), p1 = ld_state(u.master + j_hi);
         const float4 m0 = ld_state(u.m + j_lo), m1 = ld_state(u.m + j_hi);
         const float4 v0 = ld_state(u.v + j_lo), v1 = ld_state(u.v + j_hi);
+        wait_previous();
+        allow_next();
+        rsa::GradRegs<NW, GD> w;
+#pragma unroll
+        for (int q = 0; q < NW; ++q) rsa::load_grad8<GD, SPLIT>(u.grads[q], j_lo, j_hi, w.w[q]);
         r.s.c = coefficient(*a.norm, a.max_norm);
         float acc[8];
         rsa::widen8<GD>(w.w[0], acc);
@@ -60,6 +64,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 1 : 3)
         return;
     }
     // elements after the last whole chunk, and units off 16 bytes
+    wait_previous();
+    allow_next();
     const float coef = coefficient(*a.norm, a.max_norm);
     for (int e = 0; e < 8; ++e) {
         const int64_t j = SPLIT ? block + 32 * e + threadIdx.x % 32 : j_lo + e;
@@ -78,12 +84,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 1 : 3)
 
 template <int NW, int GD, bool SPLIT, int CAP>
 fsdp_status launch_capacity(const UpdateArgsOf<CAP> &a, int out_dtype, unsigned grid, cudaStream_t s) {
-    switch (out_dtype) {
-        case FSDP_BF16: update_kernel<NW, GD, FSDP_BF16, SPLIT, CAP><<<grid, kThreads, 0, s>>>(a); break;
-        case FSDP_F16: update_kernel<NW, GD, FSDP_F16, SPLIT, CAP><<<grid, kThreads, 0, s>>>(a); break;
-        default: update_kernel<NW, GD, FSDP_F32, SPLIT, CAP><<<grid, kThreads, 0, s>>>(a);
-    }
-    return check_launch();
+    auto kernel = out_dtype == FSDP_BF16  ? update_kernel<NW, GD, FSDP_BF16, SPLIT, CAP>
+                  : out_dtype == FSDP_F16 ? update_kernel<NW, GD, FSDP_F16, SPLIT, CAP>
+                                          : update_kernel<NW, GD, FSDP_F32, SPLIT, CAP>;
+    return launch_chained(kernel, grid, kThreads, 0, s, a);
 }
 
 template <int NW, int GD, bool SPLIT>

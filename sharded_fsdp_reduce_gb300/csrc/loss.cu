@@ -60,60 +60,96 @@ __device__ long long warp_sum(long long x) {
     return x;
 }
 
-// 32 rows per block: lane = row, the warps share the row's spans. The
-// statistics lie span by span, so a warp's reads are contiguous. The loss
-// adds up per block, then over the blocks in one fixed order, in fp64.
+// (top, sum): sum * 2^top. Joins another pair into it.
+__device__ __forceinline__ void join(float &top, float &sum, float other_top, float other_sum) {
+    const float most = fmaxf(top, other_top);
+    if (most == -INFINITY) return;  // both empty
+    sum = sum * exp2f(top - most) + other_sum * exp2f(other_top - most);
+    top = most;
+}
+
+constexpr int kRows = 16;     // of a block
+constexpr int kRowLoads = 8;  // spans a thread reads at once
+
+// 16 rows per block of 1024 threads: a warp reads two spans of the 16 rows at
+// a time (the statistics lie span by span), the 64 readers of a row share its
+// spans. Latency-bound: 2 x 4 bytes per span and row, eight loads in flight
+// per thread. The loss adds up per block, then over the blocks in one fixed
+// order, in fp64.
 __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowArgs a) {
-    __shared__ float tops[32][33], sums[32][33];
+    __shared__ float tops[32][kRows + 1], sums[32][kRows + 1];
     __shared__ double total[32];
     __shared__ long long count[32];
     __shared__ bool last;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t row = int64_t(blockIdx.x) * 32 + lane;
-    const bool live = row < a.rows;
-    float top = -INFINITY, sum = 0.0f;
-    if (live) {
-        for (int s = warp; s < a.spans; s += 32) {
-            const float o = a.off[s * a.ld_rows + row], x = a.sum[s * a.ld_rows + row];
-            if (o > top) {
-                sum = sum * exp2f(top - o) + x;
-                top = o;
-            } else {
-                sum += x * exp2f(o - top);
+    wait_previous();
+    allow_next();
+    {
+        const int64_t row = int64_t(blockIdx.x) * kRows + lane % kRows;
+        float top = -INFINITY, sum = 0.0f;
+        if (row < a.rows) {
+            const float *off = a.off + row, *part = a.sum + row;
+            for (int s = threadIdx.x / kRows; s < a.spans; s += 1024 / kRows * kRowLoads) {
+                float o[kRowLoads], x[kRowLoads];
+#pragma unroll
+                for (int i = 0; i < kRowLoads; ++i) {
+                    const int at = s + 1024 / kRows * i;
+                    o[i] = at < a.spans ? off[at * a.ld_rows] : -INFINITY;
+                    x[i] = at < a.spans ? part[at * a.ld_rows] : 0.0f;
+                }
+                float most = top;
+#pragma unroll
+                for (int i = 0; i < kRowLoads; ++i) most = fmaxf(most, o[i]);
+                sum *= exp2f(top - most);
+#pragma unroll
+                for (int i = 0; i < kRowLoads; ++i) sum += x[i] * exp2f(o[i] - most);
+                top = most;
             }
+        }
+        join(top, sum, __shfl_xor_sync(0xffffffffu, top, kRows), __shfl_xor_sync(0xffffffffu, sum, kRows));
+        if (lane < kRows) {
+            tops[warp][lane] = top;
+            sums[warp][lane] = sum;
         }
     }
-    tops[warp][lane] = top;
-    sums[warp][lane] = sum;
     __syncthreads();
-    if (warp == 0) {
+    if (warp < kRows) {  // a warp per row
+        const int64_t row = int64_t(blockIdx.x) * kRows + warp;
+        float top = tops[lane][warp], sum = sums[lane][warp];
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            join(top, sum, __shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o));
+        if (lane == 0) {
+            float t = 0.0f;
+            long long valid = 0;
+            if (row < a.rows) {
+                const float lse2 = top + log2f(sum);
+                a.lse2[row] = lse2;
+                const int64_t y = a.targets[row];
+                if (y != a.ignore) {
+                    valid = 1;
+                    // a target outside the vocabulary has no loss: it shows as NaN
+                    t = y >= 0 && y < a.vocab ? lse2 * kLn2 - a.target_logit[row] : NAN;
+                }
+                if (a.token_loss != nullptr) a.token_loss[row] = t;
+            }
+            total[warp] = t;
+            count[warp] = valid;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
         double loss = 0.0;
         long long valid = 0;
-        if (live) {
-            for (int w = 1; w < 32; ++w) top = fmaxf(top, tops[w][lane]);
-            float all = 0.0f;
-            for (int w = 0; w < 32; ++w)
-                if (w < a.spans) all += sums[w][lane] * exp2f(tops[w][lane] - top);
-            const float lse2 = top + log2f(all);
-            a.lse2[row] = lse2;
-            const int64_t y = a.targets[row];
-            float t = 0.0f;
-            if (y != a.ignore) {
-                valid = 1;
-                // a target outside the vocabulary has no loss: it shows as NaN
-                t = y >= 0 && y < a.vocab ? lse2 * kLn2 - a.target_logit[row] : NAN;
-            }
-            if (a.token_loss != nullptr) a.token_loss[row] = t;
-            loss = t;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            loss += total[r];
+            valid += count[r];
         }
-        loss = warp_sum(loss);
-        valid = warp_sum(valid);
-        if (lane == 0) {
-            a.part_sum[a.first_block + blockIdx.x] = loss;
-            a.part_count[a.first_block + blockIdx.x] = valid;
-            __threadfence();
-            last = atomicAdd(a.ticket, 1u) + 1 == static_cast<uint32_t>(a.all_blocks);
-        }
+        a.part_sum[a.first_block + blockIdx.x] = loss;
+        a.part_count[a.first_block + blockIdx.x] = valid;
+        __threadfence();
+        last = atomicAdd(a.ticket, 1u) + 1 == static_cast<uint32_t>(a.all_blocks);
     }
     __syncthreads();
     if (!last) return;
@@ -147,6 +183,8 @@ __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowA
 __global__ void __launch_bounds__(1024)
     count_kernel(const int64_t *targets, int64_t rows, int64_t ignore, float grad_scale, int mean, float *scale) {
     __shared__ long long count[32];
+    wait_previous();
+    allow_next();
     long long n = 0;
     for (int64_t i = threadIdx.x; i < rows; i += 1024) n += targets[i] != ignore;
     n = warp_sum(n);
@@ -169,7 +207,7 @@ struct GradArgs {
     const float *lse2;
     const int64_t *targets;
     int64_t ignore;
-    uint32_t col_blocks;
+    uint32_t row_blocks;
 };
 
 // x in three bf16 parts: each takes the next 8 bits.
@@ -187,9 +225,13 @@ constexpr int kGradCols = 512, kGradRows = 64;
 template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __grid_constant__ GradArgs a) {
     __shared__ float factor[kGradCols / kSpan][kGradRows];
     __shared__ int32_t hit[kGradRows];  // the target's column in this block, or -1; -2: no gradient
-    const int64_t row0 = int64_t(blockIdx.x / a.col_blocks) * kGradRows;
-    const int64_t col0 = int64_t(blockIdx.x % a.col_blocks) * kGradCols;
+    // from the last columns to the first, as the logits product left them in L2
+    const uint32_t block = gridDim.x - 1 - blockIdx.x;
+    const int64_t row0 = int64_t(block % a.row_blocks) * kGradRows;
+    const int64_t col0 = int64_t(block / a.row_blocks) * kGradCols;
     constexpr float kGain = DT == FSDP_F16 ? kHalfGain : 1.0f;
+    wait_previous();
+    allow_next();
     for (int i = threadIdx.x; i < kGradRows * (kGradCols / kSpan); i += 256) {
         const int r = i % kGradRows, s = i / kGradRows;
         const int64_t row = row0 + r, span = col0 / kSpan + s;
@@ -254,6 +296,8 @@ template <bool F32>
 __global__ void __launch_bounds__(256) pack_kernel(const void *src, int64_t rows, int64_t cols, int64_t ld,
                                                    uint16_t *dst, int64_t ldp, int64_t plane) {
     const int64_t words = ldp / 8, total = rows * words;
+    wait_previous();
+    allow_next();
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
         const int64_t r = i / words, c = (i - r * words) * 8;
         const int n = static_cast<int>(min(int64_t(8), cols - c));
@@ -287,6 +331,8 @@ template <int DT>
 __global__ void __launch_bounds__(256) join_kernel(const float *part, int splits, int64_t split_stride, int64_t rows,
                                                    int64_t cols, int64_t ldp, const float *scale, float scale_const,
                                                    void *out, int64_t ld) {
+    wait_previous();
+    allow_next();
     const float f = scale_const * *scale;
     const int64_t words = ldp / 4, total = rows * words;
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
@@ -338,6 +384,12 @@ int choose_splits(int64_t tiles, int64_t kblocks, int64_t m, int64_t n) {
     return best;
 }
 
+// The power of two, at most 32, that an address and a stride in bytes are multiples of.
+int32_t alignment(const void *p, int64_t stride) {
+    const uintptr_t both = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride) | 32;
+    return static_cast<int32_t>(both & -both);
+}
+
 bool direct(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
 Plan make_plan(const fsdp_head_loss_args &a) {
@@ -365,7 +417,7 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     p.blocks = 0;
     for (int64_t b = 0; b < p.bands; ++b) {
         const int64_t rows = a.tokens - b * p.band < p.band ? a.tokens - b * p.band : p.band;
-        p.blocks += ceil_div(rows, 32);
+        p.blocks += ceil_div(rows, kRows);
     }
     p.splits_x = p.splits_w = 1;
     const int64_t pairs = p.f32 ? 6 : 1;
@@ -426,27 +478,23 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// Rows of `cols` elements at stride ld, `planes` of them; boxes of 128 bytes
-// by box_rows, 128-byte swizzle, zeros outside.
-fsdp_status make_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, int64_t cols,
-                     int64_t rows, int64_t planes, int64_t ld, int64_t plane, int box_rows) {
+// Rows of `cols` elements at stride ld, `planes` of them; boxes of box_bytes
+// (128, or 64) by box_rows, swizzled over as many bytes, zeros outside.
+fsdp_status make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t cols, int64_t rows,
+                     int64_t planes, int64_t ld, int64_t plane, int box_rows, int box_bytes = 128) {
     const EncodeFn fn = encode_fn();
     if (!fn) return cuda_status(cudaErrorNotSupported);
+    const int size = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(planes)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * size), static_cast<cuuint64_t>(plane * size)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / size), static_cast<cuuint32_t>(box_rows), 1};
     const cuuint32_t unit[3] = {1, 1, 1};
     const CUresult r = fn(map, type, 3, const_cast<void *>(base), dims, strides, box, unit,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FSDP_OK : cuda_status(cudaErrorInvalidValue);
-}
-
-CUtensorMapDataType map_type(int dtype) {
-    return dtype == FSDP_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-           : dtype == FSDP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
 int grid_of(int64_t items) {
@@ -467,19 +515,16 @@ fsdp_status pack(const void *src, bool f32, int64_t rows, int64_t cols, int64_t 
                  cudaStream_t s) {
     const int grid = grid_of(rows * ldp / 8);
     uint16_t *d = reinterpret_cast<uint16_t *>(dst);
-    if (f32)
-        pack_kernel<true><<<grid, 256, 0, s>>>(src, rows, cols, ld, d, ldp, rows * ldp);
-    else
-        pack_kernel<false><<<grid, 256, 0, s>>>(src, rows, cols, ld, d, ldp, rows * ldp);
-    return check_launch();
+    return launch_chained(f32 ? pack_kernel<true> : pack_kernel<false>, static_cast<unsigned>(grid), 256, 0, s, src,
+                          rows, cols, ld, d, ldp, rows * ldp);
 }
 
-fsdp_status launch_grad(int dtype, Orders o, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
-                        const GemmArgs &g, cudaStream_t s) {
+fsdp_status launch_grad(int dtype, Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g,
+                        cudaStream_t s) {
     switch (dtype) {
-        case FSDP_BF16: return launch_grad_bf16(o, a, b, out, g, s);
-        case FSDP_F16: return launch_grad_f16(o, a, b, out, g, s);
-        default: return launch_grad_f32(o, a, b, out, g, s);
+        case FSDP_BF16: return launch_grad_bf16(o, a, b, g, s);
+        case FSDP_F16: return launch_grad_f16(o, a, b, g, s);
+        default: return launch_grad_f32(o, a, b, g, s);
     }
 }
 
@@ -515,30 +560,21 @@ fsdp_status run_product(const Product &q, const Plan &p, const fsdp_head_loss_ar
     const float *scale = reinterpret_cast<const float *>(ws + p.scale);
     const float gain = a.dtype == FSDP_F16 ? 1.0f / kHalfGain : 1.0f;
     g.timeouts = a.wait_timeouts;
-    CUtensorMap mo = ma;  // unused without TMA stores
     if (q.splits > 1) {
         g.scale_const = 1.0f;
-        g.tma_store = 1;
         float *part = reinterpret_cast<float *>(ws + p.part);
-        fsdp_status st = make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, part, q.N, q.M, q.splits, p.ldd,
-                                  q.M * p.ldd, 32);
-        if (st == FSDP_OK) st = launch_grad_f32(q.orders, ma, mb, mo, g, s);
+        g.out = part;
+        g.ld_out = g.store_cols = p.ldd;
+        g.split_stride = q.M * p.ldd;
+        g.store_bytes = 32;
+        const fsdp_status st = launch_grad_f32(q.orders, ma, mb, g, s);
         if (st != FSDP_OK) return st;
-        const int grid = grid_of(q.M * p.ldd / 4);
-        switch (q.out_dtype) {
-            case FSDP_BF16:
-                join_kernel<FSDP_BF16><<<grid, 256, 0, s>>>(part, q.splits, q.M * p.ldd, q.M, q.N, p.ldd, scale, gain,
-                                                            q.out, q.ld_out);
-                break;
-            case FSDP_F16:
-                join_kernel<FSDP_F16><<<grid, 256, 0, s>>>(part, q.splits, q.M * p.ldd, q.M, q.N, p.ldd, scale, gain,
-                                                           q.out, q.ld_out);
-                break;
-            default:
-                join_kernel<FSDP_F32><<<grid, 256, 0, s>>>(part, q.splits, q.M * p.ldd, q.M, q.N, p.ldd, scale, gain,
-                                                           q.out, q.ld_out);
-        }
-        return check_launch();
+        auto join = q.out_dtype == FSDP_BF16  ? join_kernel<FSDP_BF16>
+                    : q.out_dtype == FSDP_F16 ? join_kernel<FSDP_F16>
+                                              : join_kernel<FSDP_F32>;
+        return launch_chained(join, static_cast<unsigned>(grid_of(q.M * p.ldd / 4)), 256, 0, s,
+                              static_cast<const float *>(part), q.splits, q.M * p.ldd, q.M, q.N, p.ldd, scale, gain,
+                              q.out, q.ld_out);
     }
     g.scale = q.scaled ? scale : nullptr;
     g.scale_const = q.scaled ? gain : 1.0f;
@@ -546,14 +582,9 @@ fsdp_status run_product(const Product &q, const Plan &p, const fsdp_head_loss_ar
     g.ld_earlier = q.ld_earlier;
     g.out = q.out;
     g.ld_out = q.ld_out;
-    const int size = dtype_size(q.out_dtype);
-    g.tma_store = aligned(q.out, 16) && q.ld_out * size % 16 == 0;
-    if (g.tma_store) {
-        const fsdp_status st =
-            make_map(&mo, map_type(q.out_dtype), size, q.out, q.N, q.M, 1, q.ld_out, q.M * q.ld_out, 32);
-        if (st != FSDP_OK) return st;
-    }
-    return launch_grad(q.out_dtype, q.orders, ma, mb, mo, g, s);
+    g.store_cols = q.N;
+    g.store_bytes = alignment(q.out, q.ld_out * dtype_size(q.out_dtype));
+    return launch_grad(q.out_dtype, q.orders, ma, mb, g, s);
 }
 
 fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaStream_t s) {
@@ -574,15 +605,15 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
     if (st != FSDP_OK) return st;
     float *scale = reinterpret_cast<float *>(ws + p.scale);
     if (p.grad && p.bands > 1) {
-        count_kernel<<<1, 1024, 0, s>>>(a.targets, a.tokens, a.ignore_index, a.grad_scale,
-                                        a.reduction == FSDP_LOSS_MEAN, scale);
-        if ((st = check_launch()) != FSDP_OK) return st;
+        st = launch_chained(count_kernel, 1, 1024, 0, s, a.targets, a.tokens, a.ignore_index, a.grad_scale,
+                            static_cast<int>(a.reduction == FSDP_LOSS_MEAN), scale);
+        if (st != FSDP_OK) return st;
     }
     const CUtensorMapDataType t16 =
         a.dtype == FSDP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap w_k, w_n;
-    st = make_map(&w_k, t16, 2, w.base, D, V, w.planes, w.ld, w.plane, 128);
-    if (st == FSDP_OK) st = make_map(&w_n, t16, 2, w.base, D, V, w.planes, w.ld, w.plane, 64);
+    st = make_map(&w_k, t16, w.base, D, V, w.planes, w.ld, w.plane, 128);
+    if (st == FSDP_OK) st = make_map(&w_n, t16, w.base, D, V, w.planes, w.ld, w.plane, 64);
     if (st != FSDP_OK) return st;
     int64_t block = 0;
     for (int64_t b = 0; b < p.bands; ++b) {
@@ -590,7 +621,7 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         const int64_t rows = a.tokens - row0 < p.band ? a.tokens - row0 : p.band;
         const uint8_t *xb = x.base + 2 * row0 * x.ld;
         CUtensorMap x_k, x_n, e_out;
-        st = make_map(&x_k, t16, 2, xb, D, rows, x.planes, x.ld, x.plane, 128);
+        st = make_map(&x_k, t16, xb, D, rows, x.planes, x.ld, x.plane, 128);
         if (st != FSDP_OK) return st;
         // the logits, as statistics and exponentials
         GemmArgs g;
@@ -610,17 +641,13 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         g.sum = reinterpret_cast<float *>(ws + p.sum);
         g.target_logit = reinterpret_cast<float *>(ws + p.target_logit);
         g.ld_rows = p.band;
-        g.tma_store = 1;
         g.ticket = b == 0 ? reinterpret_cast<uint32_t *>(ws + p.ticket) : nullptr;
         g.timeouts = a.wait_timeouts;
+        e_out = x_k;
         if (p.grad) {
-            st = p.f32 ? make_map(&e_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ws + p.e, V, rows, 1, p.ldv,
-                                  rows * p.ldv, 32)
-                       : make_map(&e_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ws + p.e, V, rows, 1, p.ldv,
-                                  rows * p.ldv, 32);
+            st = make_map(&e_out, p.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + p.e,
+                          p.ldv, rows, 1, p.ldv, rows * p.ldv, 32, 64);
             if (st != FSDP_OK) return st;
-        } else {
-            e_out = x_k;
         }
         st = launch_logits(p.grad ? kExp : kStats, p.f32, x_k, w_k, e_out, g, s);
         if (st != FSDP_OK) return st;
@@ -646,10 +673,9 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         r.scale = scale;
         r.grad_scale = a.grad_scale;
         r.mean = a.reduction == FSDP_LOSS_MEAN;
-        const unsigned nblocks = static_cast<unsigned>(ceil_div(rows, 32));
-        rows_kernel<<<nblocks, 1024, 0, s>>>(r);
+        const unsigned nblocks = static_cast<unsigned>(ceil_div(rows, kRows));
+        if ((st = launch_chained(rows_kernel, nblocks, 1024, 0, s, r)) != FSDP_OK) return st;
         block += nblocks;
-        if ((st = check_launch()) != FSDP_OK) return st;
         if (!p.grad) continue;
         // d, then the two products
         GradArgs d;
@@ -666,19 +692,17 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         d.lse2 = r.lse2;
         d.targets = g.targets;
         d.ignore = a.ignore_index;
-        d.col_blocks = static_cast<uint32_t>(ceil_div(V, kGradCols));
-        const int64_t all = ceil_div(rows, kGradRows) * d.col_blocks;
+        d.row_blocks = static_cast<uint32_t>(ceil_div(rows, kGradRows));
+        const int64_t all = ceil_div(V, kGradCols) * d.row_blocks;
         if (all > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
         const unsigned dgrid = static_cast<unsigned>(all);
-        switch (a.dtype) {
-            case FSDP_BF16: grad_kernel<FSDP_BF16><<<dgrid, 256, 0, s>>>(d); break;
-            case FSDP_F16: grad_kernel<FSDP_F16><<<dgrid, 256, 0, s>>>(d); break;
-            default: grad_kernel<FSDP_F32><<<dgrid, 256, 0, s>>>(d);
-        }
-        if ((st = check_launch()) != FSDP_OK) return st;
+        auto grad = a.dtype == FSDP_BF16  ? grad_kernel<FSDP_BF16>
+                    : a.dtype == FSDP_F16 ? grad_kernel<FSDP_F16>
+                                          : grad_kernel<FSDP_F32>;
+        if ((st = launch_chained(grad, dgrid, 256, 0, s, d)) != FSDP_OK) return st;
         if (a.d_hidden) {
             CUtensorMap d_k;
-            st = make_map(&d_k, t16, 2, ws + p.d, V, rows, planes, p.ldv, plane, 128);
+            st = make_map(&d_k, t16, ws + p.d, V, rows, planes, p.ldv, plane, 128);
             if (st != FSDP_OK) return st;
             const Product q{kHiddenGrad, rows, D, V, p.splits_x, nullptr, 0,
                             static_cast<uint8_t *>(a.d_hidden) + row0 * a.ld_d_hidden * size, a.ld_d_hidden,
@@ -687,8 +711,8 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         }
         if (a.d_weight) {
             CUtensorMap d_m;
-            st = make_map(&d_m, t16, 2, ws + p.d, V, rows, planes, p.ldv, plane, 64);
-            if (st == FSDP_OK) st = make_map(&x_n, t16, 2, xb, D, rows, x.planes, x.ld, x.plane, 64);
+            st = make_map(&d_m, t16, ws + p.d, V, rows, planes, p.ldv, plane, 64);
+            if (st == FSDP_OK) st = make_map(&x_n, t16, xb, D, rows, x.planes, x.ld, x.plane, 64);
             if (st != FSDP_OK) return st;
             float *sum_w = reinterpret_cast<float *>(ws + p.sum_w);
             const bool last = b + 1 == p.bands;

@@ -45,23 +45,22 @@ struct GemmArgs {
     float scale_const;     // and this constant factor
     const float *earlier;  // fp32 [M][ld_earlier] added to the accumulator, or NULL
     int64_t ld_earlier;
-    int32_t tma_store;     // 1: through the output map, 0: element stores to out
     void *out;
-    int64_t ld_out;
+    int64_t ld_out, split_stride;
+    int64_t store_cols;    // columns that may be written (the padding of workspace rows among them)
+    int32_t store_bytes;   // 32, 16, or less: what out's base and stride are multiples of
     uint32_t *ticket;      // kStats, kExp: cleared for the row kernel that follows (or NULL)
     uint32_t *timeouts;
 };
 
 
 // One translation unit per output dtype of the gradients, and one for the logits.
-fsdp_status launch_logits(Epilogue ep, bool f32, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
-                          const GemmArgs &g, cudaStream_t s);
-fsdp_status launch_grad_bf16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
-                             const GemmArgs &g, cudaStream_t s);
-fsdp_status launch_grad_f16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
-                            const GemmArgs &g, cudaStream_t s);
-fsdp_status launch_grad_f32(Orders o, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
-                            const GemmArgs &g, cudaStream_t s);
+// `exponentials`: where they go (used with kExp).
+fsdp_status launch_logits(Epilogue ep, bool f32, const CUtensorMap &a, const CUtensorMap &b,
+                          const CUtensorMap &exponentials, const GemmArgs &g, cudaStream_t s);
+fsdp_status launch_grad_bf16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
+fsdp_status launch_grad_f16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
+fsdp_status launch_grad_f32(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
 
 }  // namespace loss
 }  // namespace fsdp

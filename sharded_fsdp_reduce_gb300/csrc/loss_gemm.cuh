@@ -8,7 +8,7 @@
 //
 // A pair of CTAs (one cluster) works on a 256 x 256 tile of the result: each
 // loads 128 rows of A and 128 of B per 64-wide K block by TMA (32 KB a stage,
-// five stages), the even CTA issues the tcgen05 products for both (M = N = 256,
+// five or six stages), the even CTA issues the tcgen05 products for both (M = N = 256,
 // K = 16), and each CTA's tensor memory holds 128 rows of the accumulator in
 // fp32, twice (2 x 256 columns): the epilogue of one tile runs while the next
 // one's products are issued. The pair shape halves the operand bytes that
@@ -32,8 +32,6 @@
 
 #include <float.h>
 
-#include <type_traits>
-
 #include "loss.cuh"
 #include "tcgen.cuh"
 
@@ -42,27 +40,36 @@ namespace loss {
 
 constexpr int kThreads = 640;
 constexpr int kEpilogueWarps = 16;
-constexpr int kStages = 5;
+// Stages of operands in shared memory. More would fit (6 and 7), and take a
+// little off products of few tiles, but cost long ones: 4096 x 128000 x 8192
+// with its gradients 15.7 ms with these, 15.9 with one more each; the hidden
+// gradient of 1021 x 50257 x 768 wants 6 (54 against 57 us with 5).
+constexpr int stages(int epilogue) { return epilogue == kExp ? 5 : 6; }
+constexpr int kMaxStages = 6;
 // K blocks summed in tensor memory before the sum moves to registers. The
 // tensor cores' own sum loses bits at every K = 16 (a chain of 5120 / 16 adds
 // left a loss 2.4e-6 off, 64 bits against it); chains of 512 / 16 joined by
-// rounded fp32 adds do not show.
-constexpr int kChunk = 8;
+// rounded fp32 adds do not show in fp32 results, chains of 2048 / 16 not in
+// 16-bit ones. Each move costs the products about 1 %.
+constexpr int chunk_blocks(int epilogue, int dtype) { return epilogue == kScale && dtype != FSDP_F32 ? 32 : 8; }
 constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // one operand's half tile: 16 KB
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;         // per CTA
-constexpr uint32_t kStoreBytes = 32 * 128;               // one warp's store box: 32 rows of 128 bytes
 constexpr uint32_t kTensorCols = 512;                    // two accumulators of 256 columns
 constexpr long long kWaitCycles = 2000000000ll;          // about one second of SM clocks
 
 struct Barriers {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tensor_base;
     int32_t gave_up;
 };
 
-constexpr size_t kSmemBytes =
-    1024 + kStages * kStageBytes + kEpilogueWarps * kStoreBytes + sizeof(Barriers);
+constexpr uint32_t kBoxBytes = 32 * 64;                  // one warp's store box: 32 rows of 64 bytes
+constexpr size_t smem_bytes(int epilogue) {
+    return 1024 + stages(epilogue) * kStageBytes + (epilogue == kExp ? kEpilogueWarps * kBoxBytes : 0) +
+           sizeof(Barriers);
+}
+static_assert(smem_bytes(kExp) <= 232448 && smem_bytes(kScale) <= 232448, "shared memory of one block");
 
 // The (A, B) planes of the six pairs, low nibble first, smallest products first.
 constexpr uint32_t kPlanesA = 0x001021, kPlanesB = 0x010201;
@@ -114,69 +121,69 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// One warp's 32 x (128 bytes) store box in swizzled shared memory.
-struct StoreBox {
-    uint8_t *smem;
-    int lane;
+// One row's 64 values (a thread's) to a gradient, rounded to DT: each thread
+// writes 128 or 256 contiguous bytes, in the widest stores that the result's
+// base and stride allow. Straight from registers: a gradient's tile is
+// written once in many K blocks, at any alignment.
+__device__ __forceinline__ void store32(void *p, uint4 a, uint4 b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
 
-    // before writing: the last store has read the box
-    __device__ __forceinline__ void open(bool tma_store) const {
-        if (tma_store && lane == 0) tma::bulk_wait_read<0>();
-        __syncwarp();
-    }
-    // 16 bytes at chunk c (0..7) of this lane's row
-    __device__ __forceinline__ void put(int c, uint4 v) const {
-        *reinterpret_cast<uint4 *>(smem + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
-    }
-    template <class T> __device__ __forceinline__ T get(int row, int e) const {
-        const int byte = e * static_cast<int>(sizeof(T));
-        return *reinterpret_cast<const T *>(smem + row * 128 + ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 15)));
-    }
-};
+template <int DT> __device__ __forceinline__ uint4 pack16(const float *v) {
+    if constexpr (DT == FSDP_F32)
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    else
+        return make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
+}
 
-// The columns from c0 of a box: 64 (16-bit types) or 32 (fp32) of a row's values.
-template <int DT> __device__ __forceinline__ void put_row(const StoreBox &box, const float *v) {
-    if constexpr (DT == FSDP_F32) {
+template <int DT>
+__device__ __forceinline__ void store_span(const GemmArgs &g, int64_t row, int64_t col0, int split, const float *v) {
+    if (row >= g.M) return;
+    constexpr int kSize = Dtype<DT>::kSize, kPer16 = 16 / kSize;
+    const int64_t at = split * g.split_stride + row * g.ld_out + col0;
+    uint8_t *out = static_cast<uint8_t *>(g.out) + at * kSize;
+    if (g.store_bytes == 32 && col0 + kSpan <= g.store_cols) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            box.put(i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                  __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
-    } else {
+        for (int j = 0; j < kSpan; j += 2 * kPer16)
+            store32(out + j * kSize, pack16<DT>(v + j), pack16<DT>(v + j + kPer16));
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            box.put(i, make_uint4(pack2<DT>(v[8 * i], v[8 * i + 1]), pack2<DT>(v[8 * i + 2], v[8 * i + 3]),
-                                  pack2<DT>(v[8 * i + 4], v[8 * i + 5]), pack2<DT>(v[8 * i + 6], v[8 * i + 7])));
+    for (int j = 0; j < kSpan; j += kPer16) {
+        if (g.store_bytes >= 16 && col0 + j + kPer16 <= g.store_cols) {
+            *reinterpret_cast<uint4 *>(out + j * kSize) = pack16<DT>(v + j);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPer16; ++e)
+                if (col0 + j + e < g.store_cols) Dtype<DT>::store(out, j + e, v[j + e]);
+        }
     }
 }
 
-// Store one warp's 32 rows x 64 columns, box by box; z: the plane or split.
+// One warp's 32 rows x 64 columns of exponentials, by TMA from a small box in
+// shared memory (64-byte rows, 64-byte swizzle), part after part: written on
+// every tile of few K blocks, stores from registers took 67 us where this
+// takes 60 (1021 x 50257 x 768).
 template <int DT>
-__device__ __forceinline__ void store_span(const StoreBox &box, const CUtensorMap *map, const GemmArgs &g,
-                                           bool tma_store, int64_t row0, int64_t col0, int z, const float *v) {
-    constexpr int kCols = 128 / Dtype<DT>::kSize;
+__device__ __forceinline__ void store_exponentials(const CUtensorMap *map, uint8_t *box, int lane, int64_t row0,
+                                                   int64_t col0, const float *v) {
+    constexpr int kPer16 = 16 / Dtype<DT>::kSize, kCols = 4 * kPer16;
+    uint8_t *row = box + lane * 64;
+    const int turn = (lane >> 1) & 3;
 #pragma unroll
     for (int c = 0; c < kSpan; c += kCols) {
-        if (col0 + c >= g.N) break;
-        box.open(tma_store);
-        put_row<DT>(box, v + c);
-        if (tma_store) {
-            tma::fence_proxy_async_smem();
-            __syncwarp();
-            if (box.lane == 0) {
-                tc::store_tile(map, static_cast<int>(col0 + c), static_cast<int>(row0), z, box.smem);
-                tma::bulk_commit();
-            }
-        } else {
-            // outputs whose rows TMA cannot address (base or stride off 16 bytes)
-            __syncwarp();
-            using T = typename std::conditional<DT == FSDP_F32, uint32_t, uint16_t>::type;
-            const int rows = static_cast<int>(min(int64_t(32), g.M - row0));
-            for (int r = 0; r < rows; ++r) {
-                T *out = static_cast<T *>(g.out) + (row0 + r) * g.ld_out + col0 + c;
+        if (lane == 0) tma::bulk_wait_read<0>();  // the last store has read the box
+        __syncwarp();
 #pragma unroll
-                for (int e = box.lane; e < kCols; e += 32)
-                    if (col0 + c + e < g.N) out[e] = box.get<T>(r, e);
-            }
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(row + ((i ^ turn) << 4)) = pack16<DT>(v + c + i * kPer16);
+        tma::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tc::store_tile(map, static_cast<int>(col0 + c), static_cast<int>(row0), 0, box);
+            tma::bulk_commit();
         }
     }
 }
@@ -186,10 +193,10 @@ __device__ __forceinline__ void store_span(const StoreBox &box, const CUtensorMa
 // max(l2) - 15: at most 2^15, so that fp16 holds them with 11 bits down to
 // 2^-29 of the span's largest (what is smaller is below 2^-40 of it).
 template <int EP, int DT>
-__device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMap *map, const StoreBox &box,
+__device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMap *map, uint8_t *box, int lane,
                                              float *v, int64_t row0, int64_t col0, int64_t target) {
     constexpr float kLog2e = 1.44269504088896340736f;
-    const int64_t row = row0 + box.lane;
+    const int64_t row = row0 + lane;
     const bool live = row < g.M;
     const int64_t at = target - col0;
     if (at >= 0 && at < kSpan && at + col0 < g.N) {
@@ -227,14 +234,13 @@ __device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMa
         g.off[to] = off;
         g.sum[to] = (s0 + s1) + (s2 + s3);
     }
-    if constexpr (EP == kExp) store_span<DT>(box, map, g, true, row0, col0, 0, v);
+    if constexpr (EP == kExp) store_exponentials<DT>(map, box, lane, row0, col0, v);
 }
 
 // scale * (accumulator + earlier) of one warp's 32 rows x 64 columns.
 template <int DT>
-__device__ __forceinline__ void scaled_span(const GemmArgs &g, const CUtensorMap *map, const StoreBox &box,
-                                            float *v, int64_t row0, int64_t col0, int split, float scale) {
-    const int64_t row = row0 + box.lane;
+__device__ __forceinline__ void scaled_span(const GemmArgs &g, float *v, int64_t row, int64_t col0, int split,
+                                            float scale) {
     if (g.earlier != nullptr && row < g.M) {
         const float *e = g.earlier + row * g.ld_earlier + col0;  // 16-byte aligned, padded to 64 columns
 #pragma unroll
@@ -250,14 +256,14 @@ __device__ __forceinline__ void scaled_span(const GemmArgs &g, const CUtensorMap
     }
 #pragma unroll
     for (int j = 0; j < kSpan; ++j) v[j] *= scale;
-    store_span<DT>(box, map, g, g.tma_store != 0, row0, col0, split, v);
+    store_span<DT>(g, row, col0, split, v);
 }
 
 // One operand's loads, by one thread of each CTA: its 128 rows of every K
 // block of every tile, into the stages in turn. Each operand has a thread of
 // its own: one thread that issued both (and divided to find its place) took
 // 830 cycles a K block, the products 512.
-template <int MN, bool A>
+template <int MN, bool A, int kStages>
 __device__ __forceinline__ void load_operand(const GemmArgs &g, const CUtensorMap *map, uint8_t *smem, Barriers *b,
                                              uint32_t rank, int first, int total, int step) {
     const uint32_t full = tc::peer_addr(tc::smem_addr(&b->full[0]), 0);
@@ -310,7 +316,7 @@ __device__ __forceinline__ void load_operand(const GemmArgs &g, const CUtensorMa
 // whole warp runs the loop and one elected thread issues: what it issues with
 // then stays in uniform registers (a single thread's loop moved every operand
 // there first, 560 cycles a K block against the products' 512).
-template <int AMN, int BMN>
+template <int AMN, int BMN, int kStages, int kChunk>
 __device__ __forceinline__ void issue_products(const GemmArgs &g, uint8_t *smem, Barriers *b, uint32_t tensor,
                                                int first, int total, int step) {
     const uint32_t idesc = tc::instruction(0, AMN, BMN, kTileM, kTileN) |
@@ -361,10 +367,11 @@ template <int AMN, int BMN, int EP, int DT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_out, const __grid_constant__ GemmArgs g) {
+    constexpr int kStages = stages(EP), kChunk = chunk_blocks(EP, DT);
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *boxes = smem + kStages * kStageBytes;
-    Barriers *b = reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * kStoreBytes);
+    Barriers *b = reinterpret_cast<Barriers *>(boxes + (EP == kExp ? kEpilogueWarps * kBoxBytes : 0));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // (uniform)
     const uint32_t rank = tc::cluster_rank();
     const int total = g.tiles_m * g.tiles_n * g.splits;
@@ -386,6 +393,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     if (warp == 2) tc::alloc_pair(&b->tensor_base, kTensorCols);
+    wait_previous();
+    allow_next();
     if constexpr (EP != kScale) {
         if (blockIdx.x == 0 && threadIdx.x == 96 && g.ticket != nullptr) *g.ticket = 0;
     }
@@ -401,15 +410,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0 && lane == 0)
-            load_operand<AMN, true>(g, &map_a, smem, b, rank, first, total, step);
+            load_operand<AMN, true, kStages>(g, &map_a, smem, b, rank, first, total, step);
         else if (warp == 3 && lane == 0)
-            load_operand<BMN, false>(g, &map_b, smem + kHalfBytes, b, rank, first, total, step);
+            load_operand<BMN, false, kStages>(g, &map_b, smem + kHalfBytes, b, rank, first, total, step);
         else if (warp == 1 && rank == 0)
-            issue_products<AMN, BMN>(g, smem, b, tensor, first, total, step);
+            issue_products<AMN, BMN, kStages, kChunk>(g, smem, b, tensor, first, total, step);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int quarter = warp % 4, part = (warp - 4) / 4;
-        const StoreBox box{boxes + (warp - 4) * kStoreBytes, lane};
         float scale = 1.0f;
         if constexpr (EP == kScale) scale = g.scale_const * (g.scale != nullptr ? *g.scale : 1.0f);
         int buf = 0;
@@ -449,12 +457,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (ok && row0 < g.M && col0 < g.N) {
                 if constexpr (EP == kScale)
-                    scaled_span<DT>(g, &map_out, box, v, row0, col0, x.split, scale);
+                    scaled_span<DT>(g, v, row0 + lane, col0, x.split, scale);
                 else
-                    softmax_span<EP, DT>(g, &map_out, box, v, row0, col0, target);
+                    softmax_span<EP, DT>(g, &map_out, boxes + (warp - 4) * kBoxBytes, lane, v, row0, col0, target);
             }
         }
-        if (lane == 0) tma::bulk_wait<0>();
+    }
+    if constexpr (EP == kExp) {
+        if (warp >= 4 && lane == 0) tma::bulk_wait<0>();
     }
     // a wait gave up: let copies and products that are only slow land before
     // the shared and tensor memory go
@@ -481,7 +491,7 @@ fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUte
     if (!once.is_done(dev)) {
         const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<AMN, BMN, EP, DT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(kSmemBytes));
+                                                   static_cast<int>(smem_bytes(EP)));
         if (e != cudaSuccess) return cuda_status(e);
         once.mark(dev);
     }
@@ -489,8 +499,7 @@ fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUte
     if (total < 1 || total > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
     const int64_t pairs = sm_count() / 2;
     const unsigned grid = static_cast<unsigned>(2 * (total < pairs ? total : (pairs > 0 ? pairs : 1)));
-    gemm_kernel<AMN, BMN, EP, DT><<<grid, kThreads, kSmemBytes, s>>>(a, b, out, g);
-    return check_launch();
+    return launch_chained(gemm_kernel<AMN, BMN, EP, DT>, grid, kThreads, smem_bytes(EP), s, a, b, out, g);
 }
 
 }  // namespace loss

@@ -4,11 +4,11 @@
 namespace fsdp {
 namespace loss {
 
-fsdp_status launch_logits(Epilogue ep, bool f32, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out,
-                          const GemmArgs &g, cudaStream_t s) {
-    if (ep == kStats) return launch_kernel<0, 0, kStats, FSDP_F16>(a, b, out, g, s);
-    return f32 ? launch_kernel<0, 0, kExp, FSDP_F32>(a, b, out, g, s)
-               : launch_kernel<0, 0, kExp, FSDP_F16>(a, b, out, g, s);
+fsdp_status launch_logits(Epilogue ep, bool f32, const CUtensorMap &a, const CUtensorMap &b,
+                          const CUtensorMap &exponentials, const GemmArgs &g, cudaStream_t s) {
+    if (ep == kStats) return launch_kernel<0, 0, kStats, FSDP_F16>(a, b, exponentials, g, s);
+    return f32 ? launch_kernel<0, 0, kExp, FSDP_F32>(a, b, exponentials, g, s)
+               : launch_kernel<0, 0, kExp, FSDP_F16>(a, b, exponentials, g, s);
 }
 
 }  // namespace loss
