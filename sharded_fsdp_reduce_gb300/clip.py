@@ -9,7 +9,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from .fsdp import AdamWHParams, UnitDescs, _check, _counter, _dev, _stream, dtype_code
+from .fsdp import AdamWHParams, UnitDescs, _check, _counter, _dev, dtype_code
 
 __all__ = ["GradClip", "ClipPlan"]
 
@@ -89,10 +89,11 @@ class GradClip:
         """out = tensors * scale * min(1, max_norm / (norm + 1e-6)). norm: the
         norm to use (a CUDA scalar, e.g. one taken over more tensors than
         these); default: these tensors', taken first. Returns the norm."""
+        s = stream if stream is not None else torch.cuda.current_stream()
         if norm is None:
-            norm = self.norm(stream=stream)
+            norm = self.norm(stream=s)
         _check(_lib.load().fsdp_clip_grads(self._src, self._dst, self._numels, self._dtypes, self._n,
-                                           _scalar(norm, "norm"), float(max_norm), self.scale, _stream(stream)),
+                                           _scalar(norm, "norm"), float(max_norm), self.scale, s.cuda_stream),
                "fsdp_clip_grads")
         return norm
 

@@ -18,9 +18,10 @@ namespace clip {
 // work grows, so that a block's sum and its turn at the counter stay small
 // beside its loads.
 int norm_per_thread(int64_t elements) {
-    const int64_t blocks = elements / (8 * kThreads), enough = int64_t(sm_count()) * 48;
-    const int64_t n = blocks / (enough > 0 ? enough : 1);
-    return static_cast<int>(n < 1 ? 1 : n > 16 ? 16 : n);
+    const int64_t blocks = elements / (8 * kThreads), enough = int64_t(sm_count()) * 32;
+    int n = 1;  // a power of two: whole groups of the chunks a thread loads together
+    while (n < 64 && blocks / (2 * n) >= enough) n *= 2;
+    return n;
 }
 
 namespace {
@@ -118,7 +119,7 @@ FSDP_API fsdp_status fsdp_grad_norm(const void *const *tensors, const int64_t *n
         for (int k = 0; k < n_tensors; ++k)
             if (numels[k] > 0) count += norm_ctas(numels[k], lead_of(tensors[k], dtypes[k]), per);
         std::unique_ptr<NormArgs<1>> a(new NormArgs<1>);  // up to 28 KB: not on the caller's stack
-        memset(a.get(), 0, sizeof(*a));
+        a->out = NormOut();
         a->out.ticket = static_cast<uint32_t *>(workspace);
         a->out.part = reinterpret_cast<double *>(static_cast<uint8_t *>(workspace) + kHeader);
         a->out.part_count = count;
@@ -192,7 +193,6 @@ FSDP_API fsdp_status fsdp_clip_grads(const void *const *tensors, void *const *ou
             }
         }
         std::unique_ptr<ScaleArgs> a(new ScaleArgs);
-        memset(a.get(), 0, sizeof(*a));
         a->norm = norm;
         a->max_norm = max_norm;
         a->scale = scale;

@@ -75,34 +75,32 @@ __device__ __forceinline__ double squares_any(const float *g) {
     return squares_any(make_float4(g[0], g[1], g[2], g[3]), make_float4(g[4], g[5], g[6], g[7]));
 }
 
-// The gradients of one chunk in registers, and their average.
-template <int NW, int GD, int W>
-__device__ __forceinline__ void average_chunk(const NormUnit<W> &u, float c, const rsa::GradRegs<NW, GD> &r,
-                                              int64_t j0, float *g) {
-    float acc[8];
-    rsa::widen8<GD>(r.w[0], acc);
+// The average of one chunk's gradients.
+template <int NW, int GD>
+__device__ __forceinline__ void average_of(float c, const rsa::GradRegs<NW, GD> &r, float *g) {
+    rsa::widen8<GD>(r.w[0], g);
 #pragma unroll
     for (int q = 1; q < NW; ++q) {
         float f[8];
         rsa::widen8<GD>(r.w[q], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = __fadd_rn(acc[e], f[e]);
+        for (int e = 0; e < 8; ++e) g[e] = __fadd_rn(g[e], f[e]);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(acc[e], c);
-    if (u.average != nullptr) {
-        // read again by the update: kept in L2 where it fits
-        *reinterpret_cast<float4 *>(u.average + j0) = make_float4(g[0], g[1], g[2], g[3]);
-        *reinterpret_cast<float4 *>(u.average + j0 + 4) = make_float4(g[4], g[5], g[6], g[7]);
-    }
+    for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], c);
 }
 
-// The sum of squares of one chunk, the elements [j0, j0 + 8) of the unit cut
-// to [0, numel): any rank count, any alignment.
-template <int GD, int W, class Rest>
-__device__ __forceinline__ void slow_chunk(const NormUnit<W> &u, int world, float c, int64_t j0, Pair &sum,
-                                           Rest &rest, uint32_t &bad) {
-    float g[8];
+// Stored where the update will read it; plain stores, kept in L2 where it fits.
+template <int W> __device__ __forceinline__ void keep_average(const NormUnit<W> &u, int64_t j0, const float *g) {
+    if (u.average == nullptr) return;
+    *reinterpret_cast<float4 *>(u.average + j0) = make_float4(g[0], g[1], g[2], g[3]);
+    *reinterpret_cast<float4 *>(u.average + j0 + 4) = make_float4(g[4], g[5], g[6], g[7]);
+}
+
+// The chunk [j0, j0 + 8) cut to [0, numel), zeros elsewhere: any rank count,
+// any alignment.
+template <int GD, int W>
+__device__ __forceinline__ void cut_chunk(const NormUnit<W> &u, int world, float c, int64_t j0, float *g) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int64_t j = j0 + e;
@@ -112,13 +110,6 @@ __device__ __forceinline__ void slow_chunk(const NormUnit<W> &u, int world, floa
         for (int q = 1; q < world; ++q) acc = __fadd_rn(acc, Dtype<GD>::load(u.grads[q], j));
         g[e] = __fmul_rn(acc, c);
         if (u.average != nullptr) u.average[j] = g[e];
-        bad += isfinite(g[e]) ? 0u : 1u;
-    }
-    const float s = squares(g);
-    if (in_range(s)) {
-        sum.add(s);
-    } else {
-        rest(squares_any(g));
     }
 }
 
@@ -138,14 +129,42 @@ __device__ __forceinline__ double warp_sum(double x) {
     return x;
 }
 
-// Chunks whose loads a thread has in flight together: registers for about
-// eight 16-byte loads. Their squares are one fp32 sum.
+// One whole chunk of any number of ranks, by 16-byte loads.
+template <int NW, int GD, int W>
+__device__ __forceinline__ void whole_chunk(const NormUnit<W> &u, int world, float c, int64_t j0, float *g) {
+    if constexpr (NW > 0) {
+        rsa::GradRegs<NW, GD> r;
+#pragma unroll
+        for (int q = 0; q < NW; ++q) rsa::load_grad8<GD>(u.grads[q], j0, r.w[q]);
+        average_of<NW, GD>(c, r, g);
+    } else {
+#pragma unroll 4
+        for (int q = 0; q < world; ++q) {
+            uint4 w[rsa::GradRegs<1, GD>::kWords];
+            rsa::load_grad8<GD>(u.grads[q], j0, w);
+            float f[8];
+            rsa::widen8<GD>(w, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = q == 0 ? f[e] : __fadd_rn(g[e], f[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], c);
+    }
+    keep_average(u, j0, g);
+}
+
+// Chunks whose loads a thread has in flight together, their squares one fp32
+// sum: eight 16-byte loads, but four for a single 16-bit tensor list, whose
+// arithmetic per byte wants a fifth block per SM more (708 M bf16 elements
+// 237 us against 281).
 template <int NW, int GD> constexpr int chunks_together() {
-    return NW == 0 ? 1 : NW * rsa::GradRegs<1, GD>::kWords >= 8 ? 1 : NW * rsa::GradRegs<1, GD>::kWords >= 4 ? 2 : 4;
+    constexpr int kLoads = NW * rsa::GradRegs<1, GD>::kWords;
+    return kLoads == 0 || kLoads >= 8 ? 1 : kLoads == 1 ? 4 : 8 / kLoads;
 }
 
 template <int NW, int GD, int W, int CAP>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormArgs<W, CAP> a) {
+__global__ void __launch_bounds__(kThreads, NW == 1 && GD != FSDP_F32 ? 5 : 4)
+    norm_kernel(const __grid_constant__ NormArgs<W, CAP> a) {
     __shared__ Pair pairs[kThreads / 32];
     __shared__ double rare[kThreads / 32];
     __shared__ bool last;
@@ -158,14 +177,16 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     double out_of_range = 0.0;  // what was summed at another scale
     bool any_rare = false;
     uint32_t bad = 0;
-    auto rest = [&](double s) {
-        out_of_range += s;
+    auto rest = [&](const float *g) {
+        out_of_range += squares_any(g);
         any_rare = true;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) bad += isfinite(g[e]) ? 0u : 1u;
     };
     for (int i = 0; i < a.per_thread; i += U) {
         const int64_t j0 = first + 8 * (int64_t(i) * kThreads + threadIdx.x);
         if (j0 >= u.numel) break;
-        if constexpr (NW > 0) {
+        if constexpr (U > 1) {
             const int64_t last_j = j0 + 8 * int64_t(U - 1) * kThreads;
             if (u.vec && j0 >= 0 && last_j + 8 <= u.numel && i + U <= a.per_thread) {
                 rsa::GradRegs<NW, GD> r[U];
@@ -174,57 +195,43 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 #pragma unroll
                     for (int q = 0; q < NW; ++q)
                         rsa::load_grad8<GD>(u.grads[q], j0 + 8 * int64_t(k) * kThreads, r[k].w[q]);
-                float g[U][8], s[U], all = 0.0f;
+                float all = 0.0f;
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    average_chunk<NW, GD, W>(u, a.c, r[k], j0 + 8 * int64_t(k) * kThreads, g[k]);
-                    s[k] = squares(g[k]);
-                    all += s[k];
+                    float g[8];
+                    average_of<NW, GD>(a.c, r[k], g);
+                    keep_average(u, j0 + 8 * int64_t(k) * kThreads, g);
+                    all += squares(g);
                 }
                 if (in_range(all)) {
                     sum.add(all);
                 } else {
 #pragma unroll
                     for (int k = 0; k < U; ++k) {
-                        rest(squares_any(g[k]));
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) bad += isfinite(g[k][e]) ? 0u : 1u;
+                        float g[8];
+                        average_of<NW, GD>(a.c, r[k], g);
+                        rest(g);
                     }
                 }
                 continue;
             }
-        } else {
-            if (u.vec && j0 >= 0 && j0 + 8 <= u.numel) {
-                float g[8];
-#pragma unroll 4
-                for (int q = 0; q < a.world; ++q) {
-                    uint4 w[rsa::GradRegs<1, GD>::kWords];
-                    rsa::load_grad8<GD>(u.grads[q], j0, w);
-                    float f[8];
-                    rsa::widen8<GD>(w, f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) g[e] = q == 0 ? f[e] : __fadd_rn(g[e], f[e]);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], a.c);
-                if (u.average != nullptr) {
-                    *reinterpret_cast<float4 *>(u.average + j0) = make_float4(g[0], g[1], g[2], g[3]);
-                    *reinterpret_cast<float4 *>(u.average + j0 + 4) = make_float4(g[4], g[5], g[6], g[7]);
-                }
-                const float s = squares(g);
-                if (in_range(s)) {
-                    sum.add(s);
-                } else {
-                    rest(squares_any(g));
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) bad += isfinite(g[e]) ? 0u : 1u;
-                }
-                continue;
-            }
         }
+#pragma unroll 1
         for (int k = 0; k < U && i + k < a.per_thread; ++k) {
             const int64_t j = j0 + 8 * int64_t(k) * kThreads;
-            if (j < u.numel) slow_chunk<GD, W>(u, a.world, a.c, j, sum, rest, bad);
+            if (j >= u.numel) break;
+            float g[8];
+            if (u.vec && j >= 0 && j + 8 <= u.numel) {
+                whole_chunk<NW, GD, W>(u, a.world, a.c, j, g);
+            } else {
+                cut_chunk<GD, W>(u, a.world, a.c, j, g);
+            }
+            const float s = squares(g);
+            if (in_range(s)) {
+                sum.add(s);
+            } else {
+                rest(g);
+            }
         }
     }
     if (a.out.nonfinite != nullptr) {
@@ -232,20 +239,26 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
         if (threadIdx.x % 32 == 0 && total) atomicAdd(a.out.nonfinite, total);
     }
     sum = warp_sum(sum);
-    if (__any_sync(0xffffffffu, any_rare)) out_of_range = warp_sum(out_of_range);
     const int warp = threadIdx.x / 32;
-    if (threadIdx.x % 32 == 0) {
-        pairs[warp] = sum;
-        rare[warp] = out_of_range;
+    if (threadIdx.x % 32 == 0) pairs[warp] = sum;
+    const bool has_rare = __syncthreads_or(any_rare);
+    if (has_rare) {
+        out_of_range = warp_sum(out_of_range);
+        if (threadIdx.x % 32 == 0) rare[warp] = out_of_range;
+        __syncthreads();
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double all = 0.0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) all += pairs[w].value() + rare[w];
-        a.out.part[a.out.part_begin + blockIdx.x] = all;
-        __threadfence();
-        last = atomicAdd(a.out.ticket, 1u) + 1 == static_cast<uint32_t>(a.out.part_count);
+    if (warp == 0) {
+        Pair x;
+        if (threadIdx.x < kThreads / 32) x = pairs[threadIdx.x];
+        x = warp_sum(x);
+        if (threadIdx.x == 0) {
+            double all = x.value();
+            if (has_rare)
+                for (int w = 0; w < kThreads / 32; ++w) all += rare[w];
+            a.out.part[a.out.part_begin + blockIdx.x] = all;
+            __threadfence();
+            last = atomicAdd(a.out.ticket, 1u) + 1 == static_cast<uint32_t>(a.out.part_count);
+        }
     }
     __syncthreads();
     if (!last) return;

@@ -68,6 +68,12 @@ __device__ __forceinline__ void join(float &top, float &sum, float other_top, fl
     top = most;
 }
 
+__device__ __forceinline__ void write_loss(const RowArgs &a, double sum, long long valid) {
+    const double by = a.mean && valid > 0 ? static_cast<double>(valid) : 1.0;
+    *a.loss = static_cast<float>(sum / by);
+    *a.scale = static_cast<float>(a.grad_scale / by);
+}
+
 constexpr int kRows = 16;     // of a block
 constexpr int kRowLoads = 8;  // spans a thread reads at once
 
@@ -146,10 +152,15 @@ __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowA
             loss += total[r];
             valid += count[r];
         }
-        a.part_sum[a.first_block + blockIdx.x] = loss;
-        a.part_count[a.first_block + blockIdx.x] = valid;
-        __threadfence();
-        last = atomicAdd(a.ticket, 1u) + 1 == static_cast<uint32_t>(a.all_blocks);
+        last = false;
+        if (a.all_blocks == 1) {
+            write_loss(a, loss, valid);
+        } else {
+            a.part_sum[a.first_block + blockIdx.x] = loss;
+            a.part_count[a.first_block + blockIdx.x] = valid;
+            __threadfence();
+            last = atomicAdd(a.ticket, 1u) + 1 == static_cast<uint32_t>(a.all_blocks);
+        }
     }
     __syncthreads();
     if (!last) return;
@@ -170,11 +181,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowA
     if (warp == 0) {
         x = warp_sum(total[lane]);
         n = warp_sum(count[lane]);
-        if (lane == 0) {
-            const double by = a.mean && n > 0 ? static_cast<double>(n) : 1.0;
-            *a.loss = static_cast<float>(x / by);
-            *a.scale = static_cast<float>(a.grad_scale / by);
-        }
+        if (lane == 0) write_loss(a, x, n);
     }
 }
 
@@ -210,10 +217,15 @@ struct GradArgs {
     uint32_t row_blocks;
 };
 
-// x in three bf16 parts: each takes the next 8 bits.
+// x in three bf16 parts: each takes the next 8 bits. An infinite x counts as
+// bf16's largest value: its products with another operand's lower parts,
+// which may be 0 or of the other sign, would be NaN.
 __device__ __forceinline__ void split3(float x, float &hi, float &mid, float &lo) {
+    constexpr float kMost = 3.38953139e38f;
     hi = __bfloat162float(__float2bfloat16_rn(x));
-    const float r = x - hi;
+    if (hi > kMost) hi = kMost;
+    if (hi < -kMost) hi = -kMost;
+    const float r = isinf(x) ? 0.0f : x - hi;
     mid = __bfloat162float(__float2bfloat16_rn(r));
     lo = r - mid;
 }
@@ -357,7 +369,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 struct Plan {
-    bool f32, grad, pack_x, pack_w;
+    bool f32, grad, few, pack_x, pack_w;
     int64_t band, bands, spans, ldv, ldd, blocks;
     int splits_x, splits_w;
     // byte offsets into the workspace
@@ -397,11 +409,12 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     memset(&p, 0, sizeof(p));
     p.f32 = a.dtype == FSDP_F32;
     p.grad = a.d_hidden != nullptr || a.d_weight != nullptr;
-    p.pack_x = p.f32 || !direct(a.hidden, a.ld_hidden);
-    p.pack_w = p.f32 || !direct(a.weight, a.ld_weight);
+    p.few = !p.grad && a.tokens <= kFewRows;
+    p.pack_x = !p.few && (p.f32 || !direct(a.hidden, a.ld_hidden));
+    p.pack_w = !p.few && (p.f32 || !direct(a.weight, a.ld_weight));
     p.ldv = round_up(a.vocab, 64);
     p.ldd = round_up(a.dim, 64);
-    p.spans = ceil_div(a.vocab, kSpan);
+    p.spans = p.few ? few_blocks(a.vocab) : ceil_div(a.vocab, kSpan);
     const int64_t planes = p.f32 ? 3 : 1;
     const int64_t per_row = p.ldv * (p.f32 ? 10 : 2);  // exponentials, and the planes of an fp32 head
     int64_t band = a.band;
@@ -587,7 +600,60 @@ fsdp_status run_product(const Product &q, const Plan &p, const fsdp_head_loss_ar
     return launch_grad(q.out_dtype, q.orders, ma, mb, g, s);
 }
 
+fsdp_status run_few(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaStream_t s) {
+    FewArgs f;
+    f.hidden = a.hidden;
+    f.weight = a.weight;
+    f.ld_hidden = a.ld_hidden;
+    f.ld_weight = a.ld_weight;
+    f.rows = a.tokens;
+    f.vocab = a.vocab;
+    f.dim = a.dim;
+    f.blocks = p.spans;
+    f.targets = a.targets;
+    f.off = reinterpret_cast<float *>(ws + p.off);
+    f.sum = reinterpret_cast<float *>(ws + p.sum);
+    f.ld_rows = p.band;
+    f.target_logit = reinterpret_cast<float *>(ws + p.target_logit);
+    f.ticket = reinterpret_cast<uint32_t *>(ws + p.ticket);
+    return launch_few(f, a.dtype, s);
+}
+
+// The rows' sums and losses, of one band.
+fsdp_status run_rows(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, int64_t row0, int64_t rows,
+                     int64_t &block, cudaStream_t s) {
+    RowArgs r;
+    r.off = reinterpret_cast<const float *>(ws + p.off);
+    r.sum = reinterpret_cast<const float *>(ws + p.sum);
+    r.ld_rows = p.band;
+    r.spans = static_cast<int32_t>(p.spans);
+    r.target_logit = reinterpret_cast<const float *>(ws + p.target_logit);
+    r.targets = a.targets + row0;
+    r.rows = rows;
+    r.vocab = a.vocab;
+    r.ignore = a.ignore_index;
+    r.lse2 = reinterpret_cast<float *>(ws + p.lse2);
+    r.token_loss = a.token_loss ? a.token_loss + row0 : nullptr;
+    r.part_sum = reinterpret_cast<double *>(ws + p.part_sum);
+    r.part_count = reinterpret_cast<int64_t *>(ws + p.part_count);
+    r.first_block = block;
+    r.all_blocks = p.blocks;
+    r.ticket = reinterpret_cast<uint32_t *>(ws + p.ticket);
+    r.loss = a.loss;
+    r.scale = reinterpret_cast<float *>(ws + p.scale);
+    r.grad_scale = a.grad_scale;
+    r.mean = a.reduction == FSDP_LOSS_MEAN;
+    const unsigned blocks = static_cast<unsigned>(ceil_div(rows, kRows));
+    block += blocks;
+    return launch_chained(rows_kernel, blocks, 1024, 0, s, r);
+}
+
 fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaStream_t s) {
+    int64_t block = 0;
+    if (p.few) {
+        const fsdp_status few = run_few(a, p, ws, s);
+        return few != FSDP_OK ? few : run_rows(a, p, ws, 0, a.tokens, block, s);
+    }
     const int64_t D = a.dim, V = a.vocab;
     const int size = dtype_size(a.dtype);
     const int planes = p.f32 ? 3 : 1;
@@ -615,7 +681,6 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
     st = make_map(&w_k, t16, w.base, D, V, w.planes, w.ld, w.plane, 128);
     if (st == FSDP_OK) st = make_map(&w_n, t16, w.base, D, V, w.planes, w.ld, w.plane, 64);
     if (st != FSDP_OK) return st;
-    int64_t block = 0;
     for (int64_t b = 0; b < p.bands; ++b) {
         const int64_t row0 = b * p.band;
         const int64_t rows = a.tokens - row0 < p.band ? a.tokens - row0 : p.band;
@@ -651,31 +716,7 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         }
         st = launch_logits(p.grad ? kExp : kStats, p.f32, x_k, w_k, e_out, g, s);
         if (st != FSDP_OK) return st;
-        // the rows' sums and losses
-        RowArgs r;
-        r.off = g.off;
-        r.sum = g.sum;
-        r.ld_rows = p.band;
-        r.spans = static_cast<int32_t>(p.spans);
-        r.target_logit = g.target_logit;
-        r.targets = g.targets;
-        r.rows = rows;
-        r.vocab = V;
-        r.ignore = a.ignore_index;
-        r.lse2 = reinterpret_cast<float *>(ws + p.lse2);
-        r.token_loss = a.token_loss ? a.token_loss + row0 : nullptr;
-        r.part_sum = reinterpret_cast<double *>(ws + p.part_sum);
-        r.part_count = reinterpret_cast<int64_t *>(ws + p.part_count);
-        r.first_block = block;
-        r.all_blocks = p.blocks;
-        r.ticket = reinterpret_cast<uint32_t *>(ws + p.ticket);
-        r.loss = a.loss;
-        r.scale = scale;
-        r.grad_scale = a.grad_scale;
-        r.mean = a.reduction == FSDP_LOSS_MEAN;
-        const unsigned nblocks = static_cast<unsigned>(ceil_div(rows, kRows));
-        if ((st = launch_chained(rows_kernel, nblocks, 1024, 0, s, r)) != FSDP_OK) return st;
-        block += nblocks;
+        if ((st = run_rows(a, p, ws, row0, rows, block, s)) != FSDP_OK) return st;
         if (!p.grad) continue;
         // d, then the two products
         GradArgs d;
@@ -689,7 +730,7 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         d.vocab = V;
         d.off = g.off;
         d.ld_rows = p.band;
-        d.lse2 = r.lse2;
+        d.lse2 = reinterpret_cast<const float *>(ws + p.lse2);
         d.targets = g.targets;
         d.ignore = a.ignore_index;
         d.row_blocks = static_cast<uint32_t>(ceil_div(rows, kGradRows));

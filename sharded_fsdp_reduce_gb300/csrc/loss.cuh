@@ -62,5 +62,22 @@ fsdp_status launch_grad_bf16(Orders o, const CUtensorMap &a, const CUtensorMap &
 fsdp_status launch_grad_f16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
 fsdp_status launch_grad_f32(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
 
+// Losses of a few rows (loss_few.cu): the statistics per block instead of
+// per span of columns.
+constexpr int64_t kFewRows = 8;
+
+struct FewArgs {
+    const void *hidden, *weight;
+    int64_t ld_hidden, ld_weight, rows, vocab, dim, blocks;
+    const int64_t *targets;
+    float *off, *sum;  // [blocks][ld_rows]
+    int64_t ld_rows;
+    float *target_logit;
+    uint32_t *ticket;  // cleared for the row kernel
+};
+
+int64_t few_blocks(int64_t vocab);
+fsdp_status launch_few(const FewArgs &a, int dtype, cudaStream_t s);
+
 }  // namespace loss
 }  // namespace fsdp

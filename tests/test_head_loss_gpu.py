@@ -127,3 +127,330 @@ def test_gradients(F, T, V, D, dt):
     x, w, y = inputs(T, V, D, dt, ignored="some")
     loss, tok, dx, dw = run(F, x, w, y)
     check(reference(x, w, y), dt, D, (V, T), loss, tok, dx, dw)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("V,D", [(5003, 768), (129, 100), (33, 3)])
+def test_losses_of_a_few_rows(F, T, V, D, dt):
+    x, w, y = inputs(T, V, D, dt, seed=T, ignored="some" if T > 4 else None)
+    loss, tok, _, _ = run(F, x, w, y, grad=False)
+    check(reference(x, w, y), dt, D, (V, T), loss, tok)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,V,D", [(5, 300, 65), (200, 1001, 129), (130, 515, 1)])
+def test_dims_that_tma_cannot_address(F, T, V, D, dt):
+    x, w, y = inputs(T, V, D, dt, seed=5, std=0.2)
+    loss, tok, dx, dw = run(F, x, w, y)
+    check(reference(x, w, y), dt, D, (V, T), loss, tok, dx, dw)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("off,pad", [(0, 8), (8, 24), (1, 0), (3, 5), (4, 4), (2, 6)])
+def test_views_at_any_offset_and_stride(F, off, pad, dt):
+    T, V, D = 140, 700, 136
+    x0, w0, y = inputs(T, V, D, dt, seed=6)
+
+    def place(rows, src=None):
+        buf = torch.full((off + rows * (D + pad) + 64,), 7.0, dtype=DT[dt], device=DEV)
+        v = buf[off:off + rows * (D + pad)].view(rows, D + pad)[:, :D]
+        if src is not None:
+            v.copy_(src)
+        return buf, v
+
+    _, x = place(T, x0)
+    _, w = place(V, w0)
+    bx, dx = place(T)
+    bw, dw = place(V)
+    assert pad == 0 or not dx.is_contiguous()
+    ref = reference(x0, w0, y)
+    loss, tok, _, _ = run(F, x, w, y, dx=dx, dw=dw)
+    check(ref, dt, D, (V, T), loss, tok, dx, dw)
+    for buf, v, rows in ((bx, dx, T), (bw, dw, V)):  # nothing beside the gradients is written
+        v.zero_()
+        assert int((buf != 0).sum()) == buf.numel() - rows * D
+    loss, tok, _, _ = run(F, x, w, y, grad=False)
+    check(ref, dt, D, (V, T), loss, tok)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,band", [(700, 256), (513, 512), (300, 100), (257, 1)])
+def test_bands_of_tokens(F, T, band, dt):
+    if band == 1 and dt != "bf16":
+        T = 9
+    V, D = 777, 200
+    x, w, y = inputs(T, V, D, dt, seed=7, ignored="some")
+    loss, tok, dx, dw = run(F, x, w, y, band=band)
+    check(reference(x, w, y), dt, D, (V, T), loss, tok, dx, dw)
+    loss, tok, _, _ = run(F, x, w, y, grad=False, band=band)
+    check(reference(x, w, y), dt, D, (V, T), loss, tok)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_split_products(F, dt):
+    # few tiles of a long K: the hidden gradient over the vocabulary, the
+    # weight gradient over the tokens
+    for T, V, D in ((100, 9000, 64), (3000, 200, 64)):
+        x, w, y = inputs(T, V, D, dt, seed=8)
+        loss, tok, dx, dw = run(F, x, w, y)
+        check(reference(x, w, y), dt, D, (V, T), loss, tok, dx, dw)
+
+
+@pytest.mark.parametrize("dt,scale", [("bf16", 1.0), ("f16", 1024.0), ("f32", 0.125)])
+@pytest.mark.parametrize("reduction", ["mean", "sum"])
+def test_reduction_and_loss_scale(F, dt, scale, reduction):
+    T, V, D = 90, 1500, 96
+    if dt == "f16" and reduction == "sum":
+        scale = 4.0  # the gradients have to fit fp16
+    x, w, y = inputs(T, V, D, dt, seed=9, ignored="some")
+    loss, tok, dx, dw = run(F, x, w, y, reduction=reduction, grad_scale=scale)
+    check(reference(x, w, y, reduction, scale), dt, D, (V, T), loss, tok, dx, dw)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [3, 200])
+def test_no_row_counts(F, T, dt):
+    x, w, y = inputs(T, 600, 64, dt, ignored="all")
+    loss, tok, dx, dw = run(F, x, w, y)
+    assert float(loss) == 0.0 and not bool(tok.any()) and not bool(dx.any()) and not bool(dw.any())
+    assert float(run(F, x, w, y, grad=False)[0]) == 0.0
+
+
+def test_no_tokens(F):
+    x, w, y = inputs(0, 100, 64, "bf16", ignored=None)
+    loss, tok, dx, dw = run(F, x, w, y)
+    assert float(loss) == 0.0 and tok.numel() == 0 and not bool(dw.any())
+
+
+def test_either_gradient_alone(F):
+    x, w, y = inputs(150, 900, 128, "bf16")
+    head = F.HeadLoss(900, 128, torch.bfloat16, 150)
+    both = [torch.empty_like(x), torch.empty_like(w)]
+    head.forward_backward(x, w, y, *both)
+    one = torch.empty_like(x)
+    head.forward_backward(x, w, y, one, None)
+    assert torch.equal(one, both[0])
+    two = torch.empty_like(w)
+    head.forward_backward(x, w, y, None, two)
+    assert torch.equal(two, both[1])
+
+
+@pytest.mark.parametrize("T", [4, 300])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_targets_outside_the_vocabulary_show_as_nan(F, T, dt):
+    V, D = 500, 64
+    for bad in (V, -1, 2 ** 40):
+        x, w, y = inputs(T, V, D, dt, ignored=None)
+        good = run(F, x, w, y)[1]
+        y[2] = bad
+        loss, tok, dx, dw = run(F, x, w, y)
+        assert math.isnan(float(loss)) and math.isnan(float(tok[2])) and bool(torch.isnan(dx[2]).all())
+        keep = torch.arange(T, device=DEV) != 2
+        assert torch.equal(tok[keep], good[keep])
+        assert not bool(torch.isnan(dx[keep]).any()) and bool(torch.isnan(dw).all())
+        assert math.isnan(float(run(F, x, w, y, grad=False)[0]))
+
+
+@pytest.mark.parametrize("T", [4, 150])
+def test_nan_in_a_row_stays_in_its_row(F, T):
+    x, w, y = inputs(T, 400, 64, "bf16", ignored=None)
+    x[1, 5] = float("nan")
+    x[2, 7] = float("inf")
+    y[2] = IGNORE  # not finite, and ignored: neither its loss nor a gradient of its own
+    loss, tok, dx, dw = run(F, x, w, y)
+    assert math.isnan(float(loss)) and math.isnan(float(tok[1])) and float(tok[2]) == 0.0
+    assert bool(torch.isnan(dx[1]).all()) and not bool(dx[2].any())
+    rest = torch.arange(T, device=DEV) > 2
+    assert not bool(torch.isnan(tok[rest]).any()) and not bool(torch.isnan(dx[rest]).any())
+    assert math.isnan(float(run(F, x, w, y, grad=False)[0]))
+
+
+@pytest.mark.parametrize("T", [2, 130])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_vocabulary_entries_that_cannot_be_drawn(F, T, dt):
+    # columns whose logits are minus infinity (a masked part of the
+    # vocabulary), whole tiles of them among them
+    V, D = 900, 64
+    x, w, y = inputs(T, V, D, dt, ignored=None)
+    x = x.abs() + 0.1
+    y %= 100
+    w[300:850] = -float("inf")
+    keep = torch.cat([torch.arange(300), torch.arange(850, V)]).to(DEV)
+    ref = reference(x, w[keep], y)
+    loss, tok, _, _ = run(F, x, w, y, grad=False)
+    check(ref, dt, D, (V, T), loss, tok)
+
+
+@pytest.mark.parametrize("T", [3, 200])
+@pytest.mark.parametrize("shift", [300.0, -300.0])
+def test_large_logits(F, T, shift):
+    # every logit shifted far from 0: the softmax does not change, exponentials
+    # without a reference would overflow or vanish
+    V, D = 1000, 64
+    x, w, y = inputs(T, V, D, "bf16", ignored=None)
+    x[:, 0] = 16.0
+    w[:, 0] = shift / 16.0
+    loss, tok, dx, dw = run(F, x, w, y)
+    check(reference(x, w, y), "bf16", D, (V, T), loss, tok, dx, dw)
+    loss, tok, _, _ = run(F, x, w, y, grad=False)
+    check(reference(x, w, y), "bf16", D, (V, T), loss, tok)
+
+
+def test_peaked_and_flat_rows(F):
+    # a row that is sure of its target, one that is sure of another, and one
+    # that has no preference at all
+    V, D = 4000, 128
+    x, w, y = inputs(3, V, D, "f16", std=1.0, ignored=None)
+    x[0] = (w[y[0]].float() * 2).half()
+    x[1] = (w[(y[1] + 1) % V].float() * 2).half()
+    x[2] = 0
+    loss, tok, dx, dw = run(F, x, w, y)
+    check(reference(x, w, y), "f16", D, (V, 3), loss, tok, dx, dw)
+    assert abs(float(tok[2]) - math.log(V)) < 1e-5
+
+
+def test_gradients_against_differences(F):
+    # the loss along a direction, in fp32: (L(x + h d) - L(x - h d)) / 2h = dx . d
+    T, V, D = 12, 300, 64
+    x, w, y = inputs(T, V, D, "f32", std=0.3)
+    _, _, dx, dw = run(F, x, w, y, reduction="sum")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    # third derivative below 2 |d|^3-ish terms: h = 2^-6 keeps h^2 terms and the
+    # losses' own 2^-20 relative error / h both under 2 %
+    h = 2.0 ** -6
+    for which, grad in (("x", dx), ("w", dw)):
+        d = torch.empty_like(grad).normal_(generator=g)
+        d /= d.norm()
+        moved = [run(F, x + s * h * d if which == "x" else x, w + s * h * d if which == "w" else w, y,
+                     grad=False, reduction="sum")[1].double().sum() for s in (1, -1)]
+        slope = float(moved[0] - moved[1]) / (2 * h)
+        want = float((grad.double() * d.double()).sum())
+        assert abs(slope - want) <= 0.02 * float(grad.double().norm()), (slope, want)
+
+
+def test_same_bits_every_time(F):
+    x, w, y = inputs(500, 3000, 256, "bf16", ignored="some")
+    a = run(F, x, w, y)
+    for _ in range(3):
+        b = run(F, x, w, y)
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_one_head_for_calls_of_many_sizes_and_streams(F):
+    V, D = 1000, 128
+    head = F.HeadLoss(V, D, torch.bfloat16, 600)
+    s = torch.cuda.Stream()
+    for k, T in enumerate((600, 1, 37, 256, 8, 599)):
+        x, w, y = inputs(T, V, D, "bf16", seed=k)
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        s.wait_stream(torch.cuda.current_stream())
+        loss, tok = head.forward_backward(x, w, y, dx, dw, stream=s)
+        l2, t2 = head.forward(x, w, y, stream=s)
+        s.synchronize()
+        ref = reference(x, w, y)
+        check(ref, "bf16", D, (V, T), loss, tok, dx, dw)
+        check(ref, "bf16", D, (V, T), l2, t2)
+
+
+def test_workspace_grows_for_packed_operands(F):
+    V, D, T = 700, 72, 50
+    head = F.HeadLoss(V, D, torch.bfloat16, T)
+    x, w, y = inputs(T, V, D, "bf16")
+    buf = torch.empty(V * D + 1, dtype=torch.bfloat16, device=DEV)
+    w1 = buf[1:].view(V, D)
+    w1.copy_(w)
+    a, b = torch.empty_like(w), torch.empty_like(w)
+    head.forward_backward(x, w, y, None, a)
+    head.forward_backward(x, w1, y, None, b)
+    assert torch.equal(a, b)
+
+
+def test_captured_in_a_graph(F):
+    T, V, D = 200, 1200, 128
+    x, w, y = inputs(T, V, D, "bf16")
+    head = F.HeadLoss(V, D, torch.bfloat16, T)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    loss, tok = torch.empty((), device=DEV), torch.empty(T, device=DEV)
+    head.forward_backward(x, w, y, dx, dw, loss=loss, token_loss=tok)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        head.forward_backward(x, w, y, dx, dw, loss=loss, token_loss=tok)
+    for k in range(2):
+        x2, w2, y2 = inputs(T, V, D, "bf16", seed=30 + k, ignored="some")
+        x.copy_(x2), w.copy_(w2), y.copy_(y2)
+        g.replay()
+        torch.cuda.synchronize()
+        check(reference(x, w, y), "bf16", D, (V, T), loss, tok, dx, dw)
+
+
+def test_results_longer_than_32_bits_of_elements(F):
+    # the exponentials of one band pass 2^31 elements
+    T, V, D = 16400, 131100, 8
+    x, w, y = inputs(T, V, D, "bf16", std=0.3, ignored=None)
+    loss, tok, dx, dw = run(F, x, w, y, band=T)
+    at = torch.tensor([0, 1, 8191, 16383, 16384, T - 1], device=DEV)
+    ref = reference(x[at], w, y[at], "sum")
+    logit = 8 * math.sqrt(D) * 2.0 ** -23 * ref["a"]
+    assert bool(((tok[at].double() - ref["tok"]).abs() <= logit + 2.0 ** -20 * ref["lse"]).all())
+    bound = 1.1 * (U["bf16"] + 2.0 ** -11) * ref["sx"] + U["bf16"] * ref["dx"].abs()
+    assert bool(((dx[at].double() * T - ref["dx"]).abs() <= bound + 1e-30).all())
+    del dx
+    # the last vocabulary rows' gradient, from the definition
+    lse = torch.cat([torch.logsumexp(x[i:i + 2048].double() @ w.double().t(), 1) for i in range(0, T, 2048)])
+    cols = torch.arange(V - 5, V, device=DEV)
+    p = torch.exp(x.double() @ w[cols].double().t() - lse[:, None])
+    p -= (y[:, None] == cols[None, :]).double()
+    want = p.t() @ x.double() / T
+    size = p.abs().t() @ x.double().abs() / T
+    assert bool(((dw[cols].double() - want).abs() <= 1.1 * (U["bf16"] + 2.0 ** -11) * size
+                 + U["bf16"] * want.abs()).all())
+
+
+def test_refusals(F):
+    x, w, y = inputs(20, 100, 64, "bf16")
+    head = F.HeadLoss(100, 64, torch.bfloat16, 20)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    for bad in (
+        lambda: head.forward(x.float(), w, y),
+        lambda: head.forward(x, w[:50], y),
+        lambda: head.forward(torch.cat([x, x]), w, y),
+        lambda: head.forward(x[:, :32], w, y),
+        lambda: head.forward(x, w, y[:10]),
+        lambda: head.forward(x, w, y.int()),
+        lambda: head.forward(x, w, y.cpu()),
+        lambda: head.forward(x.t().contiguous().t(), w, y),
+        lambda: head.forward(x[:1].expand(20, 64), w, y),
+        lambda: head.forward_backward(x, w, y, dx.float(), dw),
+        lambda: head.forward_backward(x, w, y, dx, dw[:99]),
+        lambda: head.forward(x, w, y, loss=torch.empty(2, device=DEV)),
+        lambda: F.HeadLoss(100, 64, torch.bfloat16, 20, reduction="none"),
+    ):
+        with pytest.raises((ValueError, TypeError)):
+            bad()
+    with pytest.raises(TypeError):
+        F.HeadLoss(100, 64, torch.float64, 20)
+    for bad in (
+        lambda: head.forward_backward(x, w, y, x, dw),                       # a gradient over its input
+        lambda: head.forward_backward(x, w, y, dx, w),
+        lambda: head.forward_backward(x, w, y, dw[:20], dw),                 # two gradients in one place
+        lambda: head.forward_backward(x, w, y, dx, dw, grad_scale=float("nan")),
+        lambda: F.HeadLoss(100, 64, torch.bfloat16, 20, band=-1),
+    ):
+        with pytest.raises(F.FsdpError):
+            bad()
+
+
+def test_a_workspace_too_small_is_refused(F):
+    import ctypes
+    from sharded_fsdp_reduce_gb300 import _lib, loss as mod
+    x, w, y = inputs(20, 100, 64, "bf16")
+    out = torch.empty((), device=DEV)
+    a = mod._args(x, w, y, out, None, None, None, IGNORE, "mean", 1.0, 0, None)
+    need = mod._workspace_bytes(a)
+    ws = mod._workspace(need, x.device)
+    lib = _lib.load()
+    assert lib.fsdp_head_loss(ctypes.byref(a), ws.data_ptr(), need - 1, None) == _lib.FSDP_ERR_INVALID_ARG
+    assert lib.fsdp_head_loss(ctypes.byref(a), ws.data_ptr() + 16, need, None) == _lib.FSDP_ERR_ALIGNMENT
+    assert lib.fsdp_head_loss(ctypes.byref(a), None, need, None) == _lib.FSDP_ERR_INVALID_ARG
