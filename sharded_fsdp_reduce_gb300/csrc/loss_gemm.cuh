@@ -259,16 +259,18 @@ __device__ __forceinline__ void scaled_span(const GemmArgs &g, float *v, int64_t
     store_span<DT>(g, row, col0, split, v);
 }
 
-// One operand's loads, by one thread of each CTA: its 128 rows of every K
-// block of every tile, into the stages in turn. Each operand has a thread of
-// its own: one thread that issued both (and divided to find its place) took
-// 830 cycles a K block, the products 512.
+// One operand's loads, by one warp of each CTA: its 128 rows of every K block
+// of every tile, into the stages in turn. Each operand has a warp of its own,
+// and the whole warp runs the loop while one elected thread issues, so that
+// what it issues with stays in uniform registers: a single thread's loop over
+// both operands took 830 cycles a K block, over one 500; the products take 512
+// and a load that comes late has to be made up.
 template <int MN, bool A, int kStages>
 __device__ __forceinline__ void load_operand(const GemmArgs &g, const CUtensorMap *map, uint8_t *smem, Barriers *b,
                                              uint32_t rank, int first, int total, int step) {
-    const uint32_t full = tc::peer_addr(tc::smem_addr(&b->full[0]), 0);
+    const uint32_t full = tc::peer_addr(tc::smem_addr(&b->full[0]), 0), to = tc::smem_addr(smem);
     const int kblocks = g.kblocks;
-    const bool planes = g.pairs > 1;
+    const bool planes = g.pairs > 1, expects = A && rank == 0;
     uint32_t *timeouts = g.timeouts;
     int stage = 0;
     uint32_t phase = 1;
@@ -282,14 +284,15 @@ __device__ __forceinline__ void load_operand(const GemmArgs &g, const CUtensorMa
         for (int k = k0; k < k1; ++k) {
             if (!wait(&b->empty[stage], phase, b, timeouts)) return;
             const int z = planes ? ((A ? kPlanesA : kPlanesB) >> (4 * pair)) & 15 : 0;
-            if (A && rank == 0) tma::mbar_arrive_expect_tx(&b->full[stage], 2 * kStageBytes);
-            uint8_t *dst = smem + stage * kStageBytes;
-            const uint32_t bar = full + stage * static_cast<uint32_t>(sizeof(uint64_t));
-            if constexpr (MN) {
-                tc::load_tile(dst, map, at, kb * kBlockK, z, bar);
-                tc::load_tile(dst + kHalfBytes / 2, map, at + 64, kb * kBlockK, z, bar);
-            } else {
-                tc::load_tile(dst, map, kb * kBlockK, at, z, bar);
+            const uint32_t bar = full + stage * static_cast<uint32_t>(sizeof(uint64_t)), dst = to + stage * kStageBytes;
+            if (tc::elect_one()) {
+                if (expects) tma::mbar_arrive_expect_tx(&b->full[stage], 2 * kStageBytes);
+                if constexpr (MN) {
+                    tc::load_tile(dst, map, at, kb * kBlockK, z, bar);
+                    tc::load_tile(dst + kHalfBytes / 2, map, at + 64, kb * kBlockK, z, bar);
+                } else {
+                    tc::load_tile(dst, map, kb * kBlockK, at, z, bar);
+                }
             }
             if (++kb == kblocks) {
                 kb = 0;
@@ -304,7 +307,7 @@ __device__ __forceinline__ void load_operand(const GemmArgs &g, const CUtensorMa
     // the last use of every stage has been consumed: no copy of this CTA is in
     // flight and no product still signals its barriers
     for (int s = 0; s < kStages; ++s) {
-        if (!wait(&b->empty[stage], phase, b, g.timeouts)) return;
+        if (!wait(&b->empty[stage], phase, b, timeouts)) return;
         if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
@@ -409,9 +412,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // 640 * 96 = 61,440 the block was launched with
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 0 && lane == 0)
+        if (warp == 0)
             load_operand<AMN, true, kStages>(g, &map_a, smem, b, rank, first, total, step);
-        else if (warp == 3 && lane == 0)
+        else if (warp == 3)
             load_operand<BMN, false, kStages>(g, &map_b, smem + kHalfBytes, b, rank, first, total, step);
         else if (warp == 1 && rank == 0)
             issue_products<AMN, BMN, kStages, kChunk>(g, smem, b, tensor, first, total, step);

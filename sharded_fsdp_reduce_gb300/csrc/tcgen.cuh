@@ -49,12 +49,13 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 
 // ---------------------------------------------------------------- tiled TMA
 
-// Load one box at (x, y, z) into this CTA's shared memory; the bytes count on
-// `bar`, a shared::cluster address (the pair's even CTA's barrier).
-__device__ __forceinline__ void load_tile(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+// Load one box at (x, y, z) into this CTA's shared memory (dst: its address
+// there); the bytes count on `bar`, a shared::cluster address (the pair's even
+// CTA's barrier).
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
