@@ -1,0 +1,34 @@
+// chain.cuh -- chained launches: the kernels of one call that follow one
+// another on a stream start while the one before them drains (programmatic
+// stream serialization) and wait for its results themselves. Every kernel of
+// a chain waits first and lets the next one start after that, so that a
+// kernel that has started knows all work before its predecessor to be done.
+// Six kernels of 4 to 60 us each: 239 us a call without, 225 with.
+#pragma once
+
+#include "host.cuh"
+
+namespace fsdp {
+
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launch a kernel that waits for its predecessor on the stream itself
+// (wait_previous) and may start before that one has ended.
+template <class... Params, class... Args>
+fsdp_status launch_chained(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                           Args &&...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(grid);
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = smem;
+    config.stream = s;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&config, kernel, static_cast<Args &&>(args)...));
+}
+
+}  // namespace fsdp

@@ -5,7 +5,7 @@
 #include <stddef.h>
 #include <string.h>
 
-#include "host.cuh"
+#include "chain.cuh"
 
 namespace fsdp {
 namespace clip {

@@ -121,16 +121,6 @@ template <> __device__ __forceinline__ uint32_t pack2<FSDP_F16>(float a, float b
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// ---------------------------------------------------------------- chained launches
-// A call's kernels that follow one another are launched with programmatic
-// stream serialization (launch_chained in host.cuh): a kernel may start while
-// the one before it drains, and waits for its results here. Every kernel of
-// a chain waits first and lets the next one start after that, so that a
-// kernel that has started knows all work before its predecessor to be done.
-
-__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ---------------------------------------------------------------- kernel arguments
 
 struct AdamScalars {

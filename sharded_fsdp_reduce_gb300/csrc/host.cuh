@@ -52,24 +52,6 @@ inline int grid_for(int64_t items, int threads, int per_thread, int64_t wave) {
 // Check the launch that was just enqueued.
 inline fsdp_status check_launch() { return cuda_status(cudaGetLastError()); }
 
-// Launch a kernel that waits for its predecessor on the stream itself
-// (wait_previous in common.cuh) and may start before that one has ended.
-template <class... Params, class... Args>
-fsdp_status launch_chained(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
-                           Args &&...args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t config = {};
-    config.gridDim = dim3(grid);
-    config.blockDim = dim3(threads);
-    config.dynamicSmemBytes = smem;
-    config.stream = s;
-    config.attrs = &attr;
-    config.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&config, kernel, static_cast<Args &&>(args)...));
-}
-
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Whether p is host memory (page-locked and mapped, or another host address

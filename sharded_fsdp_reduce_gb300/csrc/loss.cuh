@@ -4,7 +4,7 @@
 
 #include <cuda.h>  // CUtensorMap
 
-#include "host.cuh"
+#include "chain.cuh"
 
 namespace fsdp {
 namespace loss {
