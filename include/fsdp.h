@@ -616,6 +616,21 @@ fsdp_status fsdp_clip_plan_create(const fsdp_unit *units, int n_units, int gathe
                                   fsdp_clip_plan **plan_out);
 fsdp_status fsdp_clip_plan_launch(fsdp_clip_plan *plan, const fsdp_adamw_hparams *hp, float max_norm,
                                   float *norm_out, void *stream);
+
+/* The same for the variant steps (fsdp_step_units_ex): other optimizers, bf16
+ * and fp16 state. Every unit's fp32 average is kept in the workspace (4 bytes
+ * an element), multiplied there by the coefficient, and stepped as one rank's
+ * gradient is. cfg's reduce_dtype must be FSDP_F32
+ * (FSDP_ERR_UNSUPPORTED_DTYPE otherwise); the optimizer is the plan's, the
+ * other scalars are each launch's. */
+fsdp_status fsdp_clip_plan_workspace_ex(const fsdp_unit_ex *units, int n_units, const fsdp_step_config *cfg,
+                                        int64_t *bytes_out);
+fsdp_status fsdp_clip_plan_create_ex(const fsdp_unit_ex *units, int n_units, const fsdp_step_config *cfg,
+                                     int gathers, void *workspace, int64_t workspace_bytes,
+                                     uint32_t *nonfinite_count, uint32_t *wait_timeouts,
+                                     fsdp_clip_plan **plan_out);
+fsdp_status fsdp_clip_plan_launch_ex(fsdp_clip_plan *plan, const fsdp_step_config *cfg, float max_norm,
+                                     float *norm_out, void *stream);
 fsdp_status fsdp_clip_plan_destroy(fsdp_clip_plan *plan);
 
 /* Human-readable name of a status. Never NULL. */

@@ -62,6 +62,9 @@ EXPORTS = (
     "fsdp_clip_plan_create",
     "fsdp_clip_plan_launch",
     "fsdp_clip_plan_destroy",
+    "fsdp_clip_plan_workspace_ex",
+    "fsdp_clip_plan_create_ex",
+    "fsdp_clip_plan_launch_ex",
 )
 
 
@@ -169,6 +172,11 @@ def load() -> ctypes.CDLL:
                                             ctypes.POINTER(vp)]),
             "fsdp_clip_plan_launch": (i32, [vp, ctypes.POINTER(FsdpAdamwHparams), ctypes.c_float, vp, vp]),
             "fsdp_clip_plan_destroy": (i32, [vp]),
+            "fsdp_clip_plan_workspace_ex": (i32, [ctypes.POINTER(FsdpUnitEx), i32, ctypes.POINTER(FsdpStepConfig),
+                                                  ctypes.POINTER(i64)]),
+            "fsdp_clip_plan_create_ex": (i32, [ctypes.POINTER(FsdpUnitEx), i32, ctypes.POINTER(FsdpStepConfig), i32,
+                                               vp, i64, vp, vp, ctypes.POINTER(vp)]),
+            "fsdp_clip_plan_launch_ex": (i32, [vp, ctypes.POINTER(FsdpStepConfig), ctypes.c_float, vp, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)

@@ -9,7 +9,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from .fsdp import AdamWHParams, UnitDescs, _check, _counter, _dev, dtype_code
+from .fsdp import StepConfig, UnitDescs, _check, _counter, _dev, dtype_code
 
 __all__ = ["GradClip", "ClipPlan"]
 
@@ -99,37 +99,45 @@ class GradClip:
 
 
 class ClipPlan:
-    """A model's clipped step, validated once (fsdp_clip_plan_create): launch()
-    takes the averaged gradient's norm over all units, then each unit's AdamW
-    step with the clipped gradient and its all-gathers. The units' buffers
-    must stay allocated (the units are kept alive here)."""
+    """A model's clipped step, validated once (fsdp_clip_plan_create, or
+    fsdp_clip_plan_create_ex when `config` is given): launch() takes the
+    averaged gradient's norm over all units, then each unit's step with the
+    clipped gradient and its all-gathers. The units' buffers must stay
+    allocated (the units are kept alive here)."""
 
     def __init__(self, units, gathers: int = 1, nonfinite_count: Optional[torch.Tensor] = None,
-                 wait_timeouts: Optional[torch.Tensor] = None):
+                 config: Optional[StepConfig] = None, wait_timeouts: Optional[torch.Tensor] = None):
         self.descs = units if isinstance(units, UnitDescs) else UnitDescs(units)
-        if not self.descs.adamw:
-            raise ValueError("a clipped model step needs fp32 master and AdamW state in every unit")
+        if config is None and not self.descs.adamw:
+            raise ValueError("an AdamW model step needs fp32 master and AdamW state in every unit")
+        self.config = config
         self._counters = (nonfinite_count, wait_timeouts)
         self._handle = ctypes.c_void_p(None)
         lib = _lib.load()
         size = ctypes.c_int64(0)
-        _check(lib.fsdp_clip_plan_workspace(self.descs.array, self.descs.n, ctypes.byref(size)),
-               "fsdp_clip_plan_workspace")
+        nf, wt = _counter(nonfinite_count), _counter(wait_timeouts, "wait_timeouts")
+        if config is None:
+            name, model = "fsdp_clip_plan_create", (self.descs.array, self.descs.n)
+            _check(lib.fsdp_clip_plan_workspace(*model, ctypes.byref(size)), "fsdp_clip_plan_workspace")
+        else:
+            cfg = config.to_c()
+            name, model = "fsdp_clip_plan_create_ex", (self.descs.array_ex, self.descs.n, ctypes.byref(cfg))
+            _check(lib.fsdp_clip_plan_workspace_ex(*model, ctypes.byref(size)), "fsdp_clip_plan_workspace_ex")
         self._ws = _Workspace(size.value, torch.device("cuda", torch.cuda.current_device()))
-        _check(lib.fsdp_clip_plan_create(self.descs.array, self.descs.n, int(gathers),
-                                         self._ws.buf.data_ptr(), self._ws.buf.numel(), _counter(nonfinite_count),
-                                         _counter(wait_timeouts, "wait_timeouts"), ctypes.byref(self._handle)),
-               "fsdp_clip_plan_create")
+        _check(getattr(lib, name)(*model, int(gathers), self._ws.buf.data_ptr(), self._ws.buf.numel(), nf, wt,
+                                  ctypes.byref(self._handle)), name)
 
-    def launch(self, hparams: AdamWHParams, max_norm: float, norm: torch.Tensor,
+    def launch(self, hparams, max_norm: float, norm: torch.Tensor,
                stream: Optional[torch.cuda.Stream] = None) -> None:
-        """One step; norm (fp32 CUDA scalar) receives the gradient's norm."""
+        """One step (hparams: AdamWHParams, or a StepConfig of the plan's
+        optimizer); norm (fp32 CUDA scalar) receives the gradient's norm."""
         if not self._handle:
             raise RuntimeError("the model step was destroyed")
         s = self._ws.on(stream)
         c = hparams.to_c()
-        _check(_lib.load().fsdp_clip_plan_launch(self._handle, ctypes.byref(c), float(max_norm),
-                                                 _scalar(norm, "norm"), s.cuda_stream), "fsdp_clip_plan_launch")
+        name = "fsdp_clip_plan_launch" if self.config is None else "fsdp_clip_plan_launch_ex"
+        _check(getattr(_lib.load(), name)(self._handle, ctypes.byref(c), float(max_norm), _scalar(norm, "norm"),
+                                          s.cuda_stream), name)
 
     def close(self) -> None:
         if self._handle:

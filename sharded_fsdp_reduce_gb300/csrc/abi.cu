@@ -1496,9 +1496,14 @@ constexpr int64_t kClipHeader = 256;  // the norm's counter
 
 }  // namespace
 
-// A validated clipped model step (fsdp_clip_plan_*).
+// A validated clipped model step (fsdp_clip_plan_*). Variant plans keep every
+// unit's average, scale it in place and run the variant step on it as on one
+// rank's fp32 gradient: `m` then holds those steps.
 struct fsdp_clip_plan {
     ModelPlan m;
+    bool variant = false;
+    int optimizer = 0;
+    std::vector<clip::ScaleUnit> averages;  // variant: what the coefficient multiplies
     std::vector<NormLaunch> norms;
     std::vector<UpdateLaunch> updates;
     int64_t blocks = 0;       // of all the norm launches
@@ -1533,19 +1538,30 @@ int fused_full(const UnitPlan &u) {
     return u.separate_gathers > 0 && u.gather.n_dst <= clip::kUpdateFull ? u.gather.n_dst : 0;
 }
 
+// What the norm pass needs of a unit, whichever its update.
+struct Gradients {
+    const void *const *ranks;
+    int world, dtype;
+    int64_t numel;
+};
+
+Gradients gradients_of(const UnitPlan &u) {
+    return u.variant ? Gradients{u.step.args.grads, u.step.args.world, u.grad_dtype, u.step.args.end}
+                     : Gradients{u.rsa.grads, u.rsa.world, u.grad_dtype, u.rsa.end};
+}
+
 template <class Args>
-fsdp_status add_norm_unit(fsdp_clip_plan &p, std::unique_ptr<Args> NormLaunch::*which, int width, const UnitPlan &u,
+fsdp_status add_norm_unit(fsdp_clip_plan &p, std::unique_ptr<Args> NormLaunch::*which, int width, const Gradients &r,
                           float *average, uint32_t *nonfinite, int per_thread) {
-    const RsaArgs &r = u.rsa;
     NormLaunch *l = nullptr;
     for (NormLaunch &x : p.norms)
-        if (x.width == width && x.world == r.world && x.dtype == u.grad_dtype && (x.*which)->n < Args::kUnits) l = &x;
+        if (x.width == width && x.world == r.world && x.dtype == r.dtype && (x.*which)->n < Args::kUnits) l = &x;
     if (!l) {
         p.norms.emplace_back();
         l = &p.norms.back();
         l->width = width;
         l->world = r.world;
-        l->dtype = u.grad_dtype;
+        l->dtype = r.dtype;
         (l->*which).reset(new Args);
         memset((l->*which).get(), 0, sizeof(Args));
         (l->*which)->world = r.world;
@@ -1555,14 +1571,14 @@ fsdp_status add_norm_unit(fsdp_clip_plan &p, std::unique_ptr<Args> NormLaunch::*
     }
     Args &a = *(l->*which);
     auto &d = a.u[a.n++];
-    for (int q = 0; q < r.world; ++q) d.grads[q] = r.grads[q];
+    for (int q = 0; q < r.world; ++q) d.grads[q] = r.ranks[q];
     d.average = average;
-    d.numel = r.end;
+    d.numel = r.numel;
     d.cta_begin = l->grid;
     d.lead = 0;
     d.vec = 1;
-    for (int q = 0; q < r.world; ++q) d.vec = d.vec && aligned(r.grads[q], 16);
-    l->grid += clip::norm_ctas(r.end, 0, per_thread);
+    for (int q = 0; q < r.world; ++q) d.vec = d.vec && aligned(r.ranks[q], 16);
+    l->grid += clip::norm_ctas(r.numel, 0, per_thread);
     return FSDP_OK;
 }
 
@@ -1611,52 +1627,66 @@ void add_update_unit(fsdp_clip_plan &p, const UnitPlan &u, bool host, float *ave
 
 // The launches of a validated model; addresses in the workspace are filled
 // when `workspace` is known (sizes do not depend on it).
-fsdp_status plan_clip(fsdp_clip_plan &p, uint8_t *workspace, uint32_t *nonfinite) {
+fsdp_status plan_clip(fsdp_clip_plan &p, const std::vector<UnitPlan> &units, uint8_t *workspace,
+                      uint32_t *nonfinite) {
     ResidencyMemo res;
     int64_t total = 0;
-    for (const UnitPlan &u : p.m.units)
-        if (!u.empty) total += u.rsa.end;
+    for (const UnitPlan &u : units)
+        if (!u.empty) total += gradients_of(u).numel;
     const int per_thread = clip::norm_per_thread(total);
     int64_t blocks = 0;
-    for (const UnitPlan &u : p.m.units)
-        if (!u.empty) blocks += clip::norm_ctas(u.rsa.end, 0, per_thread);
+    for (const UnitPlan &u : units)
+        if (!u.empty) blocks += clip::norm_ctas(gradients_of(u).numel, 0, per_thread);
     if (blocks > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
     p.blocks = blocks;
     const int64_t averages = kClipHeader + (8 * blocks + 255) / 256 * 256;
     p.average_bytes = 0;
-    for (const UnitPlan &u : p.m.units) {
+    for (const UnitPlan &u : units) {
         if (u.empty) continue;
-        bool host = res.host_resident(u.rsa.master) || res.host_resident(u.rsa.m) || res.host_resident(u.rsa.v);
-        bool host_grads = false;
-        for (int q = 0; q < u.rsa.world; ++q) host_grads = host_grads || res.host_resident(u.rsa.grads[q]);
-        const bool keep = keeps_average(u, host || host_grads);
+        const Gradients r = gradients_of(u);
+        bool keep = u.variant, host = false;
+        if (!keep) {
+            host = res.host_resident(u.rsa.master) || res.host_resident(u.rsa.m) || res.host_resident(u.rsa.v);
+            bool host_grads = false;
+            for (int q = 0; q < r.world; ++q) host_grads = host_grads || res.host_resident(r.ranks[q]);
+            keep = keeps_average(u, host || host_grads);
+        }
         float *average = nullptr;
         if (keep) {
             if (workspace) average = reinterpret_cast<float *>(workspace + averages + p.average_bytes);
-            p.average_bytes += (4 * u.rsa.end + 255) / 256 * 256;
+            p.average_bytes += (4 * r.numel + 255) / 256 * 256;
         }
         if (!workspace) continue;
         fsdp_status st = FSDP_OK;
-        switch (u.rsa.world) {
-            case 1: st = add_norm_unit(p, &NormLaunch::a1, 1, u, average, nonfinite, per_thread); break;
-            case 2: st = add_norm_unit(p, &NormLaunch::a2, 2, u, average, nonfinite, per_thread); break;
-            case 4: st = add_norm_unit(p, &NormLaunch::a4, 4, u, average, nonfinite, per_thread); break;
-            case 8: st = add_norm_unit(p, &NormLaunch::a8, 8, u, average, nonfinite, per_thread); break;
-            default: st = add_norm_unit(p, &NormLaunch::any, FSDP_MAX_WORLD, u, average, nonfinite, per_thread);
+        switch (r.world) {
+            case 1: st = add_norm_unit(p, &NormLaunch::a1, 1, r, average, nonfinite, per_thread); break;
+            case 2: st = add_norm_unit(p, &NormLaunch::a2, 2, r, average, nonfinite, per_thread); break;
+            case 4: st = add_norm_unit(p, &NormLaunch::a4, 4, r, average, nonfinite, per_thread); break;
+            case 8: st = add_norm_unit(p, &NormLaunch::a8, 8, r, average, nonfinite, per_thread); break;
+            default: st = add_norm_unit(p, &NormLaunch::any, FSDP_MAX_WORLD, r, average, nonfinite, per_thread);
         }
         if (st != FSDP_OK) return st;
-        add_update_unit(p, u, host, average, keep);
+        if (u.variant) {
+            clip::ScaleUnit x = {};
+            x.src = x.dst = average;
+            x.numel = r.numel;
+            x.vec = 1;
+            p.averages.push_back(x);
+        } else {
+            add_update_unit(p, u, host, average, keep);
+        }
     }
     p.workspace = workspace;
     return FSDP_OK;
 }
 
-fsdp_status run_clip(fsdp_clip_plan &p, const fsdp_adamw_hparams &hp, float max_norm, float *norm, cudaStream_t s) {
+// The norm of the averages, c being 1 / (world * grad_scale).
+fsdp_status run_norm(fsdp_clip_plan &p, double grad_scale, float *norm, cudaStream_t s) {
     if (p.blocks == 0) return cuda_status(cudaMemsetAsync(norm, 0, 4, s));
     int64_t part = 0;
     for (NormLaunch &l : p.norms) {
         const fsdp_status st = l.with([&](auto &a) {
-            a->c = make_scalars(hp, l.world).c;
+            a->c = static_cast<float>(1.0 / (static_cast<double>(l.world) * grad_scale));
             a->out.ticket = reinterpret_cast<uint32_t *>(p.workspace);
             a->out.part = reinterpret_cast<double *>(p.workspace + kClipHeader);
             a->out.part_begin = part;
@@ -1667,6 +1697,34 @@ fsdp_status run_clip(fsdp_clip_plan &p, const fsdp_adamw_hparams &hp, float max_
         if (st != FSDP_OK) return st;
         part += l.grid;
     }
+    return FSDP_OK;
+}
+
+// The coefficient on every average, in place (nothing is done for 1).
+fsdp_status scale_averages(const fsdp_clip_plan &p, float max_norm, const float *norm, cudaStream_t s) {
+    std::unique_ptr<clip::ScaleArgs> a(new clip::ScaleArgs);
+    a->norm = norm;
+    a->max_norm = max_norm;
+    a->scale = 1.0f;
+    a->in_place = 1;
+    for (size_t end = p.averages.size(); end > 0;) {
+        const size_t begin = end > clip::ScaleArgs::kUnits ? end - clip::ScaleArgs::kUnits : 0;
+        int64_t grid = 0;
+        a->n = static_cast<int32_t>(end - begin);
+        for (size_t i = begin; i < end; ++i) {
+            clip::ScaleUnit &u = a->u[i - begin];
+            u = p.averages[i];
+            u.cta_begin = grid;
+            grid += clip::scale_ctas(u.numel, 0);
+        }
+        if (fsdp_status st = clip::launch_scale(*a, FSDP_F32, grid, s); st != FSDP_OK) return st;
+        end = begin;
+    }
+    return FSDP_OK;
+}
+
+fsdp_status run_clip(fsdp_clip_plan &p, const fsdp_adamw_hparams &hp, float max_norm, float *norm, cudaStream_t s) {
+    if (fsdp_status st = run_norm(p, hp.grad_scale, norm, s); st != FSDP_OK) return st;
     for (size_t i = p.updates.size(); i-- > 0;) {
         UpdateLaunch &l = p.updates[i];
         l.a->s = make_scalars(hp, l.unit_world);
@@ -1694,6 +1752,29 @@ fsdp_status run_clip(fsdp_clip_plan &p, const fsdp_adamw_hparams &hp, float max_
     return FSDP_OK;
 }
 
+int device_now() {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return -1;
+    }
+    return dev;
+}
+
+// The workspace's size and overlap with the units' buffers; then the plan is the caller's.
+fsdp_status finish_clip(std::unique_ptr<fsdp_clip_plan> &p, const ModelPlan &given, void *workspace,
+                        int64_t workspace_bytes, fsdp_clip_plan **plan_out) {
+    const int64_t bytes = clip_bytes(*p);
+    if (workspace_bytes < bytes) return FSDP_ERR_INVALID_ARG;
+    for (const std::vector<Span> *spans : {&given.writes, &given.reads})
+        for (const Span &x : *spans)
+            if (overlaps(reinterpret_cast<const void *>(x.lo), x.hi - x.lo, workspace, static_cast<size_t>(bytes)))
+                return FSDP_ERR_INVALID_ARG;
+    p->device = device_now();
+    *plan_out = p.release();
+    return FSDP_OK;
+}
+
 static_assert(kGroupMaxWorld <= clip::kUpdateFull, "a batched unit's first gather is written by its update");
 
 }  // namespace
@@ -1705,7 +1786,7 @@ FSDP_API fsdp_status fsdp_clip_plan_workspace(const fsdp_unit *units, int n_unit
         if (!bytes_out) return FSDP_ERR_INVALID_ARG;
         fsdp_clip_plan p;
         fsdp_status st = plan_units(units, n_units, &kPlaceholderHp, 0, 0, nullptr, nullptr, p.m);
-        if (st == FSDP_OK) st = plan_clip(p, nullptr, nullptr);
+        if (st == FSDP_OK) st = plan_clip(p, p.m.units, nullptr, nullptr);
         if (st != FSDP_OK) return st;
         *bytes_out = clip_bytes(p);
         return FSDP_OK;
@@ -1723,35 +1804,90 @@ FSDP_API fsdp_status fsdp_clip_plan_create(const fsdp_unit *units, int n_units, 
         if (st != FSDP_OK) return st;
         if (!workspace) return FSDP_ERR_INVALID_ARG;
         if (!aligned(workspace, 256)) return FSDP_ERR_ALIGNMENT;
-        if ((st = plan_clip(*p, static_cast<uint8_t *>(workspace), nonfinite_count)) != FSDP_OK) return st;
-        const int64_t bytes = clip_bytes(*p);
-        if (workspace_bytes < bytes) return FSDP_ERR_INVALID_ARG;
-        for (const std::vector<Span> *spans : {&p->m.writes, &p->m.reads})
-            for (const Span &x : *spans)
-                if (overlaps(reinterpret_cast<const void *>(x.lo), x.hi - x.lo, workspace, static_cast<size_t>(bytes)))
-                    return FSDP_ERR_INVALID_ARG;
-        if (cudaGetDevice(&p->device) != cudaSuccess) {
-            (void)cudaGetLastError();
-            p->device = -1;
-        }
-        *plan_out = p.release();
+        st = plan_clip(*p, p->m.units, static_cast<uint8_t *>(workspace), nonfinite_count);
+        if (st != FSDP_OK) return st;
+        return finish_clip(p, p->m, workspace, workspace_bytes, plan_out);
+    });
+}
+
+// The variant form: validated as fsdp_step_units_ex validates its units, then
+// planned as the variant step of one rank whose fp32 gradient is the average.
+FSDP_API fsdp_status fsdp_clip_plan_workspace_ex(const fsdp_unit_ex *units, int n_units, const fsdp_step_config *cfg,
+                                                 int64_t *bytes_out) {
+    return guarded([&]() -> fsdp_status {
+        if (!bytes_out) return FSDP_ERR_INVALID_ARG;
+        fsdp_clip_plan p;
+        fsdp_status st = plan_units_ex(units, n_units, cfg, 0, nullptr, nullptr, p.m);
+        if (st == FSDP_OK) st = plan_clip(p, p.m.units, nullptr, nullptr);
+        if (st != FSDP_OK) return st;
+        *bytes_out = clip_bytes(p);
         return FSDP_OK;
+    });
+}
+
+FSDP_API fsdp_status fsdp_clip_plan_create_ex(const fsdp_unit_ex *units, int n_units, const fsdp_step_config *cfg,
+                                              int gathers, void *workspace, int64_t workspace_bytes,
+                                              uint32_t *nonfinite_count, uint32_t *wait_timeouts,
+                                              fsdp_clip_plan **plan_out) {
+    return guarded([&]() -> fsdp_status {
+        if (!plan_out) return FSDP_ERR_INVALID_ARG;
+        *plan_out = nullptr;
+        std::unique_ptr<fsdp_clip_plan> p(new fsdp_clip_plan);
+        ModelPlan given;
+        fsdp_status st = plan_units_ex(units, n_units, cfg, gathers, nonfinite_count, wait_timeouts, given);
+        if (st != FSDP_OK) return st;
+        if (cfg->reduce_dtype != FSDP_F32) return FSDP_ERR_UNSUPPORTED_DTYPE;
+        if (!workspace) return FSDP_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256)) return FSDP_ERR_ALIGNMENT;
+        st = plan_clip(*p, given.units, static_cast<uint8_t *>(workspace), nonfinite_count);
+        if (st != FSDP_OK) return st;
+        std::vector<fsdp_unit_ex> own(units, units + n_units);
+        std::vector<const void *> average(static_cast<size_t>(n_units), nullptr);
+        for (size_t u = 0, k = 0; u < own.size(); ++u) {
+            if (given.units[u].empty) {
+                own[u].padded_numel = 0;
+                continue;
+            }
+            average[u] = p->averages[k++].src;
+            own[u].grads = &average[u];
+            own[u].world = 1;
+            own[u].grad_dtype = FSDP_F32;
+        }
+        st = plan_units_ex(own.data(), n_units, cfg, gathers, nullptr, wait_timeouts, p->m);
+        if (st != FSDP_OK) return st;
+        p->variant = true;
+        p->optimizer = cfg->optimizer;
+        return finish_clip(p, given, workspace, workspace_bytes, plan_out);
     });
 }
 
 FSDP_API fsdp_status fsdp_clip_plan_launch(fsdp_clip_plan *plan, const fsdp_adamw_hparams *hp, float max_norm,
                                            float *norm_out, void *stream) {
     return guarded([&]() -> fsdp_status {
-        if (!plan || !hp || !norm_out || !(max_norm > 0.0f)) return FSDP_ERR_INVALID_ARG;
+        if (!plan || plan->variant || !hp || !norm_out || !(max_norm > 0.0f)) return FSDP_ERR_INVALID_ARG;
         if (!adam_step_valid(*hp)) return FSDP_ERR_INVALID_ARG;
         if (!aligned(norm_out, 4)) return FSDP_ERR_ALIGNMENT;
-        int dev = -1;
-        if (cudaGetDevice(&dev) != cudaSuccess) {
-            (void)cudaGetLastError();
-            dev = -1;
-        }
-        if (dev != plan->device) return FSDP_ERR_INVALID_ARG;
+        if (device_now() != plan->device) return FSDP_ERR_INVALID_ARG;
         return run_clip(*plan, *hp, max_norm, norm_out, static_cast<cudaStream_t>(stream));
+    });
+}
+
+FSDP_API fsdp_status fsdp_clip_plan_launch_ex(fsdp_clip_plan *plan, const fsdp_step_config *cfg, float max_norm,
+                                              float *norm_out, void *stream) {
+    return guarded([&]() -> fsdp_status {
+        if (!plan || !plan->variant || !cfg || !norm_out || !(max_norm > 0.0f)) return FSDP_ERR_INVALID_ARG;
+        if (fsdp_status st = step_config_valid(*cfg, plan->optimizer, {}); st != FSDP_OK) return st;
+        if (cfg->reduce_dtype != FSDP_F32) return FSDP_ERR_UNSUPPORTED_DTYPE;
+        if (!aligned(norm_out, 4)) return FSDP_ERR_ALIGNMENT;
+        if (device_now() != plan->device) return FSDP_ERR_INVALID_ARG;
+        const cudaStream_t s = static_cast<cudaStream_t>(stream);
+        fsdp_status st = run_norm(*plan, cfg->grad_scale, norm_out, s);
+        if (st == FSDP_OK) st = scale_averages(*plan, max_norm, norm_out, s);
+        if (st != FSDP_OK) return st;
+        fsdp_step_config one = *cfg;
+        one.grad_scale = 1.0f;  // the average is unscaled
+        set_step_scalars(plan->m, one);
+        return run_units(plan->m, s);
     });
 }
 

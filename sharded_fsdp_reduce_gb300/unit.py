@@ -346,31 +346,34 @@ class UnitSequence:
             self._plan_key = key
         self._plan.launch(hp if config is None else config, stream)
 
-    def clip_step(self, hp: AdamWHParams, max_norm: float, gathers: int = 1,
-                  nonfinite_count: Optional[torch.Tensor] = None, stream=None,
-                  wait_timeouts: Optional[torch.Tensor] = None, norm: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def clip_step(self, hp, max_norm: float, gathers: int = 1, nonfinite_count: Optional[torch.Tensor] = None,
+                  stream=None, wait_timeouts: Optional[torch.Tensor] = None,
+                  norm: Optional[torch.Tensor] = None) -> torch.Tensor:
         """step() with the averaged gradient clipped to max_norm by its L2 norm
-        over all units before AdamW; returns that norm (an fp32 CUDA scalar:
-        norm, or a new one). The norm is of the gradient the shards hold
-        together, the one a single replica would clip. Every unit must take
-        the fused AdamW step (fp32 state). As step() does, the model is
-        validated once and that plan (with 4 bytes an element of workspace for
-        units of more than 8 gradient bytes an element) kept."""
-        if not self._adamw_fused(hp):
-            raise ValueError("clip_step needs AdamWHParams and fp32 AdamW state in every unit")
+        over all units before the update; returns that norm (an fp32 CUDA
+        scalar: norm, or a new one). The norm is of the gradient the shards
+        hold together, the one a single replica would clip. hp as in step()
+        (the reduction in fp32). As step() does, the model is validated once
+        and that plan kept, with 4 bytes an element of workspace for units of
+        more than 8 gradient bytes an element and for variant steps."""
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        key = (int(gathers), ptr(nonfinite_count), ptr(wait_timeouts))
+        if self._adamw_fused(hp):
+            config, kind = None, "adamw"
+        else:
+            config = self._variant_config(hp, False)
+            kind = config.optimizer
+        key = (kind, config is None, int(gathers), ptr(nonfinite_count), ptr(wait_timeouts))
         if key != self._clip_key:
             if self._clip_plan is not None:
                 self._clip_plan.close()
                 self._clip_plan, self._clip_key = None, None
-            self._clip_plan = ClipPlan(self.descs, gathers, nonfinite_count, wait_timeouts)
+            self._clip_plan = ClipPlan(self.descs, gathers, nonfinite_count, config, wait_timeouts)
             self._clip_key = key
         s = stream if stream is not None else torch.cuda.current_stream()
         if norm is None:
             with torch.cuda.stream(s):
                 norm = torch.empty((), dtype=torch.float32, device=self.units[0].device if self.units else "cuda")
-        self._clip_plan.launch(hp, max_norm, norm, s)
+        self._clip_plan.launch(hp if config is None else config, max_norm, norm, s)
         return norm
 
     def step_unplanned(self, hp, gathers: int = 1, nonfinite_count: Optional[torch.Tensor] = None,

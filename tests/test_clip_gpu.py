@@ -359,9 +359,63 @@ def test_clipped_step_refusals(F):
     with pytest.raises(F.FsdpError):
         model.clip_step(F.AdamWHParams(**dict(HP, step=0)), 1.0)
     sgd = F.FlatParamUnit([("w", (8,))], 2, BF16, BF16, device=DEV, optimizer="sgd")
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError):  # an SGD unit steps with a StepConfig
         F.UnitSequence([sgd]).clip_step(F.AdamWHParams(**HP), 1.0)
-    with pytest.raises(ValueError):
-        model.clip_step(F.StepConfig("adamw", 1e-3), 1.0)
+    with pytest.raises(F.FsdpError):  # the norm is of the fp32 average
+        F.UnitSequence([sgd]).clip_step(F.StepConfig("sgd", 1e-3, reduce_dtype=BF16), 1.0)
+    with pytest.raises(F.FsdpError):
+        F.UnitSequence([sgd]).clip_step(F.StepConfig("sgd", 1e-3), -1.0)
     with pytest.raises(ValueError):
         model.clip_step(F.AdamWHParams(**HP), 1.0, norm=torch.empty(2, device=DEV))
+
+
+VARIANTS = [("sgd", F32), ("adamax", F32), ("adadelta", F32), ("adamw", BF16), ("sgd", BF16), ("adamax", F16)]
+
+
+@pytest.mark.parametrize("world", [1, 3, 8])
+@pytest.mark.parametrize("optimizer,state", VARIANTS, ids=lambda v: str(v).split(".")[-1])
+@pytest.mark.parametrize("share", [0.3, float("inf")])
+def test_clipped_variant_step(F, optimizer, state, world, share):
+    """Against the variant kernel run on the clipped average as one rank's fp32 gradient."""
+    odt = BF16 if state == F32 else state
+    scale = 64.0
+    make = lambda: make_units(F, [4099, 0, 37, 20_000], world, odt, odt, 21, n_full=2, scale=scale,  # noqa: E731
+                              optimizer=optimizer, state_dtype=state) if optimizer != "sgd" else \
+        sgd_units(F, [4099, 0, 37, 20_000], world, odt, odt, scale, state)
+    a, b = make(), make()
+    if optimizer == "adadelta":
+        for u in a + b:
+            u.exp_avg.abs_()  # its first state is a running mean of squares
+    avg = [average(u, scale) for u in a]
+    want = norm64(avg)
+    cfg = F.StepConfig(optimizer, 1e-3, 0.9, 0.95, 1e-8, 0.1, 7, scale)
+    nf = torch.zeros(1, dtype=torch.int32, device=DEV)
+    norm = F.UnitSequence(a).clip_step(cfg, share * want, nonfinite_count=nf)
+    torch.cuda.synchronize()
+    assert_norm(norm, want)
+    assert int(nf) == 0
+    coef = factor(norm, share * want)
+    one = F.StepConfig(optimizer, 1e-3, 0.9, 0.95, 1e-8, 0.1, 7, 1.0)
+    for ua, ub, g in zip(a, b, avg):
+        if not g.numel():
+            continue
+        F.fsdp_reduce_scatter_step([g * coef], ub.master, ub.exp_avg, ub.exp_avg_sq,
+                                   None if state != F32 else ub.shard_out, one)
+        torch.cuda.synchronize()
+        for name in ("master", "exp_avg", "exp_avg_sq"):
+            x, y = getattr(ua, name), getattr(ub, name)
+            assert (x is None and y is None) or torch.equal(x, y), name
+        for f in ua.full:
+            assert torch.equal(f, ub.shard_out)
+
+
+def sgd_units(F, sizes, world, gdt, odt, scale, state):
+    units = []
+    for k, n in enumerate(sizes):
+        u = F.FlatParamUnit([("w", (n,))], world, gdt, odt, device=DEV, n_full=2, optimizer="sgd", state_dtype=state)
+        u.load_master([rand(n, F32, 50 + k, 0.1)])
+        u.exp_avg[:n] = rand(n, F32, 60 + k, 1e-3)
+        for r in range(world):
+            u.load_grad(r, [rand(n, F32, 70 + 10 * k + r, 1e-2 * scale).to(gdt)])
+        units.append(u)
+    return units
