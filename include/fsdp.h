@@ -501,8 +501,8 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  * products, the exponentials are held in fp16 relative to the largest of 64
  * columns before that. fp32 heads: every operand as three bf16 parts, the
  * products as exact as fp32's (an infinite operand counts as the largest
- * bf16 value). Calls of up to 8 tokens for losses alone form plain fp32 dot
- * products.
+ * bf16 value). Calls of a few tokens (4; 24 of an fp32 head) for losses
+ * alone form plain fp32 dot products.
  *   hidden       device, tokens rows of dim elements at stride ld_hidden.
  *   weight       device, vocab rows of dim elements at stride ld_weight.
  *                Rows that are not 16-byte aligned are packed into the

@@ -409,7 +409,7 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     memset(&p, 0, sizeof(p));
     p.f32 = a.dtype == FSDP_F32;
     p.grad = a.d_hidden != nullptr || a.d_weight != nullptr;
-    p.few = !p.grad && a.tokens <= kFewRows;
+    p.few = !p.grad && a.tokens <= few_rows(a.dtype);
     p.pack_x = !p.few && (p.f32 || !direct(a.hidden, a.ld_hidden));
     p.pack_w = !p.few && (p.f32 || !direct(a.weight, a.ld_weight));
     p.ldv = round_up(a.vocab, 64);
@@ -417,7 +417,7 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     p.spans = p.few ? few_blocks(a.vocab) : ceil_div(a.vocab, kSpan);
     const int64_t planes = p.f32 ? 3 : 1;
     const int64_t per_row = p.ldv * (p.f32 ? 10 : 2);  // exponentials, and the planes of an fp32 head
-    int64_t band = a.band;
+    int64_t band = p.few ? a.tokens : a.band;  // (a few rows are one band whatever was asked for)
     if (band == 0) {
         // gradients: what fits the default budget; losses alone: the statistics
         // (8 bytes a span and row) stay below it for any band this size

@@ -499,7 +499,7 @@ fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUte
         once.mark(dev);
     }
     const int64_t total = int64_t(g.tiles_m) * g.tiles_n * g.splits;
-    if (total < 1 || total > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
+    if (total < 1 || total > 0x3fffffff) return FSDP_ERR_INVALID_ARG;  // (the kernel's tile counter adds to it)
     const int64_t pairs = sm_count() / 2;
     const unsigned grid = static_cast<unsigned>(2 * (total < pairs ? total : (pairs > 0 ? pairs : 1)));
     return launch_chained(gemm_kernel<AMN, BMN, EP, DT>, grid, kThreads, smem_bytes(EP), s, a, b, out, g);

@@ -130,7 +130,7 @@ def test_gradients(F, T, V, D, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9, 17, 24, 25])
 @pytest.mark.parametrize("V,D", [(5003, 768), (129, 100), (33, 3)])
 def test_losses_of_a_few_rows(F, T, V, D, dt):
     x, w, y = inputs(T, V, D, dt, seed=T, ignored="some" if T > 4 else None)
@@ -185,6 +185,14 @@ def test_bands_of_tokens(F, T, band, dt):
     check(reference(x, w, y), dt, D, (V, T), loss, tok, dx, dw)
     loss, tok, _, _ = run(F, x, w, y, grad=False, band=band)
     check(reference(x, w, y), dt, D, (V, T), loss, tok)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_band_smaller_than_a_few_rows(F, dt):
+    for T, band in ((3, 1), (4, 2), (20, 7)):
+        x, w, y = inputs(T, 300, 64, dt, seed=T)
+        loss, tok, _, _ = run(F, x, w, y, grad=False, band=band)
+        check(reference(x, w, y), dt, 64, (300, T), loss, tok)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
