@@ -510,7 +510,7 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  *   targets      device int64, tokens.
  *   dtype        fsdp_dtype of hidden, weight and both gradients.
  *   band         tokens worked on together; 0: as many as keep the 16-bit
- *                exponentials within 2 GiB. A gradient call of more tokens
+ *                exponentials within 4 GiB. A gradient call of more tokens
  *                than that adds the bands' weight gradients in fp32 in the
  *                workspace (4 * vocab * dim bytes).
  *   loss         device fp32 scalar. token_loss: device fp32, tokens, or NULL.
@@ -519,7 +519,8 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  *   wait_timeouts  device uint32 or NULL: incremented by each bounded wait of
  *                this call that gave up (see "Bounded waits" above; this
  *                call's waits show here only).
- * No output may overlap an input or another output. tokens may be 0. */
+ * No output may overlap an input or another output. tokens may be 0. hidden
+ * and weight in host memory are refused (FSDP_ERR_INVALID_ARG). */
 typedef enum { FSDP_LOSS_MEAN = 0, FSDP_LOSS_SUM = 1 } fsdp_loss_reduction;
 
 typedef struct {

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float *part, int splits
 
 // ---------------------------------------------------------------- host: the plan
 
-constexpr int64_t kDefaultBandBytes = int64_t(2) << 30;
+constexpr int64_t kDefaultBandBytes = int64_t(4) << 30;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -424,6 +424,9 @@ Plan make_plan(const fsdp_head_loss_args &a) {
         band = p.grad ? kDefaultBandBytes / per_row : kDefaultBandBytes / (8 * p.spans);
         band = band / kTileM * kTileM;
         if (band < kTileM) band = kTileM;
+        // as many bands as that takes, of nearly equal length
+        const int64_t each = ceil_div(a.tokens, ceil_div(a.tokens, band));
+        band = round_up(each, kTileM) < band ? round_up(each, kTileM) : band;
     }
     p.band = band < a.tokens ? band : a.tokens;
     p.bands = ceil_div(a.tokens, p.band);
@@ -865,6 +868,8 @@ FSDP_API fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *works
                              a.d_weight ? ((a.vocab - 1) * a.ld_d_weight + a.dim) * size : 0};
     for (int i = 0; i < 7; ++i)
         if (overlaps(used[i], bytes[i], workspace, static_cast<size_t>(p.bytes))) return FSDP_ERR_INVALID_ARG;
+    // the operands' tiles are bulk copies between device buffers
+    if (host_resident(a.hidden) || host_resident(a.weight)) return FSDP_ERR_INVALID_ARG;
     return loss::run(a, p, static_cast<uint8_t *>(workspace), s);
 }
 

@@ -15,33 +15,38 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from .fsdp import _check, _counter, _on_current_device, _stream, dtype_code
+from .fsdp import _check, _counter, _on_current_device, dtype_code
 
 __all__ = ["HeadLoss", "fsdp_head_loss"]
 
 _REDUCTIONS = {"mean": _lib.FSDP_LOSS_MEAN, "sum": _lib.FSDP_LOSS_SUM}
 
 
-def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype) -> Tuple[int, int]:
-    """Address and row stride of a [rows, cols] CUDA matrix whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or tuple(t.shape) != (rows, cols):
+def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype, device: int) -> Tuple[int, int]:
+    """Address and row stride of a [rows, cols] matrix on the current device whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        _refuse_device(t, name)
+    if t.dtype != dtype or t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}] of {dtype}")
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and rows > 0 and t.stride(1) != 1) or ld < cols:
+    stride = t.stride()
+    ld = stride[0] if rows > 1 else cols
+    if (cols > 1 and rows > 0 and stride[1] != 1) or ld < cols:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    _on_current_device(t, name)
     return t.data_ptr(), ld
 
 
-def _vector(t: torch.Tensor, name: str, numel: int, dtype: torch.dtype) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if t.dtype != dtype or t.numel() != numel:
-        raise ValueError(f"{name} must hold {numel} elements of {dtype}")
-    _on_current_device(t, name)
+def _vector(t: torch.Tensor, name: str, numel: int, dtype: torch.dtype, device: int) -> int:
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        _refuse_device(t, name)
+    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {numel} contiguous elements of {dtype}")
     return t.data_ptr()
+
+
+def _refuse_device(t, name: str) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    _on_current_device(t, name)
 
 
 def _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, ignore_index, reduction, grad_scale, band,
@@ -53,24 +58,28 @@ def _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, ignore_
     T, D = hidden.shape
     V = weight.shape[0]
     dt = hidden.dtype
+    if not hidden.is_cuda:
+        _refuse_device(hidden, "hidden")
+    cur = torch.cuda.current_device()
     a = _lib.FsdpHeadLossArgs()
     a.dtype = dtype_code(dt)
     a.tokens, a.vocab, a.dim = T, V, D
-    a.hidden, a.ld_hidden = _matrix(hidden, "hidden", T, D, dt)
-    a.weight, a.ld_weight = _matrix(weight, "weight", V, D, dt)
-    a.targets = _vector(targets, "targets", T, torch.int64)
-    a.loss = _vector(loss, "loss", 1, torch.float32)
+    a.hidden, a.ld_hidden = _matrix(hidden, "hidden", T, D, dt, cur)
+    a.weight, a.ld_weight = _matrix(weight, "weight", V, D, dt, cur)
+    a.targets = _vector(targets, "targets", T, torch.int64, cur)
+    a.loss = _vector(loss, "loss", 1, torch.float32, cur)
     if token_loss is not None:
-        a.token_loss = _vector(token_loss, "token_loss", T, torch.float32)
+        a.token_loss = _vector(token_loss, "token_loss", T, torch.float32, cur)
     if d_hidden is not None:
-        a.d_hidden, a.ld_d_hidden = _matrix(d_hidden, "d_hidden", T, D, dt)
+        a.d_hidden, a.ld_d_hidden = _matrix(d_hidden, "d_hidden", T, D, dt, cur)
     if d_weight is not None:
-        a.d_weight, a.ld_d_weight = _matrix(d_weight, "d_weight", V, D, dt)
+        a.d_weight, a.ld_d_weight = _matrix(d_weight, "d_weight", V, D, dt, cur)
     a.ignore_index = int(ignore_index)
     a.reduction = _REDUCTIONS[reduction]
     a.grad_scale = float(grad_scale)
     a.band = int(band)
-    a.wait_timeouts = _counter(wait_timeouts, "wait_timeouts")
+    if wait_timeouts is not None:
+        a.wait_timeouts = _counter(wait_timeouts, "wait_timeouts")
     return a
 
 
@@ -86,9 +95,8 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return buf.narrow(0, -buf.data_ptr() % 1024, nbytes)
 
 
-def _launch(a: _lib.FsdpHeadLossArgs, workspace: torch.Tensor, stream) -> None:
-    _check(_lib.load().fsdp_head_loss(ctypes.byref(a), workspace.data_ptr(), workspace.numel(), _stream(stream)),
-           "fsdp_head_loss")
+def _launch(a: _lib.FsdpHeadLossArgs, address: int, nbytes: int, stream: torch.cuda.Stream) -> int:
+    return _lib.load().fsdp_head_loss(ctypes.byref(a), address, nbytes, stream.cuda_stream)
 
 
 def fsdp_head_loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, loss: torch.Tensor,
@@ -105,7 +113,7 @@ def fsdp_head_loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
               band, wait_timeouts)
     ws = _workspace(_workspace_bytes(a), hidden.device)
     s = stream if stream is not None else torch.cuda.current_stream()
-    _launch(a, ws, s)
+    _check(_launch(a, ws.data_ptr(), ws.numel(), s), "fsdp_head_loss")
     ws.record_stream(s)
 
 
@@ -115,7 +123,7 @@ class HeadLoss:
     vocab, dim, dtype: the weight's shape and the dtype of hidden, weight and
     gradients. max_tokens: the most rows of a call. grad: whether gradients
     will be asked for (the workspace is sized for it). band: rows worked on
-    together (0: as many as keep the 16-bit exponentials within 2 GiB).
+    together (0: as many as keep the 16-bit exponentials within 4 GiB).
     ignore_index, reduction ("mean" over the rows that count, or "sum") as in
     fsdp_head_loss. The workspace grows by itself, once, when a call needs
     more (rows that are not 16-byte aligned are packed into it). Calls on one
@@ -141,7 +149,11 @@ class HeadLoss:
         if grad:
             a.d_hidden, a.d_weight = 5 * step, 6 * step
         a.grad_scale = 1.0
-        self._ws = _workspace(_workspace_bytes(a), self.device)
+        self._allocate(_workspace_bytes(a))
+
+    def _allocate(self, nbytes: int) -> None:
+        self._ws = _workspace(nbytes, self.device)
+        self._ws_at, self._ws_bytes = self._ws.data_ptr(), nbytes
         self._ws_stream = torch.cuda.current_stream(self.device).cuda_stream
 
     def forward(self, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
@@ -176,11 +188,13 @@ class HeadLoss:
                     token_loss = torch.empty(hidden.shape[0], dtype=torch.float32, device=hidden.device)
         a = _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, self.ignore_index, self.reduction,
                   grad_scale, self.band, wait_timeouts)
-        need = _workspace_bytes(a)
-        if need > self._ws.numel():
-            self._ws = _workspace(need, self.device)
-            self._ws_stream = torch.cuda.current_stream(self.device).cuda_stream
         if s.cuda_stream != self._ws_stream:
             self._ws.record_stream(s)  # freed only after this call's work
-        _launch(a, self._ws, s)
+        status = _launch(a, self._ws_at, self._ws_bytes, s)
+        if status == _lib.FSDP_ERR_INVALID_ARG and _workspace_bytes(a) > self._ws_bytes:
+            self._allocate(_workspace_bytes(a))
+            if s.cuda_stream != self._ws_stream:
+                self._ws.record_stream(s)
+            status = _launch(a, self._ws_at, self._ws_bytes, s)
+        _check(status, "fsdp_head_loss")
         return loss, token_loss
