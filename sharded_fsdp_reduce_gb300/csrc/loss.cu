@@ -378,15 +378,16 @@ struct Plan {
 
 // How many pieces a product's K is cut into: with few tiles most pairs would
 // idle, and with little more than a multiple of the pairs the last round is
-// nearly empty. Takes the least of rounds of K blocks (about 0.3 us each)
-// plus the fp32 partial results written and read (about 6 TB/s).
-int choose_splits(int64_t tiles, int64_t kblocks, int64_t m, int64_t n) {
+// nearly empty. Takes the least of rounds of K blocks (about 0.3 us for each
+// of its plane products) plus the fp32 partial results written and read (about
+// 6 TB/s).
+int choose_splits(int64_t tiles, int64_t kblocks, int products, int64_t m, int64_t n) {
     const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
     int best = 1;
     double least = 0.0;
-    for (int s = 1; s <= 32 && (s == 1 || kblocks / s >= 8); ++s) {
+    for (int s = 1; s <= 32 && (s == 1 || kblocks * products / s >= 8); ++s) {
         const double rounds = static_cast<double>(ceil_div(tiles * s, pairs));
-        double us = rounds * (static_cast<double>(ceil_div(kblocks, s)) * 0.3 + 2.0);
+        double us = rounds * (static_cast<double>(ceil_div(kblocks, s)) * products * 0.3 + 2.0);
         if (s > 1) us += 4.0 + static_cast<double>(m) * n * 8.0 * s / 6.0e6;
         if (s == 1 || us < least) {
             least = us;
@@ -436,13 +437,13 @@ Plan make_plan(const fsdp_head_loss_args &a) {
         p.blocks += ceil_div(rows, kRows);
     }
     p.splits_x = p.splits_w = 1;
-    const int64_t pairs = p.f32 ? 6 : 1;
+    const int products = p.f32 ? 6 : 1;
     if (a.d_hidden)
         p.splits_x = choose_splits(ceil_div(p.band, kTileM) * ceil_div(a.dim, kTileN),
-                                   ceil_div(a.vocab, kBlockK) * pairs, p.band, p.ldd);
+                                   ceil_div(a.vocab, kBlockK), products, p.band, p.ldd);
     if (a.d_weight && p.bands == 1)
         p.splits_w = choose_splits(ceil_div(a.vocab, kTileM) * ceil_div(a.dim, kTileN),
-                                   ceil_div(p.band, kBlockK) * pairs, a.vocab, p.ldd);
+                                   ceil_div(p.band, kBlockK), products, a.vocab, p.ldd);
     int64_t at = 0;
     auto take = [&at](int64_t bytes) {
         const int64_t here = at;
@@ -495,7 +496,8 @@ EncodeFn encode_fn() {
 }
 
 // Rows of `cols` elements at stride ld, `planes` of them; boxes of box_bytes
-// (128, or 64) by box_rows, swizzled over as many bytes, zeros outside.
+// (128, or 64) by box_rows by all planes, swizzled over as many bytes, zeros
+// outside.
 fsdp_status make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t cols, int64_t rows,
                      int64_t planes, int64_t ld, int64_t plane, int box_rows, int box_bytes = 128) {
     const EncodeFn fn = encode_fn();
@@ -504,7 +506,8 @@ fsdp_status make_map(CUtensorMap *map, CUtensorMapDataType type, const void *bas
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(planes)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * size), static_cast<cuuint64_t>(plane * size)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / size), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / size), static_cast<cuuint32_t>(box_rows),
+                               static_cast<cuuint32_t>(planes)};
     const cuuint32_t unit[3] = {1, 1, 1};
     const CUresult r = fn(map, type, 3, const_cast<void *>(base), dims, strides, box, unit,
                           CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -564,7 +567,7 @@ fsdp_status run_product(const Product &q, const Plan &p, const fsdp_head_loss_ar
     g.M = q.M;
     g.N = q.N;
     g.kblocks = static_cast<int32_t>(ceil_div(q.K, kBlockK));
-    g.pairs = p.f32 ? 6 : 1;
+    g.planes = p.f32 ? 3 : 1;
     g.tiles_m = static_cast<int32_t>(ceil_div(q.M, kTileM));
     g.tiles_n = static_cast<int32_t>(ceil_div(q.N, kTileN));
     g.splits = q.splits;
@@ -697,7 +700,7 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         g.M = rows;
         g.N = V;
         g.kblocks = static_cast<int32_t>(ceil_div(D, kBlockK));
-        g.pairs = p.f32 ? 6 : 1;
+        g.planes = p.f32 ? 3 : 1;
         g.tiles_m = static_cast<int32_t>(ceil_div(rows, kTileM));
         g.tiles_n = static_cast<int32_t>(ceil_div(V, kTileN));
         g.splits = 1;

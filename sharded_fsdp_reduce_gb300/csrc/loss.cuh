@@ -28,8 +28,8 @@ enum Orders { kLogits, kHiddenGrad, kWeightGrad };
 
 struct GemmArgs {
     int64_t M, N;          // valid rows and columns
-    int32_t kblocks;       // K blocks per operand pair
-    int32_t pairs;         // 1, or 6 plane pairs of an fp32 head
+    int32_t kblocks;
+    int32_t planes;        // 1, or 3 bf16 planes of an fp32 head's operands
     int32_t tiles_m, tiles_n, splits;
     int32_t k_each, k_more;  // K blocks of a split, and the splits that have one more
     int32_t group;         // tiles of the fast dimension visited together

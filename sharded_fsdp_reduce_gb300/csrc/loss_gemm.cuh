@@ -22,9 +22,12 @@
 // thread), columns 64 ((w - 4) / 4) .. + 63.
 //
 // An fp32 operand is held as three bf16 planes (its leading, middle and last
-// 8 bits); the K loop then runs over the six plane pairs whose products reach
+// 8 bits). A stage then holds all three planes of both operands (96 KB, two
+// stages), and each K block issues the six plane pairs whose products reach
 // 2^-16 of the leading one, smallest first, into the same accumulator. What it
-// leaves out is below 2^-23 of the product of the operands' magnitudes.
+// leaves out is below 2^-23 of the product of the operands' magnitudes. (K
+// loops over one pair after the other read every plane twice: 512 x 32000 x
+// 1280 with its gradients 610 us, with planes side by side 573.)
 //
 // Every wait gives up after about a second, records itself and makes the pair
 // leave; the result is then incomplete and the counter says so.
@@ -44,16 +47,18 @@ constexpr int kEpilogueWarps = 16;
 // little off products of few tiles, but cost long ones: 4096 x 128000 x 8192
 // with its gradients 15.7 ms with these, 15.9 with one more each; the hidden
 // gradient of 1021 x 50257 x 768 wants 6 (54 against 57 us with 5).
-constexpr int stages(int epilogue) { return epilogue == kExp ? 5 : 6; }
+constexpr int stages(int epilogue, int planes) { return planes == 3 ? 2 : epilogue == kExp ? 5 : 6; }
 constexpr int kMaxStages = 6;
 // K blocks summed in tensor memory before the sum moves to registers. The
 // tensor cores' own sum loses bits at every K = 16 (a chain of 5120 / 16 adds
 // left a loss 2.4e-6 off, 64 bits against it); chains of 512 / 16 joined by
 // rounded fp32 adds do not show in fp32 results, chains of 2048 / 16 not in
 // 16-bit ones. Each move costs the products about 1 %.
-constexpr int chunk_blocks(int epilogue, int dtype) { return epilogue == kScale && dtype != FSDP_F32 ? 32 : 8; }
-constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // one operand's half tile: 16 KB
-constexpr uint32_t kStageBytes = 2 * kHalfBytes;         // per CTA
+constexpr int chunk_blocks(int epilogue, int dtype, int planes) {
+    return planes == 3 ? 1 : epilogue == kScale && dtype != FSDP_F32 ? 32 : 8;  // (a block of planes is 24 adds)
+}
+constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // one plane of one operand's half tile: 16 KB
+constexpr uint32_t stage_bytes(int planes) { return 2 * planes * kHalfBytes; }  // per CTA
 constexpr uint32_t kTensorCols = 512;                    // two accumulators of 256 columns
 constexpr long long kWaitCycles = 2000000000ll;          // about one second of SM clocks
 
@@ -65,14 +70,19 @@ struct Barriers {
 };
 
 constexpr uint32_t kBoxBytes = 32 * 64;                  // one warp's store box: 32 rows of 64 bytes
-constexpr size_t smem_bytes(int epilogue) {
-    return 1024 + stages(epilogue) * kStageBytes + (epilogue == kExp ? kEpilogueWarps * kBoxBytes : 0) +
+constexpr size_t smem_bytes(int epilogue, int planes) {
+    return 1024 + stages(epilogue, planes) * stage_bytes(planes) + (epilogue == kExp ? kEpilogueWarps * kBoxBytes : 0) +
            sizeof(Barriers);
 }
-static_assert(smem_bytes(kExp) <= 232448 && smem_bytes(kScale) <= 232448, "shared memory of one block");
+static_assert(smem_bytes(kExp, 1) <= 232448 && smem_bytes(kScale, 1) <= 232448 && smem_bytes(kExp, 3) <= 232448, "shared memory of one block");
 
-// The (A, B) planes of the six pairs, low nibble first, smallest products first.
+// The products of one K block of three planes: the (A, B) planes of each, low
+// nibble first.
 constexpr uint32_t kPlanesA = 0x001021, kPlanesB = 0x010201;
+constexpr int plane_products(int planes) { return planes == 3 ? 6 : 1; }
+constexpr uint32_t plane_of(uint32_t list, int planes, int product) {
+    return planes == 3 ? (list >> (4 * product)) & 15 : 0;
+}
 
 struct Tile {
     int m, n, split;
@@ -93,7 +103,7 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs &g, int t) {
     return r;
 }
 
-// The K blocks (of all operand pairs) of a split.
+// The K blocks of a split.
 __device__ __forceinline__ void k_range(const GemmArgs &g, int split, int &begin, int &end) {
     begin = split * g.k_each + min(split, g.k_more);
     end = begin + g.k_each + (split < g.k_more ? 1 : 0);
@@ -265,12 +275,11 @@ __device__ __forceinline__ void scaled_span(const GemmArgs &g, float *v, int64_t
 // what it issues with stays in uniform registers: a single thread's loop over
 // both operands took 830 cycles a K block, over one 500; the products take 512
 // and a load that comes late has to be made up.
-template <int MN, bool A, int kStages>
+template <int MN, bool A, int P, int kStages>
 __device__ __forceinline__ void load_operand(const GemmArgs &g, const CUtensorMap *map, uint8_t *smem, Barriers *b,
                                              uint32_t rank, int first, int total, int step) {
     const uint32_t full = tc::peer_addr(tc::smem_addr(&b->full[0]), 0), to = tc::smem_addr(smem);
-    const int kblocks = g.kblocks;
-    const bool planes = g.pairs > 1, expects = A && rank == 0;
+    const bool expects = A && rank == 0;
     uint32_t *timeouts = g.timeouts;
     int stage = 0;
     uint32_t phase = 1;
@@ -279,24 +288,19 @@ __device__ __forceinline__ void load_operand(const GemmArgs &g, const CUtensorMa
         int k0, k1;
         k_range(g, x.split, k0, k1);
         const int at = (A ? x.m * kTileM : x.n * kTileN) + static_cast<int>(rank) * 128;
-        int pair = planes ? k0 / kblocks : 0;
-        int kb = k0 - pair * kblocks;
         for (int k = k0; k < k1; ++k) {
             if (!wait(&b->empty[stage], phase, b, timeouts)) return;
-            const int z = planes ? ((A ? kPlanesA : kPlanesB) >> (4 * pair)) & 15 : 0;
-            const uint32_t bar = full + stage * static_cast<uint32_t>(sizeof(uint64_t)), dst = to + stage * kStageBytes;
+            const uint32_t bar = full + stage * static_cast<uint32_t>(sizeof(uint64_t));
+            const uint32_t dst = to + stage * stage_bytes(P);
             if (tc::elect_one()) {
-                if (expects) tma::mbar_arrive_expect_tx(&b->full[stage], 2 * kStageBytes);
+                if (expects) tma::mbar_arrive_expect_tx(&b->full[stage], 2 * stage_bytes(P));
+                // boxes hold all planes: K-major 128 rows each, MN-major twice 64 columns
                 if constexpr (MN) {
-                    tc::load_tile(dst, map, at, kb * kBlockK, z, bar);
-                    tc::load_tile(dst + kHalfBytes / 2, map, at + 64, kb * kBlockK, z, bar);
+                    tc::load_tile(dst, map, at, k * kBlockK, 0, bar);
+                    tc::load_tile(dst + P * (kHalfBytes / 2), map, at + 64, k * kBlockK, 0, bar);
                 } else {
-                    tc::load_tile(dst, map, kb * kBlockK, at, z, bar);
+                    tc::load_tile(dst, map, k * kBlockK, at, 0, bar);
                 }
-            }
-            if (++kb == kblocks) {
-                kb = 0;
-                ++pair;
             }
             if (++stage == kStages) {
                 stage = 0;
@@ -319,7 +323,7 @@ __device__ __forceinline__ void load_operand(const GemmArgs &g, const CUtensorMa
 // whole warp runs the loop and one elected thread issues: what it issues with
 // then stays in uniform registers (a single thread's loop moved every operand
 // there first, 560 cycles a K block against the products' 512).
-template <int AMN, int BMN, int kStages, int kChunk>
+template <int AMN, int BMN, int P, int kStages, int kChunk>
 __device__ __forceinline__ void issue_products(const GemmArgs &g, uint8_t *smem, Barriers *b, uint32_t tensor,
                                                int first, int total, int step) {
     const uint32_t idesc = tc::instruction(0, AMN, BMN, kTileM, kTileN) |
@@ -329,8 +333,11 @@ __device__ __forceinline__ void issue_products(const GemmArgs &g, uint8_t *smem,
     constexpr uint32_t kStepA = (AMN ? 2048 : 32) >> 4, kStepB = (BMN ? 2048 : 32) >> 4;
     constexpr uint32_t kHigh = tc::operand_high(1024);
     const uint32_t sa = tc::smem_addr(smem);
-    const uint32_t a0 = tc::operand_low(sa, AMN ? kHalfBytes / 2 : 16);
-    const uint32_t b0 = tc::operand_low(sa + kHalfBytes, BMN ? kHalfBytes / 2 : 16);
+    const uint32_t a0 = tc::operand_low(sa, AMN ? P * (kHalfBytes / 2) : 16);
+    const uint32_t b0 = tc::operand_low(sa + P * kHalfBytes, BMN ? P * (kHalfBytes / 2) : 16);
+    // from one plane of an operand to the next
+    constexpr uint32_t kPlaneA = (AMN ? kHalfBytes / 2 : kHalfBytes) >> 4;
+    constexpr uint32_t kPlaneB = (BMN ? kHalfBytes / 2 : kHalfBytes) >> 4;
     const int tiles = g.tiles_m * g.tiles_n, splits = g.splits;
     uint32_t *timeouts = g.timeouts;
     int k0, k1;
@@ -347,11 +354,15 @@ __device__ __forceinline__ void issue_products(const GemmArgs &g, uint8_t *smem,
             for (int k = c; k < end; ++k) {
                 if (!wait(&b->full[stage], phase, b, timeouts)) return;
                 tc::fence_after();
-                const uint32_t da = a0 + stage * (kStageBytes >> 4), db = b0 + stage * (kStageBytes >> 4);
+                const uint32_t da = a0 + stage * (stage_bytes(P) >> 4), db = b0 + stage * (stage_bytes(P) >> 4);
                 if (tc::elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < kBlockK / 16; ++j)
-                        tc::mma_pair(d, da + j * kStepA, db + j * kStepB, kHigh, idesc, k > c || j > 0);
+                    for (int q = 0; q < plane_products(P); ++q)
+#pragma unroll
+                        for (int j = 0; j < kBlockK / 16; ++j)
+                            tc::mma_pair(d, da + plane_of(kPlanesA, P, q) * kPlaneA + j * kStepA,
+                                         db + plane_of(kPlanesB, P, q) * kPlaneB + j * kStepB, kHigh, idesc,
+                                         k > c || q > 0 || j > 0);
                     tc::commit_pair(&b->empty[stage]);
                     if (k + 1 == end) tc::commit_pair(&b->acc_full[buf]);
                 }
@@ -366,14 +377,14 @@ __device__ __forceinline__ void issue_products(const GemmArgs &g, uint8_t *smem,
     }
 }
 
-template <int AMN, int BMN, int EP, int DT>
+template <int AMN, int BMN, int EP, int DT, int P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_out, const __grid_constant__ GemmArgs g) {
-    constexpr int kStages = stages(EP), kChunk = chunk_blocks(EP, DT);
+    constexpr int kStages = stages(EP, P), kChunk = chunk_blocks(EP, DT, P);
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *boxes = smem + kStages * kStageBytes;
+    uint8_t *boxes = smem + kStages * stage_bytes(P);
     Barriers *b = reinterpret_cast<Barriers *>(boxes + (EP == kExp ? kEpilogueWarps * kBoxBytes : 0));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // (uniform)
     const uint32_t rank = tc::cluster_rank();
@@ -413,11 +424,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0)
-            load_operand<AMN, true, kStages>(g, &map_a, smem, b, rank, first, total, step);
+            load_operand<AMN, true, P, kStages>(g, &map_a, smem, b, rank, first, total, step);
         else if (warp == 3)
-            load_operand<BMN, false, kStages>(g, &map_b, smem + kHalfBytes, b, rank, first, total, step);
+            load_operand<BMN, false, P, kStages>(g, &map_b, smem + P * kHalfBytes, b, rank, first, total, step);
         else if (warp == 1 && rank == 0)
-            issue_products<AMN, BMN, kStages, kChunk>(g, smem, b, tensor, first, total, step);
+            issue_products<AMN, BMN, P, kStages, kChunk>(g, smem, b, tensor, first, total, step);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int quarter = warp % 4, part = (warp - 4) / 4;
@@ -483,18 +494,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 2) tc::free_pair(tensor, kTensorCols);
 }
 
-template <int AMN, int BMN, int EP, int DT>
+template <int AMN, int BMN, int EP, int DT, int P>
 fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, GemmArgs g,
                           cudaStream_t s) {
-    const int32_t blocks = g.kblocks * g.pairs;
-    g.k_each = blocks / g.splits;
-    g.k_more = blocks % g.splits;
+    g.k_each = g.kblocks / g.splits;
+    g.k_more = g.kblocks % g.splits;
     static PerDeviceOnce once;
     const int dev = current_device();
     if (!once.is_done(dev)) {
-        const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<AMN, BMN, EP, DT>,
+        const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<AMN, BMN, EP, DT, P>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem_bytes(EP)));
+                                                   static_cast<int>(smem_bytes(EP, P)));
         if (e != cudaSuccess) return cuda_status(e);
         once.mark(dev);
     }
@@ -502,7 +512,7 @@ fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUte
     if (total < 1 || total > 0x3fffffff) return FSDP_ERR_INVALID_ARG;  // (the kernel's tile counter adds to it)
     const int64_t pairs = sm_count() / 2;
     const unsigned grid = static_cast<unsigned>(2 * (total < pairs ? total : (pairs > 0 ? pairs : 1)));
-    return launch_chained(gemm_kernel<AMN, BMN, EP, DT>, grid, kThreads, smem_bytes(EP), s, a, b, out, g);
+    return launch_chained(gemm_kernel<AMN, BMN, EP, DT, P>, grid, kThreads, smem_bytes(EP, P), s, a, b, out, g);
 }
 
 }  // namespace loss

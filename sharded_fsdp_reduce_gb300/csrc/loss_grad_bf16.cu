@@ -5,8 +5,8 @@ namespace fsdp {
 namespace loss {
 
 fsdp_status launch_grad_bf16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s) {
-    return o == kHiddenGrad ? launch_kernel<0, 1, kScale, FSDP_BF16>(a, b, a, g, s)
-                            : launch_kernel<1, 1, kScale, FSDP_BF16>(a, b, a, g, s);
+    return o == kHiddenGrad ? launch_kernel<0, 1, kScale, FSDP_BF16, 1>(a, b, a, g, s)
+                            : launch_kernel<1, 1, kScale, FSDP_BF16, 1>(a, b, a, g, s);
 }
 
 }  // namespace loss
