@@ -489,7 +489,7 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  *   d_hidden = g * d * weight,   d_weight = g * d^T * hidden
  *   g       = grad_scale / n (MEAN) or grad_scale (SUM)
  * n is the number of rows whose target is not ignore_index; the others have
- * loss 0 and no gradient. A target outside [0, vocab) that is not
+ * loss 0 and no gradient, whatever their hidden values are. A target outside [0, vocab) that is not
  * ignore_index makes its row's loss and gradients NaN. Both gradients are
  * overwritten, not added to; the pair (weight, d_weight) may be views of a
  * unit's gathered buffer and of a rank's flat gradient buffer, whatever their
@@ -501,8 +501,8 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  * products, the exponentials are held in fp16 relative to the largest of 64
  * columns before that. fp32 heads: every operand as three bf16 parts, the
  * products as exact as fp32's (an infinite operand counts as the largest
- * bf16 value). Calls of a few tokens (4; 24 of an fp32 head) for losses
- * alone form plain fp32 dot products.
+ * bf16 value). A few tokens (4, or 24 of an fp32 head, for losses alone; 8
+ * of an fp32 head with gradients) are plain fp32 dot products.
  *   hidden       device, tokens rows of dim elements at stride ld_hidden.
  *   weight       device, vocab rows of dim elements at stride ld_weight.
  *                Rows that are not 16-byte aligned are packed into the

@@ -16,13 +16,13 @@ __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.laun
 // Launch a kernel that waits for its predecessor on the stream itself
 // (wait_previous) and may start before that one has ended.
 template <class... Params, class... Args>
-fsdp_status launch_chained(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+fsdp_status launch_chained(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
                            Args &&...args) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t config = {};
-    config.gridDim = dim3(grid);
+    config.gridDim = grid;
     config.blockDim = dim3(threads);
     config.dynamicSmemBytes = smem;
     config.stream = s;

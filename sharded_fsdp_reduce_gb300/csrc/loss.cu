@@ -303,21 +303,31 @@ template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __gri
 // ---------------------------------------------------------------- operands TMA cannot address
 
 // rows x cols at stride ld into 16-bit rows padded to ldp (a multiple of 8):
-// a copy for 16-bit types, three bf16 planes for fp32.
+// a copy for 16-bit types, three bf16 planes for fp32. With targets (hidden
+// states), rows that are ignored become zeros.
 template <bool F32>
 __global__ void __launch_bounds__(256) pack_kernel(const void *src, int64_t rows, int64_t cols, int64_t ld,
-                                                   uint16_t *dst, int64_t ldp, int64_t plane) {
+                                                   uint16_t *dst, int64_t ldp, int64_t plane,
+                                                   const int64_t *targets, int64_t ignore, bool vec) {
     const int64_t words = ldp / 8, total = rows * words;
     wait_previous();
     allow_next();
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
         const int64_t r = i / words, c = (i - r * words) * 8;
-        const int n = static_cast<int>(min(int64_t(8), cols - c));
+        const bool zero = targets != nullptr && targets[r] == ignore;
+        const int n = zero ? 0 : static_cast<int>(min(int64_t(8), cols - c));
         if constexpr (F32) {
             const float *s = static_cast<const float *>(src) + r * ld + c;
-            float p[3][8];
+            float x[8], p[3][8];
+            if (vec && n == 8) {
+                const float4 lo = *reinterpret_cast<const float4 *>(s), hi = *reinterpret_cast<const float4 *>(s + 4);
+                x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) split3(j < n ? s[j] : 0.0f, p[0][j], p[1][j], p[2][j]);
+                for (int j = 0; j < 8; ++j) x[j] = j < n ? s[j] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) split3(x[j], p[0][j], p[1][j], p[2][j]);
 #pragma unroll
             for (int z = 0; z < 3; ++z)
                 *reinterpret_cast<uint4 *>(dst + z * plane + r * ldp + c) =
@@ -325,6 +335,10 @@ __global__ void __launch_bounds__(256) pack_kernel(const void *src, int64_t rows
                                pack2<FSDP_BF16>(p[z][4], p[z][5]), pack2<FSDP_BF16>(p[z][6], p[z][7]));
         } else {
             const uint16_t *s = static_cast<const uint16_t *>(src) + r * ld + c;
+            if (vec && n == 8) {
+                *reinterpret_cast<uint4 *>(dst + r * ldp + c) = *reinterpret_cast<const uint4 *>(s);
+                continue;
+            }
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -410,8 +424,12 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     memset(&p, 0, sizeof(p));
     p.f32 = a.dtype == FSDP_F32;
     p.grad = a.d_hidden != nullptr || a.d_weight != nullptr;
-    p.few = !p.grad && a.tokens <= few_rows(a.dtype);
-    p.pack_x = !p.few && (p.f32 || !direct(a.hidden, a.ld_hidden));
+    // (the few rows' gradient kernels take up to 2^16 column tiles)
+    p.few = a.tokens <= few_rows(a.dtype, p.grad) && a.dim <= (1 << 22);
+    // the weight gradient multiplies every row's hidden values: the packed copy
+    // has zeros in ignored rows, so that what lies there (padding that was never
+    // written) does not matter
+    p.pack_x = !p.few && (p.f32 || a.d_weight != nullptr || !direct(a.hidden, a.ld_hidden));
     p.pack_w = !p.few && (p.f32 || !direct(a.weight, a.ld_weight));
     p.ldv = round_up(a.vocab, 64);
     p.ldd = round_up(a.dim, 64);
@@ -438,10 +456,12 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     }
     p.splits_x = p.splits_w = 1;
     const int products = p.f32 ? 6 : 1;
-    if (a.d_hidden)
+    if (a.d_hidden && p.few)
+        p.splits_x = static_cast<int>(few_parts(a.vocab, a.dim));
+    else if (a.d_hidden)
         p.splits_x = choose_splits(ceil_div(p.band, kTileM) * ceil_div(a.dim, kTileN),
                                    ceil_div(a.vocab, kBlockK), products, p.band, p.ldd);
-    if (a.d_weight && p.bands == 1)
+    if (a.d_weight && p.bands == 1 && !p.few)
         p.splits_w = choose_splits(ceil_div(a.vocab, kTileM) * ceil_div(a.dim, kTileN),
                                    ceil_div(p.band, kBlockK), products, a.vocab, p.ldd);
     int64_t at = 0;
@@ -462,8 +482,8 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     if (p.pack_w) p.w = take(2 * planes * a.vocab * p.ldd);
     if (p.grad) {
         p.e = take(p.band * p.ldv * (p.f32 ? 4 : 2));
-        p.d = p.f32 ? take(p.band * p.ldv * 6) : p.e;
-        const int64_t part_x = p.splits_x > 1 ? 4 * p.splits_x * p.band * p.ldd : 0;
+        p.d = p.f32 && !p.few ? take(p.band * p.ldv * 6) : p.e;
+        const int64_t part_x = p.splits_x > 1 || p.few ? 4 * p.splits_x * p.band * p.ldd : 0;
         const int64_t part_w = p.splits_w > 1 ? 4 * p.splits_w * a.vocab * p.ldd : 0;
         p.part = take(part_x > part_w ? part_x : part_w);
         if (a.d_weight && p.bands > 1) p.sum_w = take(4 * a.vocab * p.ldd);
@@ -531,11 +551,12 @@ struct Operand {
 };
 
 fsdp_status pack(const void *src, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t *dst, int64_t ldp,
-                 cudaStream_t s) {
+                 const int64_t *targets, int64_t ignore, cudaStream_t s) {
     const int grid = grid_of(rows * ldp / 8);
     uint16_t *d = reinterpret_cast<uint16_t *>(dst);
     return launch_chained(f32 ? pack_kernel<true> : pack_kernel<false>, static_cast<unsigned>(grid), 256, 0, s, src,
-                          rows, cols, ld, d, ldp, rows * ldp);
+                          rows, cols, ld, d, ldp, rows * ldp, targets, ignore,
+                          aligned(src, 16) && ld * (f32 ? 4 : 2) % 16 == 0);
 }
 
 fsdp_status launch_grad(int dtype, Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g,
@@ -622,7 +643,41 @@ fsdp_status run_few(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cu
     f.ld_rows = p.band;
     f.target_logit = reinterpret_cast<float *>(ws + p.target_logit);
     f.ticket = reinterpret_cast<uint32_t *>(ws + p.ticket);
+    f.logits = p.grad ? reinterpret_cast<float *>(ws + p.e) : nullptr;
+    f.ld_logits = p.ldv;
     return launch_few(f, a.dtype, s);
+}
+
+// The gradients of a few fp32 rows, from their logits and lse.
+fsdp_status run_few_grad(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaStream_t s) {
+    FewGradArgs f;
+    f.hidden = static_cast<const float *>(a.hidden);
+    f.weight = static_cast<const float *>(a.weight);
+    f.logits = reinterpret_cast<const float *>(ws + p.e);
+    f.lse2 = reinterpret_cast<const float *>(ws + p.lse2);
+    f.ld_hidden = a.ld_hidden;
+    f.ld_weight = a.ld_weight;
+    f.ld_logits = p.ldv;
+    f.rows = a.tokens;
+    f.vocab = a.vocab;
+    f.dim = a.dim;
+    f.targets = a.targets;
+    f.ignore = a.ignore_index;
+    f.part = reinterpret_cast<float *>(ws + p.part);
+    f.ld_part = p.ldd;
+    f.parts = p.splits_x;
+    f.d_weight = static_cast<float *>(a.d_weight);
+    f.ld_d_weight = a.ld_d_weight;
+    f.scale = reinterpret_cast<const float *>(ws + p.scale);
+    if (a.d_hidden) {
+        fsdp_status st = launch_few_dx(f, s);
+        if (st == FSDP_OK)
+            st = launch_chained(join_kernel<FSDP_F32>, static_cast<unsigned>(grid_of(a.tokens * p.ldd / 4)), 256, 0, s,
+                                static_cast<const float *>(f.part), p.splits_x, a.tokens * p.ldd, a.tokens, a.dim,
+                                p.ldd, f.scale, 1.0f, a.d_hidden, a.ld_d_hidden);
+        if (st != FSDP_OK) return st;
+    }
+    return a.d_weight ? launch_few_dw(f, s) : FSDP_OK;
 }
 
 // The rows' sums and losses, of one band.
@@ -657,8 +712,9 @@ fsdp_status run_rows(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, i
 fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaStream_t s) {
     int64_t block = 0;
     if (p.few) {
-        const fsdp_status few = run_few(a, p, ws, s);
-        return few != FSDP_OK ? few : run_rows(a, p, ws, 0, a.tokens, block, s);
+        fsdp_status few = run_few(a, p, ws, s);
+        if (few == FSDP_OK) few = run_rows(a, p, ws, 0, a.tokens, block, s);
+        return few == FSDP_OK && p.grad ? run_few_grad(a, p, ws, s) : few;
     }
     const int64_t D = a.dim, V = a.vocab;
     const int size = dtype_size(a.dtype);
@@ -667,11 +723,11 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
     Operand w{static_cast<const uint8_t *>(a.weight), a.ld_weight, V * a.ld_weight, 1};
     fsdp_status st = FSDP_OK;
     if (p.pack_x) {
-        st = pack(a.hidden, p.f32, a.tokens, D, a.ld_hidden, ws + p.x, p.ldd, s);
+        st = pack(a.hidden, p.f32, a.tokens, D, a.ld_hidden, ws + p.x, p.ldd, a.targets, a.ignore_index, s);
         x = Operand{ws + p.x, p.ldd, a.tokens * p.ldd, planes};
     }
     if (st == FSDP_OK && p.pack_w) {
-        st = pack(a.weight, p.f32, V, D, a.ld_weight, ws + p.w, p.ldd, s);
+        st = pack(a.weight, p.f32, V, D, a.ld_weight, ws + p.w, p.ldd, nullptr, 0, s);
         w = Operand{ws + p.w, p.ldd, V * p.ldd, planes};
     }
     if (st != FSDP_OK) return st;

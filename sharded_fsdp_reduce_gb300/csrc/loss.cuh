@@ -62,12 +62,13 @@ fsdp_status launch_grad_bf16(Orders o, const CUtensorMap &a, const CUtensorMap &
 fsdp_status launch_grad_f16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
 fsdp_status launch_grad_f32(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
 
-// Losses of a few rows (loss_few.cu): the statistics per block instead of
-// per span of columns. Up to where the matrix product takes over: 4 rows of
-// 50257 x 768 bf16 24 us against 27, 8 rows 43 against 26; an fp32 weight is
-// packed first for the product, so 24 rows of 32000 x 4096 fp32 take 322 us
-// against 475, of 50257 x 768 137 against 158.
-inline int64_t few_rows(int dtype) { return dtype == FSDP_F32 ? 24 : 4; }
+// A few rows (loss_few.cu): the statistics per block instead of per span of
+// columns. Up to where the matrix products take over: losses of 4 rows of
+// 50257 x 768 bf16 24 us against 27, of 8 rows 43 against 26. An fp32 weight is
+// packed first for the products: losses of 24 rows of 32000 x 4096 324 us
+// against 433, of 50257 x 768 137 against 142; gradients of 4 rows 362 against
+// 756 and 141 against 256, of 16 rows 950 against 762.
+inline int64_t few_rows(int dtype, bool grad) { return dtype == FSDP_F32 ? (grad ? 8 : 24) : (grad ? 0 : 4); }
 
 struct FewArgs {
     const void *hidden, *weight;
@@ -76,11 +77,28 @@ struct FewArgs {
     float *off, *sum;  // [blocks][ld_rows]
     int64_t ld_rows;
     float *target_logit;
+    float *logits;     // [rows][ld_logits], for the gradients, or NULL
+    int64_t ld_logits;
     uint32_t *ticket;  // cleared for the row kernel
 };
 
+struct FewGradArgs {
+    const float *hidden, *weight, *logits, *lse2;
+    int64_t ld_hidden, ld_weight, ld_logits, rows, vocab, dim;
+    const int64_t *targets;
+    int64_t ignore;
+    float *part;       // [parts][rows][ld_part]: the hidden gradient's sums
+    int64_t ld_part, parts;
+    float *d_weight;
+    int64_t ld_d_weight;
+    const float *scale;
+};
+
 int64_t few_blocks(int64_t vocab);
+int64_t few_parts(int64_t vocab, int64_t dim);
 fsdp_status launch_few(const FewArgs &a, int dtype, cudaStream_t s);
+fsdp_status launch_few_dx(const FewGradArgs &a, cudaStream_t s);
+fsdp_status launch_few_dw(const FewGradArgs &a, cudaStream_t s);
 
 }  // namespace loss
 }  // namespace fsdp

@@ -274,6 +274,34 @@ def test_nan_in_a_row_stays_in_its_row(F, T):
     assert math.isnan(float(run(F, x, w, y, grad=False)[0]))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,band", [(3, 0), (64, 0), (65, 0), (300, 0), (600, 256)])
+def test_what_lies_in_ignored_rows_does_not_matter(F, T, band, dt):
+    V, D = 700, 136
+    x, w, y = inputs(T, V, D, dt, ignored="some", seed=3)
+    y[0], y[1] = 5, IGNORE
+    ref = reference(x, w, y)
+    dirty = x.clone()
+    junk = torch.tensor([float("nan"), float("inf"), -float("inf"), 6e4], device=DEV).to(DT[dt])
+    dirty[y == IGNORE] = junk.repeat(D // 4)
+    loss, tok, dx, dw = run(F, dirty, w, y, band=band)
+    check(ref, dt, D, (V, T), loss, tok, dx, dw)
+    loss, tok, _, _ = run(F, dirty, w, y, grad=False, band=band)
+    check(ref, dt, D, (V, T), loss, tok)
+
+
+@pytest.mark.parametrize("T,V,D", [(1, 1, 1), (7, 65, 127), (16, 640, 256), (33, 1001, 131), (64, 3000, 516), (65, 200, 64)])
+def test_gradients_of_a_few_fp32_rows(F, T, V, D):
+    x, w, y = inputs(T, V, D, "f32", seed=T, ignored="some" if T > 4 else None, std=0.2)
+    loss, tok, dx, dw = run(F, x, w, y)
+    ref = reference(x, w, y)
+    check(ref, "f32", D, (V, T), loss, tok, dx, dw)
+    a = run(F, x, w, y)
+    assert torch.equal(a[2], dx) and torch.equal(a[3], dw)
+    loss, tok, dx, dw = run(F, x, w, y, reduction="sum", grad_scale=3.0)
+    check(reference(x, w, y, "sum", 3.0), "f32", D, (V, T), loss, tok, dx, dw)
+
+
 @pytest.mark.parametrize("T", [2, 130])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_vocabulary_entries_that_cannot_be_drawn(F, T, dt):
