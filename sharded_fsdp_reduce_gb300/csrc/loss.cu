@@ -24,6 +24,7 @@ namespace loss {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
 // fp16 gradients of the logits are held times 2^14: d is at most 1 in
 // magnitude, and a probability down to 2^-28 keeps all its bits.
 constexpr float kHalfGain = 16384.0f;
@@ -37,7 +38,7 @@ struct RowArgs {
     const float *target_logit;
     const int64_t *targets;
     int64_t rows, vocab, ignore;
-    float *lse2;             // log2-sum of the row's exponentials
+    float2 *row_state;       // {reference, sum}: the row's exponentials add up to sum * 2^reference
     float *token_loss;       // or NULL
     // the loss over all bands: block sums, joined by the last block
     double *part_sum;
@@ -129,13 +130,17 @@ __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowA
             float t = 0.0f;
             long long valid = 0;
             if (row < a.rows) {
-                const float lse2 = top + log2f(sum);
-                a.lse2[row] = lse2;
+                a.row_state[row] = make_float2(top, sum);
                 const int64_t y = a.targets[row];
                 if (y != a.ignore) {
                     valid = 1;
-                    // a target outside the vocabulary has no loss: it shows as NaN
-                    t = y >= 0 && y < a.vocab ? lse2 * kLn2 - a.target_logit[row] : NAN;
+                    // log sum - (target - reference), in one rounding after the
+                    // logarithm: both are small for a row that is sure of its
+                    // target. A target outside the vocabulary has no loss: it
+                    // shows as NaN.
+                    t = y >= 0 && y < a.vocab
+                            ? fmaf(-kLn2, fmaf(a.target_logit[row], kLog2e, -top), logf(sum))
+                            : NAN;
                 }
                 if (a.token_loss != nullptr) a.token_loss[row] = t;
             }
@@ -211,7 +216,8 @@ struct GradArgs {
     int64_t ld, rows, vocab;
     const float *off;        // [spans][ld_rows]
     int64_t ld_rows;
-    const float *lse2;
+    const float2 *row_state;
+    const float *target_logit;
     const int64_t *targets;
     int64_t ignore;
     uint32_t row_blocks;
@@ -237,6 +243,7 @@ constexpr int kGradCols = 512, kGradRows = 64;
 template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __grid_constant__ GradArgs a) {
     __shared__ float factor[kGradCols / kSpan][kGradRows];
     __shared__ int32_t hit[kGradRows];  // the target's column in this block, or -1; -2: no gradient
+    __shared__ float at_target[kGradRows];
     // from the last columns to the first, as the logits product left them in L2
     const uint32_t block = gridDim.x - 1 - blockIdx.x;
     const int64_t row0 = int64_t(block % a.row_blocks) * kGradRows;
@@ -248,13 +255,20 @@ template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __gri
         const int r = i % kGradRows, s = i / kGradRows;
         const int64_t row = row0 + r, span = col0 / kSpan + s;
         if (row < a.rows) {
-            // e * 2^(off - lse2) is the probability; a target outside the
-            // vocabulary makes the row's gradient NaN, as its loss is
+            // e * 2^(off - reference) / sum is the probability; a target outside
+            // the vocabulary makes the row's gradient NaN, as its loss is
             const int64_t y = a.targets[row], at = y - col0;
             const bool bad = y != a.ignore && (y < 0 || y >= a.vocab);
+            const float2 state = a.row_state[row];
             if (span * kSpan < a.vocab)
-                factor[s][r] = bad ? NAN : kGain * exp2f(a.off[span * a.ld_rows + row] - a.lse2[row]);
-            if (s == 0) hit[r] = y == a.ignore ? -2 : at >= 0 && at < kGradCols ? static_cast<int32_t>(at) : -1;
+                factor[s][r] = bad ? NAN : kGain * exp2f(a.off[span * a.ld_rows + row] - state.x) / state.y;
+            if (s == 0) {
+                hit[r] = y == a.ignore ? -2 : at >= 0 && at < kGradCols ? static_cast<int32_t>(at) : -1;
+                // the target's own d from its fp32 logit: near 1 the stored
+                // exponential's rounding would be all that is left of p - 1
+                if (hit[r] >= 0 && at + col0 < a.vocab)
+                    at_target[r] = kGain * (exp2f(fmaf(a.target_logit[row], kLog2e, -state.x)) / state.y - 1.0f);
+            }
         }
     }
     __syncthreads();
@@ -277,8 +291,7 @@ template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __gri
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            v[j] *= f;
-            if (h == j) v[j] -= kGain;
+            v[j] = h == j ? at_target[r] : v[j] * f;
         }
         if (hit[r] == -2) {
 #pragma unroll
@@ -387,7 +400,7 @@ struct Plan {
     int64_t band, bands, spans, ldv, ldd, blocks;
     int splits_x, splits_w;
     // byte offsets into the workspace
-    int64_t scale, ticket, part_sum, part_count, lse2, target_logit, off, sum, x, w, e, d, part, sum_w, bytes;
+    int64_t scale, ticket, part_sum, part_count, row_state, target_logit, off, sum, x, w, e, d, part, sum_w, bytes;
 };
 
 // How many pieces a product's K is cut into: with few tiles most pairs would
@@ -474,7 +487,7 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     p.ticket = p.scale + 4;
     p.part_sum = take(8 * p.blocks);
     p.part_count = take(8 * p.blocks);
-    p.lse2 = take(4 * p.band);
+    p.row_state = take(8 * p.band);
     p.target_logit = take(4 * p.band);
     p.off = take(4 * p.spans * p.band);
     p.sum = take(4 * p.spans * p.band);
@@ -654,7 +667,7 @@ fsdp_status run_few_grad(const fsdp_head_loss_args &a, const Plan &p, uint8_t *w
     f.hidden = static_cast<const float *>(a.hidden);
     f.weight = static_cast<const float *>(a.weight);
     f.logits = reinterpret_cast<const float *>(ws + p.e);
-    f.lse2 = reinterpret_cast<const float *>(ws + p.lse2);
+    f.row_state = reinterpret_cast<const float2 *>(ws + p.row_state);
     f.ld_hidden = a.ld_hidden;
     f.ld_weight = a.ld_weight;
     f.ld_logits = p.ldv;
@@ -693,7 +706,7 @@ fsdp_status run_rows(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, i
     r.rows = rows;
     r.vocab = a.vocab;
     r.ignore = a.ignore_index;
-    r.lse2 = reinterpret_cast<float *>(ws + p.lse2);
+    r.row_state = reinterpret_cast<float2 *>(ws + p.row_state);
     r.token_loss = a.token_loss ? a.token_loss + row0 : nullptr;
     r.part_sum = reinterpret_cast<double *>(ws + p.part_sum);
     r.part_count = reinterpret_cast<int64_t *>(ws + p.part_count);
@@ -792,7 +805,8 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         d.vocab = V;
         d.off = g.off;
         d.ld_rows = p.band;
-        d.lse2 = reinterpret_cast<const float *>(ws + p.lse2);
+        d.row_state = reinterpret_cast<const float2 *>(ws + p.row_state);
+        d.target_logit = g.target_logit;
         d.targets = g.targets;
         d.ignore = a.ignore_index;
         d.row_blocks = static_cast<uint32_t>(ceil_div(rows, kGradRows));

@@ -83,7 +83,8 @@ struct FewArgs {
 };
 
 struct FewGradArgs {
-    const float *hidden, *weight, *logits, *lse2;
+    const float *hidden, *weight, *logits;
+    const float2 *row_state;  // {reference, sum} of the row's exponentials
     int64_t ld_hidden, ld_weight, ld_logits, rows, vocab, dim;
     const int64_t *targets;
     int64_t ignore;

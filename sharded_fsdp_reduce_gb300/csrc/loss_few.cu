@@ -28,10 +28,10 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kTake = 4;  // vocabulary rows of a warp's step
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// sum * 2^top with one more term 2^x.
-__device__ __forceinline__ void take(float &top, float &sum, float x) {
-    const float most = fmaxf(top, x);
-    sum = sum * exp2f(top - most) + exp2f(x - most);
+// sum * 2^top with one more term 2^(logit log2(e)).
+__device__ __forceinline__ void take(float &top, float &sum, float logit) {
+    const float most = fmaxf(top, logit * kLog2e);
+    sum = sum * exp2f(top - most) + exp2f(fmaf(logit, kLog2e, -most));
     top = most;
 }
 __device__ __forceinline__ void join(float &top, float &sum, float other_top, float other_sum) {
@@ -152,7 +152,7 @@ template <int DT, int R, bool VEC> __global__ void __launch_bounds__(kThreads, 2
             if (v < a.vocab) {
                 if (first && v == target[t]) a.target_logit[row0 + t] = logit;
                 if (first && a.logits != nullptr && t < rows) a.logits[(row0 + t) * a.ld_logits + v] = logit;
-                take(top[t], sum[t], logit * kLog2e);
+                take(top[t], sum[t], logit);
             }
         }
     }
@@ -199,7 +199,8 @@ __device__ __forceinline__ float d_of(const FewGradArgs &a, int64_t t, int64_t v
     const int64_t y = a.targets[t];
     if (y == a.ignore) return 0.0f;
     if (y < 0 || y >= a.vocab) return NAN;
-    const float p = exp2f(fmaf(a.logits[t * a.ld_logits + v], kLog2e, -a.lse2[t]));
+    const float2 state = a.row_state[t];
+    const float p = exp2f(fmaf(a.logits[t * a.ld_logits + v], kLog2e, -state.x)) / state.y;
     return v == y ? p - 1.0f : p;
 }
 

@@ -346,6 +346,47 @@ def test_peaked_and_flat_rows(F):
     assert abs(float(tok[2]) - math.log(V)) < 1e-5
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,V,D", [(5, 1, 64), (130, 1, 8), (6, 3, 40), (200, 2, 64), (150, 700, 128)])
+def test_rows_that_are_sure_of_their_target(F, T, V, D, dt):
+    """p - 1 at the target, down to probabilities a few 2^-20 from 1 (and one
+    column, where it is 0): every probability is good to its logit's error and
+    2^-20, whatever is left of the difference."""
+    x, w, y = inputs(T, V, D, dt, std=0.05, ignored=None, seed=V)
+    lift = torch.linspace(0, 14, T, device=DEV)[:, None]
+    toward = w[y].float()
+    x = (x.float() * 0.3 + lift * toward / toward.square().sum(1, keepdim=True)).to(DT[dt])
+    ref = reference(x, w, y)
+    loss, tok, dx, dw = run(F, x, w, y)
+    logit = 8 * math.sqrt(D) * 2.0 ** -23 * ref["a"] + 2.0 ** -20
+    assert bool(((tok.double() - ref["tok"]).abs() <= logit * (1 + ref["tok"])).all())
+    p = torch.softmax(x.double() @ w.double().t(), 1)
+    le = float(logit.max())
+    for got, want, size, each in ((dx, ref["dx"], ref["sx"], p @ w.double().abs() / ref["n"]),
+                                  (dw, ref["dw"], ref["sw"], p.t() @ x.double().abs() / ref["n"])):
+        rounding = 4 * math.sqrt(max(V, T)) * 2.0 ** -23 if dt == "f32" else 1.1 * (U[dt] + 2.0 ** -11)
+        bound = rounding * size + 2 * le * each + U[dt] * want.abs() + (2.0 ** -25 if dt == "f16" else 1e-37)
+        assert bool(((got.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_one_column_has_no_gradient(F, T, dt):
+    """softmax of one logit is 1 whatever the logit is, its rounding included:
+    the exponential and the sum see the same one, so p - 1 is no more than an
+    exponential's two units and a division's one on either side, under 2^-21,
+    and does not grow with the logit."""
+    D = 64
+    x, w, _ = inputs(T, 1, D, dt, std=4.0, ignored=None, seed=T)
+    y = torch.zeros(T, dtype=torch.int64, device=DEV)
+    assert float((x.double() @ w.double().t()).abs().max()) > 30
+    _, _, dx, dw = run(F, x, w, y, reduction="sum")
+    least = 2.0 ** -25 if dt == "f16" else 1e-37
+    d, more = 2.0 ** -21, 1 + 4 * U[dt]
+    assert bool((dx.double().abs() <= d * more * w.double().abs() + least).all())
+    assert bool((dw.double().abs() <= d * more * x.double().abs().sum(0) + least).all())
+
+
 def test_gradients_against_differences(F):
     # the loss along a direction, in fp32: (L(x + h d) - L(x - h d)) / 2h = dx . d
     T, V, D = 12, 300, 64
