@@ -499,7 +499,9 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  * Precision: every sum and statistic is fp32 or wider. bf16 and fp16 heads:
  * d is rounded once to the head's type (fp16: times 2^14) for the gradient
  * products, the exponentials are held in fp16 relative to the largest of 64
- * columns before that. fp32 heads: every operand as three bf16 parts, the
+ * columns before that, but for the target's entry, which comes from its fp32
+ * logit: p - 1 is good to a few 2^-24 beside the logit's own error. A p that
+ * differs from 1 by less than that shows as 1. fp32 heads: every operand as three bf16 parts, the
  * products as exact as fp32's (an infinite operand counts as the largest
  * bf16 value). A few tokens (4, or 24 of an fp32 head, for losses alone; 8
  * of an fp32 head with gradients) are plain fp32 dot products.
