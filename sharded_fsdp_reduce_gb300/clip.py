@@ -71,8 +71,11 @@ class GradClip:
         _check(_lib.load().fsdp_grad_norm_workspace(self._numels, self._dtypes, n, ctypes.byref(size)),
                "fsdp_grad_norm_workspace")
         device = self.tensors[0].device if n else torch.device("cuda", torch.cuda.current_device())
-        self._ws = _Workspace(size.value, device)
-        self._norm = torch.zeros((), dtype=torch.float32, device=device)
+        # the norm lies behind the kernels' part, so that a stream that is ordered
+        # after the workspace's zeroing, and holds it, does so for both
+        at = -(-size.value // 256) * 256
+        self._ws = _Workspace(at + 4, device)
+        self._norm = self._ws.buf[at:].view(torch.float32).reshape(())
 
     def norm(self, out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """The norm of scale * tensors, an fp32 CUDA scalar: out, or one this

@@ -163,6 +163,44 @@ def test_on_another_stream_than_it_was_made_on(F):
         assert_norm(norm, norm64([t]))
 
 
+def test_its_own_norm_on_another_stream_while_the_first_is_busy(F, monkeypatch):
+    """Whatever the object prepares on the stream it was made on is done
+    before a call on another stream: every fill is made to come late here."""
+    s = torch.cuda.Stream()
+    t = rand(100_003, F32, 1)
+    ref, want = t.clone(), norm64([t])
+    F.GradClip([t.clone()]).clip(1.0)  # (a kernel's first launch waits for the device)
+    zeros = torch.zeros
+
+    def late(*args, **kw):
+        torch.cuda._sleep(20_000_000)
+        return zeros(*args, **kw)
+
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "zeros", late)
+    clip = F.GradClip([t])
+    monkeypatch.undo()
+    norm = clip.clip(0.25 * want, stream=s)
+    torch.cuda.synchronize()
+    assert_norm(norm, want)
+    assert torch.equal(t, ref * factor(norm, 0.25 * want))
+
+
+def test_its_own_norm_is_held_for_the_stream(F):
+    s = torch.cuda.Stream()
+    t = rand(100_003, F32, 1)
+    clip = F.GradClip([t])
+    clip.clip(1.0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(40_000_000)
+    clip.clip(0.1, stream=s)
+    del clip
+    others = [torch.full((), 7.0, device=DEV) for _ in range(4000)]  # would land in freed blocks of its size
+    torch.cuda.synchronize()
+    assert all(float(x) == 7.0 for x in others)
+
+
 def test_captured_in_a_graph(F):
     t = rand(70_001, BF16, 9)
     out = torch.empty_like(t)
