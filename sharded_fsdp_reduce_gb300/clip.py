@@ -10,6 +10,7 @@ import torch
 
 from . import _lib
 from .fsdp import StepConfig, UnitDescs, _check, _counter, _dev, dtype_code
+from .workspace import Workspace
 
 __all__ = ["GradClip", "ClipPlan"]
 
@@ -18,27 +19,6 @@ def _scalar(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() != 1:
         raise ValueError(f"{name} must be a float32 CUDA scalar")
     return _dev(t, name)
-
-
-class _Workspace:
-    """Zeroed device memory that calls on any stream may use, in order."""
-
-    def __init__(self, nbytes: int, device):
-        self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        made_on = torch.cuda.current_stream(self.buf.device)
-        self._made_on = made_on.cuda_stream
-        self._zeroed = made_on.record_event()
-
-    def on(self, stream: Optional[torch.cuda.Stream]) -> torch.cuda.Stream:
-        """The stream of a call (the current one by default), ordered after
-        the zeroing and holding the memory until its work is done."""
-        s = stream if stream is not None else torch.cuda.current_stream()
-        if s.cuda_stream != self._made_on:
-            # (a capture starts after the device is idle and cannot wait for work outside it)
-            if not torch.cuda.is_current_stream_capturing():
-                s.wait_event(self._zeroed)
-            self.buf.record_stream(s)
-        return s
 
 
 class GradClip:
@@ -74,7 +54,7 @@ class GradClip:
         # the norm lies behind the kernels' part, so that a stream that is ordered
         # after the workspace's zeroing, and holds it, does so for both
         at = -(-size.value // 256) * 256
-        self._ws = _Workspace(at + 4, device)
+        self._ws = Workspace(at + 4, device, zeroed=True)
         self._norm = self._ws.buf[at:].view(torch.float32).reshape(())
 
     def norm(self, out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
@@ -126,7 +106,7 @@ class ClipPlan:
             cfg = config.to_c()
             name, model = "fsdp_clip_plan_create_ex", (self.descs.array_ex, self.descs.n, ctypes.byref(cfg))
             _check(lib.fsdp_clip_plan_workspace_ex(*model, ctypes.byref(size)), "fsdp_clip_plan_workspace_ex")
-        self._ws = _Workspace(size.value, torch.device("cuda", torch.cuda.current_device()))
+        self._ws = Workspace(size.value, torch.device("cuda", torch.cuda.current_device()), zeroed=True)
         _check(getattr(lib, name)(*model, int(gathers), self._ws.buf.data_ptr(), self._ws.buf.numel(), nf, wt,
                                   ctypes.byref(self._handle)), name)
 

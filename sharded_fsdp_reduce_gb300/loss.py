@@ -16,6 +16,7 @@ import torch
 
 from . import _lib
 from .fsdp import _check, _counter, _on_current_device, dtype_code
+from .workspace import Workspace, take
 
 __all__ = ["HeadLoss", "fsdp_head_loss"]
 
@@ -90,9 +91,7 @@ def _workspace_bytes(a: _lib.FsdpHeadLossArgs) -> int:
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
-    # torch aligns allocations to 512 bytes: one kilobyte more, cut to the alignment
-    buf = torch.empty(nbytes + 1024, dtype=torch.uint8, device=device)
-    return buf.narrow(0, -buf.data_ptr() % 1024, nbytes)
+    return take(nbytes, device, alignment=1024)
 
 
 def _launch(a: _lib.FsdpHeadLossArgs, address: int, nbytes: int, stream: torch.cuda.Stream) -> int:
@@ -111,10 +110,10 @@ def fsdp_head_loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
     and d_weight [V, D] of hidden's dtype are written (d_* None: not formed)."""
     a = _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, ignore_index, reduction, grad_scale,
               band, wait_timeouts)
-    ws = _workspace(_workspace_bytes(a), hidden.device)
     s = stream if stream is not None else torch.cuda.current_stream()
+    with torch.cuda.stream(s):  # taken, and given back, in that stream's order
+        ws = _workspace(_workspace_bytes(a), hidden.device)
     _check(_launch(a, ws.data_ptr(), ws.numel(), s), "fsdp_head_loss")
-    ws.record_stream(s)
 
 
 class HeadLoss:
@@ -152,9 +151,8 @@ class HeadLoss:
         self._allocate(_workspace_bytes(a))
 
     def _allocate(self, nbytes: int) -> None:
-        self._ws = _workspace(nbytes, self.device)
-        self._ws_at, self._ws_bytes = self._ws.data_ptr(), nbytes
-        self._ws_stream = torch.cuda.current_stream(self.device).cuda_stream
+        self._ws = Workspace(nbytes, self.device, alignment=1024)
+        self._ws_at, self._ws_bytes = self._ws.buf.data_ptr(), nbytes
 
     def forward(self, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                 loss: Optional[torch.Tensor] = None, token_loss: Optional[torch.Tensor] = None,
@@ -188,13 +186,11 @@ class HeadLoss:
                     token_loss = torch.empty(hidden.shape[0], dtype=torch.float32, device=hidden.device)
         a = _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, self.ignore_index, self.reduction,
                   grad_scale, self.band, wait_timeouts)
-        if s.cuda_stream != self._ws_stream:
-            self._ws.record_stream(s)  # freed only after this call's work
+        self._ws.on(s)
         status = _launch(a, self._ws_at, self._ws_bytes, s)
         if status == _lib.FSDP_ERR_INVALID_ARG and _workspace_bytes(a) > self._ws_bytes:
-            self._allocate(_workspace_bytes(a))
-            if s.cuda_stream != self._ws_stream:
-                self._ws.record_stream(s)
+            with torch.cuda.stream(s):
+                self._allocate(_workspace_bytes(a))
             status = _launch(a, self._ws_at, self._ws_bytes, s)
         _check(status, "fsdp_head_loss")
         return loss, token_loss

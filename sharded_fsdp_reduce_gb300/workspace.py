@@ -1,0 +1,41 @@
+"""Device memory that an object's calls work in, on any stream."""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+__all__ = ["Workspace", "take"]
+
+
+def take(nbytes: int, device, alignment: int = 512, zeroed: bool = False) -> torch.Tensor:
+    """nbytes of the allocator's memory at a multiple of `alignment`, in the
+    current stream's order."""
+    room = alignment if alignment > 512 else 0  # torch aligns allocations to 512 bytes
+    whole = (torch.zeros if zeroed else torch.empty)(nbytes + room, dtype=torch.uint8, device=device)
+    return whole.narrow(0, -whole.data_ptr() % alignment, nbytes)
+
+
+class Workspace:
+    """nbytes of device memory at a multiple of `alignment`, that calls on any
+    stream may use, in order; zeroed, or with whatever it holds. The memory may
+    have had another user on the stream it is taken on, whose work is still
+    queued there: other streams wait for that."""
+
+    def __init__(self, nbytes: int, device, alignment: int = 512, zeroed: bool = False):
+        self.buf = take(nbytes, device, alignment, zeroed)
+        made_on = torch.cuda.current_stream(self.buf.device)
+        self._made_on = made_on.cuda_stream
+        self._ready = made_on.record_event()
+
+    def on(self, stream: Optional[torch.cuda.Stream]) -> torch.cuda.Stream:
+        """The stream of a call (the current one by default), ordered after
+        what the memory was used for before and holding it until its work is
+        done."""
+        s = stream if stream is not None else torch.cuda.current_stream()
+        if s.cuda_stream != self._made_on:
+            # (a capture starts after the device is idle and cannot wait for work outside it)
+            if not torch.cuda.is_current_stream_capturing():
+                s.wait_event(self._ready)
+            self.buf.record_stream(s)
+        return s

@@ -430,6 +430,45 @@ def test_one_head_for_calls_of_many_sizes_and_streams(F):
         check(ref, "bf16", D, (V, T), l2, t2)
 
 
+def block_with_a_queued_reader(nbytes):
+    """A copy, still to be made on the current stream, of a block of that many
+    bytes, which is already back with the allocator."""
+    block = torch.full((nbytes,), 7, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    return block.clone()
+
+
+@pytest.mark.parametrize("form", ["function", "object", "growth"])
+def test_a_workspace_waits_for_its_memorys_last_user(F, form):
+    from sharded_fsdp_reduce_gb300 import loss as mod
+    T, V, D = 300, 5000, 256
+    x, w, y = inputs(T, V, D, "bf16")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    loss, tok = torch.empty((), device=DEV), torch.empty(T, device=DEV)
+    s = torch.cuda.Stream()
+    if form == "growth":  # the weight at an address that has to be packed
+        head = F.HeadLoss(V, D, torch.bfloat16, T)
+        buf = torch.empty(V * D + 1, dtype=torch.bfloat16, device=DEV)
+        buf[1:].view(V, D).copy_(w)
+        w = buf[1:].view(V, D)
+    F.fsdp_head_loss(x, w, y, loss, tok, dx, dw)  # (a kernel's first launch waits for the device)
+    need = mod._workspace_bytes(mod._args(x, w, y, loss, tok, dx, dw, IGNORE, "mean", 1.0, 0, None))
+    assert need > 4 << 20
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    copy = block_with_a_queued_reader(need + 1024)
+    if form == "function":
+        F.fsdp_head_loss(x, w, y, loss, tok, dx, dw, stream=s)
+    else:
+        if form == "object":
+            head = F.HeadLoss(V, D, torch.bfloat16, T)
+        head.forward_backward(x, w, y, dx, dw, loss=loss, token_loss=tok, stream=s)
+    torch.cuda.synchronize()
+    assert bool((copy == 7).all())
+    check(reference(x, w, y), "bf16", D, (V, T), loss, tok, dx, dw)
+
+
 def test_workspace_grows_for_packed_operands(F):
     V, D, T = 700, 72, 50
     head = F.HeadLoss(V, D, torch.bfloat16, T)
