@@ -551,12 +551,17 @@ typedef struct {
 
 /* Bytes of workspace fsdp_head_loss needs for these arguments (host only;
  * they depend on the sizes, the type, the band, which outputs are asked for
- * and whether hidden and weight are 16-byte aligned). */
+ * and whether hidden and weight are 16-byte aligned). They are enough for
+ * every call of fewer tokens too, all else alike, with these gradients or one
+ * of them: size a workspace once, by the longest call. (Losses alone are
+ * sized by a call without gradients; aligned hidden and weight need no more
+ * than others do.) */
 fsdp_status fsdp_head_loss_workspace(const fsdp_head_loss_args *args, int64_t *bytes_out);
 
-/* Enqueue it. workspace: device, at least that many bytes, 1024-byte aligned,
- * not overlapping any buffer of the call; its contents before the call do not
- * matter and nothing is kept in it between calls. */
+/* Enqueue it. workspace: device, at least that many bytes (a call that needs
+ * more than workspace_bytes is refused), 1024-byte aligned, not overlapping
+ * any buffer of the call; its contents before the call do not matter and
+ * nothing is kept in it between calls. */
 fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* The global L2 norm of many tensors (device), in one pass:

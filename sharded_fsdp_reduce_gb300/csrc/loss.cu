@@ -403,6 +403,8 @@ struct Plan {
     int64_t scale, ticket, part_sum, part_count, row_state, target_logit, off, sum, x, w, e, d, part, sum_w, bytes;
 };
 
+constexpr int kMostSplits = 32;
+
 // How many pieces a product's K is cut into: with few tiles most pairs would
 // idle, and with little more than a multiple of the pairs the last round is
 // nearly empty. Takes the least of rounds of K blocks (about 0.3 us for each
@@ -412,7 +414,7 @@ int choose_splits(int64_t tiles, int64_t kblocks, int products, int64_t m, int64
     const int64_t pairs = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
     int best = 1;
     double least = 0.0;
-    for (int s = 1; s <= 32 && (s == 1 || kblocks * products / s >= 8); ++s) {
+    for (int s = 1; s <= kMostSplits && (s == 1 || kblocks * products / s >= 8); ++s) {
         const double rounds = static_cast<double>(ceil_div(tiles * s, pairs));
         double us = rounds * (static_cast<double>(ceil_div(kblocks, s)) * products * 0.3 + 2.0);
         if (s > 1) us += 4.0 + static_cast<double>(m) * n * 8.0 * s / 6.0e6;
@@ -432,7 +434,23 @@ int32_t alignment(const void *p, int64_t stride) {
 
 bool direct(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
-Plan make_plan(const fsdp_head_loss_args &a) {
+// Rows that the default budget allows a band.
+int64_t budget_band(int64_t bytes_per_row) {
+    const int64_t band = kDefaultBandBytes / bytes_per_row / kTileM * kTileM;
+    return band < kTileM ? kTileM : band;
+}
+
+int hidden_splits(const fsdp_head_loss_args &a, int64_t rows) {
+    return choose_splits(ceil_div(rows, kTileM) * ceil_div(a.dim, kTileN), ceil_div(a.vocab, kBlockK),
+                         a.dtype == FSDP_F32 ? 6 : 1, rows, round_up(a.dim, 64));
+}
+int weight_splits(const fsdp_head_loss_args &a, int64_t rows) {
+    return choose_splits(ceil_div(a.vocab, kTileM) * ceil_div(a.dim, kTileN), ceil_div(rows, kBlockK),
+                         a.dtype == FSDP_F32 ? 6 : 1, a.vocab, round_up(a.dim, 64));
+}
+
+// How a call runs.
+Plan choose(const fsdp_head_loss_args &a) {
     Plan p;
     memset(&p, 0, sizeof(p));
     p.f32 = a.dtype == FSDP_F32;
@@ -447,15 +465,12 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     p.ldv = round_up(a.vocab, 64);
     p.ldd = round_up(a.dim, 64);
     p.spans = p.few ? few_blocks(a.vocab) : ceil_div(a.vocab, kSpan);
-    const int64_t planes = p.f32 ? 3 : 1;
-    const int64_t per_row = p.ldv * (p.f32 ? 10 : 2);  // exponentials, and the planes of an fp32 head
     int64_t band = p.few ? a.tokens : a.band;  // (a few rows are one band whatever was asked for)
     if (band == 0) {
-        // gradients: what fits the default budget; losses alone: the statistics
-        // (8 bytes a span and row) stay below it for any band this size
-        band = p.grad ? kDefaultBandBytes / per_row : kDefaultBandBytes / (8 * p.spans);
-        band = band / kTileM * kTileM;
-        if (band < kTileM) band = kTileM;
+        // gradients: what fits the default budget (exponentials, and the planes
+        // of an fp32 head); losses alone: the statistics (8 bytes a span and
+        // row) stay below it for any band this size
+        band = budget_band(p.grad ? p.ldv * (p.f32 ? 10 : 2) : 8 * p.spans);
         // as many bands as that takes, of nearly equal length
         const int64_t each = ceil_div(a.tokens, ceil_div(a.tokens, band));
         band = round_up(each, kTileM) < band ? round_up(each, kTileM) : band;
@@ -468,15 +483,85 @@ Plan make_plan(const fsdp_head_loss_args &a) {
         p.blocks += ceil_div(rows, kRows);
     }
     p.splits_x = p.splits_w = 1;
-    const int products = p.f32 ? 6 : 1;
-    if (a.d_hidden && p.few)
-        p.splits_x = static_cast<int>(few_parts(a.vocab, a.dim));
-    else if (a.d_hidden)
-        p.splits_x = choose_splits(ceil_div(p.band, kTileM) * ceil_div(a.dim, kTileN),
-                                   ceil_div(a.vocab, kBlockK), products, p.band, p.ldd);
-    if (a.d_weight && p.bands == 1 && !p.few)
-        p.splits_w = choose_splits(ceil_div(a.vocab, kTileM) * ceil_div(a.dim, kTileN),
-                                   ceil_div(p.band, kBlockK), products, a.vocab, p.ldd);
+    if (a.d_hidden) p.splits_x = p.few ? static_cast<int>(few_parts(a.vocab, a.dim)) : hidden_splits(a, p.band);
+    if (a.d_weight && p.bands == 1 && !p.few) p.splits_w = weight_splits(a, p.band);
+    return p;
+}
+
+// What the workspace's parts hold.
+struct Room {
+    int64_t blocks, band, stats, x, w, e, d, part, sum_w;  // counts of the first three, then bytes
+};
+
+int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
+
+Room room_of(const fsdp_head_loss_args &a, const Plan &p) {
+    Room r;
+    memset(&r, 0, sizeof(r));
+    const int64_t planes = p.f32 ? 3 : 1;
+    r.blocks = p.blocks;
+    r.band = p.band;
+    r.stats = p.spans * p.band;
+    if (p.pack_x) r.x = 2 * planes * a.tokens * p.ldd;
+    if (p.pack_w) r.w = 2 * planes * a.vocab * p.ldd;
+    if (p.grad) {
+        r.e = p.band * p.ldv * (p.f32 ? 4 : 2);
+        if (p.f32 && !p.few) r.d = p.band * p.ldv * 6;
+        if (p.splits_x > 1 || p.few) r.part = 4 * p.splits_x * p.band * p.ldd;
+        if (p.splits_w > 1) r.part = larger(r.part, 4 * p.splits_w * a.vocab * p.ldd);
+        if (a.d_weight && p.bands > 1) r.sum_w = 4 * a.vocab * p.ldd;
+    }
+    return r;
+}
+
+// Every part as large as any call of at most this one's tokens needs it. A
+// shorter call can need more of some than a longer one: it may cut a product
+// into more pieces, work in one band where the longer one takes two halves,
+// or run as a few rows.
+Room room_up_to(const fsdp_head_loss_args &a) {
+    const Plan p = choose(a);
+    Room r = room_of(a, p);
+    if (p.few) return r;  // (grows with the rows)
+    fsdp_head_loss_args few = a;
+    few.tokens = few_rows(a.dtype, p.grad);
+    if (few.tokens > 0 && a.dim <= (1 << 22)) {
+        const Plan q = choose(few);
+        const Room f = room_of(few, q);
+        r.band = larger(r.band, f.band);
+        r.stats = larger(r.stats, f.stats);
+        r.e = larger(r.e, f.e);
+        r.part = larger(r.part, f.part);
+    }
+    // the longest band of these calls: they are as long as their tokens up to
+    // what was asked for or what the budget allows
+    int64_t band = a.band > 0 ? a.band : budget_band(p.grad ? p.ldv * (p.f32 ? 10 : 2) : 8 * p.spans);
+    band = band < a.tokens ? band : a.tokens;
+    r.band = larger(r.band, band);
+    r.stats = larger(r.stats, p.spans * band);
+    if (p.grad) {
+        r.e = larger(r.e, band * p.ldv * (p.f32 ? 4 : 2));
+        if (p.f32) r.d = band * p.ldv * 6;
+        if (a.d_hidden) {
+            // the more rows of a tile, the fewer pieces: the tile's first row
+            // has the most, its last the longest
+            for (int64_t rows = 1; rows <= band; rows += kTileM) {
+                const int s = hidden_splits(a, rows);
+                const int64_t end = rows + kTileM - 1 < band ? rows + kTileM - 1 : band;
+                if (s > 1) r.part = larger(r.part, 4 * s * end * p.ldd);
+            }
+        }
+        if (a.d_weight) {
+            int most = 1;
+            for (int64_t rows = 1; rows <= band && most < kMostSplits; rows += kBlockK)
+                if (const int s = weight_splits(a, rows); s > most) most = s;
+            if (most > 1) r.part = larger(r.part, 4 * most * a.vocab * p.ldd);
+        }
+    }
+    return r;
+}
+
+// The parts one after another, at multiples of a kilobyte.
+void place(Plan &p, const Room &r) {
     int64_t at = 0;
     auto take = [&at](int64_t bytes) {
         const int64_t here = at;
@@ -485,24 +570,32 @@ Plan make_plan(const fsdp_head_loss_args &a) {
     };
     p.scale = take(8);
     p.ticket = p.scale + 4;
-    p.part_sum = take(8 * p.blocks);
-    p.part_count = take(8 * p.blocks);
-    p.row_state = take(8 * p.band);
-    p.target_logit = take(4 * p.band);
-    p.off = take(4 * p.spans * p.band);
-    p.sum = take(4 * p.spans * p.band);
-    if (p.pack_x) p.x = take(2 * planes * a.tokens * p.ldd);
-    if (p.pack_w) p.w = take(2 * planes * a.vocab * p.ldd);
-    if (p.grad) {
-        p.e = take(p.band * p.ldv * (p.f32 ? 4 : 2));
-        p.d = p.f32 && !p.few ? take(p.band * p.ldv * 6) : p.e;
-        const int64_t part_x = p.splits_x > 1 || p.few ? 4 * p.splits_x * p.band * p.ldd : 0;
-        const int64_t part_w = p.splits_w > 1 ? 4 * p.splits_w * a.vocab * p.ldd : 0;
-        p.part = take(part_x > part_w ? part_x : part_w);
-        if (a.d_weight && p.bands > 1) p.sum_w = take(4 * a.vocab * p.ldd);
-    }
+    p.part_sum = take(8 * r.blocks);
+    p.part_count = take(8 * r.blocks);
+    p.row_state = take(8 * r.band);
+    p.target_logit = take(4 * r.band);
+    p.off = take(4 * r.stats);
+    p.sum = take(4 * r.stats);
+    p.x = take(r.x);
+    p.w = take(r.w);
+    p.e = take(r.e);
+    p.d = r.d > 0 ? take(r.d) : p.e;
+    p.part = take(r.part);
+    p.sum_w = take(r.sum_w);
     p.bytes = at;
+}
+
+Plan make_plan(const fsdp_head_loss_args &a) {
+    Plan p = choose(a);
+    place(p, room_of(a, p));
     return p;
+}
+
+// The bytes that are enough for this call and for every shorter one.
+int64_t bytes_up_to(const fsdp_head_loss_args &a) {
+    Plan p = choose(a);
+    place(p, room_up_to(a));
+    return p.bytes;
 }
 
 // ---------------------------------------------------------------- host: tensor maps
@@ -908,7 +1001,7 @@ FSDP_API fsdp_status fsdp_head_loss_workspace(const fsdp_head_loss_args *args, i
     const fsdp_status st = loss::check(args);
     if (st != FSDP_OK) return st;
     if (!bytes_out) return FSDP_ERR_INVALID_ARG;
-    *bytes_out = args->tokens == 0 ? 0 : loss::make_plan(*args).bytes;
+    *bytes_out = args->tokens == 0 ? 0 : loss::bytes_up_to(*args);
     return FSDP_OK;
 }
 

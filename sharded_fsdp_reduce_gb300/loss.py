@@ -124,9 +124,12 @@ class HeadLoss:
     will be asked for (the workspace is sized for it). band: rows worked on
     together (0: as many as keep the 16-bit exponentials within 4 GiB).
     ignore_index, reduction ("mean" over the rows that count, or "sum") as in
-    fsdp_head_loss. The workspace grows by itself, once, when a call needs
-    more (rows that are not 16-byte aligned are packed into it). Calls on one
-    stream, or ordered between streams, may share it; calls that run at the
+    fsdp_head_loss. No call of up to max_tokens rows, contiguous or 16-byte
+    aligned, needs more workspace than the object starts with. Other rows of
+    16-bit types are packed into it, and gradients of an object made without
+    them need more: the first such call takes a larger one, and the earlier one
+    is kept, so that a captured graph of earlier calls still finds it. Calls on one stream,
+    or ordered between streams, may share the object; calls that run at the
     same time need a HeadLoss each."""
 
     def __init__(self, vocab: int, dim: int, dtype: torch.dtype, max_tokens: int, grad: bool = True, band: int = 0,
@@ -137,22 +140,39 @@ class HeadLoss:
         self.max_tokens, self.grad, self.band = int(max_tokens), bool(grad), int(band)
         self.ignore_index, self.reduction = int(ignore_index), reduction
         self.device = torch.device(device)
-        # sized as a call with aligned operands needs it (addresses are not read)
+        self._kept = []
+        odd = self.dim % 8 != 0  # (contiguous rows are then not aligned)
+        self._forms = (self.grad, odd, odd)
+        self._allocate(self._need(*self._forms))
+
+    def _need(self, grad: bool, odd_hidden: bool, odd_weight: bool) -> int:
+        """Workspace of every call of up to max_tokens rows: with gradients or
+        not, hidden and weight 16-byte aligned or not (addresses are not read)."""
         a = _lib.FsdpHeadLossArgs()
-        a.dtype = dtype_code(dtype)
+        a.dtype = dtype_code(self.dtype)
         a.tokens, a.vocab, a.dim, a.band = self.max_tokens, self.vocab, self.dim, self.band
-        pad = -(-self.dim // 8) * 8
-        step = 1 << 56
-        a.hidden, a.weight, a.targets, a.loss = step, 2 * step, 3 * step, 4 * step
-        a.ld_hidden = a.ld_weight = a.ld_d_hidden = a.ld_d_weight = pad
+        step, off = 1 << 56, self.dtype.itemsize
+        a.hidden, a.weight = step + (off if odd_hidden else 0), 2 * step + (off if odd_weight else 0)
+        a.targets, a.loss = 3 * step, 4 * step
+        a.ld_hidden = a.ld_weight = a.ld_d_hidden = a.ld_d_weight = -(-self.dim // 8) * 8
+        a.grad_scale = 1.0
+        need = _workspace_bytes(a)
         if grad:
             a.d_hidden, a.d_weight = 5 * step, 6 * step
-        a.grad_scale = 1.0
-        self._allocate(_workspace_bytes(a))
+            need = max(need, _workspace_bytes(a))
+        return need
 
     def _allocate(self, nbytes: int) -> None:
         self._ws = Workspace(nbytes, self.device, alignment=1024)
         self._ws_at, self._ws_bytes = self._ws.buf.data_ptr(), nbytes
+
+    def _grow(self, a: _lib.FsdpHeadLossArgs) -> None:
+        """A larger workspace, for a call's form and all the earlier ones."""
+        odd = [p % 16 != 0 or ld % 8 != 0 for p, ld in ((a.hidden, a.ld_hidden), (a.weight, a.ld_weight))]
+        new = (a.d_hidden is not None or a.d_weight is not None, *odd)
+        self._forms = tuple(x or y for x, y in zip(self._forms, new))
+        self._kept.append(self._ws)
+        self._allocate(self._need(*self._forms))
 
     def forward(self, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                 loss: Optional[torch.Tensor] = None, token_loss: Optional[torch.Tensor] = None,
@@ -190,7 +210,7 @@ class HeadLoss:
         status = _launch(a, self._ws_at, self._ws_bytes, s)
         if status == _lib.FSDP_ERR_INVALID_ARG and _workspace_bytes(a) > self._ws_bytes:
             with torch.cuda.stream(s):
-                self._allocate(_workspace_bytes(a))
+                self._grow(a)
             status = _launch(a, self._ws_at, self._ws_bytes, s)
         _check(status, "fsdp_head_loss")
         return loss, token_loss

@@ -482,6 +482,54 @@ def test_workspace_grows_for_packed_operands(F):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dt,most,V,D", [("bf16", 600, 2000, 1024), ("f16", 1100, 4000, 1024), ("f32", 1100, 1003, 512),
+                                         ("f16", 300, 300, 65)])
+@pytest.mark.parametrize("grad", [True, False])
+def test_no_shorter_call_grows_the_workspace(F, dt, most, V, D, grad):
+    head = F.HeadLoss(V, D, DT[dt], most, grad=grad)
+    at, size = head._ws_at, head._ws_bytes
+    x, w, y = inputs(most, V, D, dt, ignored="some")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    # (1024 and 585 rows cut a product into more pieces than 1100 and 600)
+    lengths = (1100, 1025, 1024, 1000, 700, 600, 585, 513, 512, 300, 257, 256, 255, 130, 65, 64, 33, 25, 24, 9, 8, 5, 4, 1)
+    for T in (t for t in lengths if t <= most):
+        if grad:
+            head.forward_backward(x[:T], w, y[:T], dx[:T], dw)
+            head.forward_backward(x[:T], w, y[:T], None, dw)
+            head.forward_backward(x[:T], w, y[:T], dx[:T], None)
+        head.forward(x[:T], w, y[:T])
+        assert (head._ws_at, head._ws_bytes) == (at, size), T
+
+
+def test_a_captured_graph_outlives_a_growth(F):
+    """A graph's calls keep writing to the workspace that they were captured
+    with: it has to stay theirs when a later call takes a larger one."""
+    T, V, D = 64, 5000, 256
+    x, w, y = inputs(T, V, D, "bf16", ignored="some")
+    head = F.HeadLoss(V, D, torch.bfloat16, T)
+    size = head._ws_bytes
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    loss, tok = torch.empty((), device=DEV), torch.empty(T, device=DEV)
+    head.forward_backward(x, w, y, dx, dw, loss=loss, token_loss=tok)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        head.forward_backward(x, w, y, dx, dw, loss=loss, token_loss=tok)
+    buf = torch.empty(V * D + 1, dtype=torch.bfloat16, device=DEV)
+    buf[1:].view(V, D).copy_(w)
+    for _ in range(2):
+        head.forward_backward(x, buf[1:].view(V, D), y, None, torch.empty_like(w))
+    assert head._ws_bytes > size
+    torch.cuda.synchronize()
+    others = [torch.full((size + 1024,), 7, dtype=torch.uint8, device=DEV) for _ in range(3)]
+    for t in (dx, dw, loss, tok):
+        t.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    check(reference(x, w, y), "bf16", D, (V, T), loss, tok, dx, dw)
+    assert all(bool((o == 7).all()) for o in others)
+
+
 def test_captured_in_a_graph(F):
     T, V, D = 200, 1200, 128
     x, w, y = inputs(T, V, D, "bf16")

@@ -64,6 +64,29 @@ def test_head_loss_workspace(lib, L):
     assert st == L.FSDP_OK and n == 0
 
 
+@pytest.mark.parametrize("T,V,D,dtype,band", [
+    (2048, 32000, 4096, "bf16", 0), (4096, 128256, 8192, "bf16", 0), (3000, 1003, 200, "f16", 0),
+    (700, 5003, 768, "f32", 0), (30, 33, 8, "f32", 0), (9, 40, 72, "bf16", 0), (900, 700, 64, "bf16", 100),
+    (70_000, 131_072, 64, "bf16", 0),  # longer than one band's budget: two of about half its length
+])
+@pytest.mark.parametrize("grads", ["both", "none"])
+def test_head_loss_workspace_is_enough_for_every_shorter_call(lib, L, T, V, D, dtype, band, grads):
+    """What the longest call needs is enough for all shorter ones, with both
+    gradients or one: they may cut a product into more pieces than it does,
+    work in one band where it takes two, or run as a few rows."""
+    code = dict(f32=L.FSDP_F32, bf16=L.FSDP_BF16, f16=L.FSDP_F16)[dtype]
+    for weight in (2 << 40, (2 << 40) + 4):  # aligned, and to be packed
+        kw = dict(V=V, D=D, dtype=code, band=band, weight=BASE + weight, grad=grads != "none")
+        st, most = workspace(lib, loss_args(L, T=T, **kw))
+        assert st == L.FSDP_OK
+        for t in list(range(1, 600)) + list(range(600, T, max(1, T // 3000))):
+            if t >= T:
+                break
+            for alone in (dict(), dict(d_hidden=None), dict(d_weight=None)) if kw["grad"] else (dict(),):
+                st, n = workspace(lib, loss_args(L, T=t, **kw, **alone))
+                assert st == L.FSDP_OK and n <= most, (t, alone, n, most)
+
+
 def test_head_loss_refuses(lib, L):
     bad = L.FSDP_ERR_INVALID_ARG
     cases = [
