@@ -72,6 +72,7 @@ class GradClip:
         """out = tensors * scale * min(1, max_norm / (norm + 1e-6)). norm: the
         norm to use (a CUDA scalar, e.g. one taken over more tensors than
         these); default: these tensors', taken first. Returns the norm."""
+        self._ws.check_device()
         s = stream if stream is not None else torch.cuda.current_stream()
         if norm is None:
             norm = self.norm(stream=s)

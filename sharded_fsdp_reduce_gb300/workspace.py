@@ -24,14 +24,22 @@ class Workspace:
 
     def __init__(self, nbytes: int, device, alignment: int = 512, zeroed: bool = False):
         self.buf = take(nbytes, device, alignment, zeroed)
+        self._device = self.buf.get_device()
         made_on = torch.cuda.current_stream(self.buf.device)
         self._made_on = made_on.cuda_stream
         self._ready = made_on.record_event()
+
+    def check_device(self) -> None:
+        """The kernels run on the current device, which has to be the memory's."""
+        if torch.cuda.current_device() != self._device:
+            raise ValueError(f"this object's workspace is on cuda:{self._device} but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
 
     def on(self, stream: Optional[torch.cuda.Stream]) -> torch.cuda.Stream:
         """The stream of a call (the current one by default), ordered after
         what the memory was used for before and holding it until its work is
         done."""
+        self.check_device()
         s = stream if stream is not None else torch.cuda.current_stream()
         if s.cuda_stream != self._made_on:
             # (a capture starts after the device is idle and cannot wait for work outside it)

@@ -210,3 +210,19 @@ def test_binding_refuses_tensors_that_are_not_on_the_gpu():
         F.HeadLoss(10, 8, torch.float64, 4)
     with pytest.raises(ValueError):
         F.HeadLoss(10, 8, torch.bfloat16, 4, reduction="none")
+
+
+def test_a_workspace_of_another_device_is_refused(monkeypatch):
+    """An object made on one GPU and called with another one current, its
+    tensors there: the workspace would reach the kernels as a foreign address."""
+    import types
+    import torch
+    from sharded_fsdp_reduce_gb300.workspace import Workspace
+    ws = Workspace.__new__(Workspace)
+    ws.buf, ws._device, ws._made_on, ws._ready = torch.zeros(8), 0, 5, None
+    s = types.SimpleNamespace(cuda_stream=5)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert ws.on(s) is s
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        ws.on(s)
