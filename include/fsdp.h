@@ -611,7 +611,9 @@ fsdp_status fsdp_clip_grads(const void *const *tensors, void *const *outs, const
  *                8 gradient bytes an element, or offloaded, keep the fp32
  *                average there: 4 bytes an element), 256-byte aligned, zeroed
  *                once by the caller before the first launch; it must stay
- *                allocated, like the units' buffers, and belongs to this plan.
+ *                allocated, like the units' buffers (a captured graph's
+ *                launches use it too), and may be shared with plans whose
+ *                launches come in order with this one's.
  *   nonfinite_count  device uint32 or NULL: incremented by the number of
  *                averaged elements that are not finite (reported, never
  *                skipped: the norm is then not finite either).

@@ -87,10 +87,12 @@ class ClipPlan:
     fsdp_clip_plan_create_ex when `config` is given): launch() takes the
     averaged gradient's norm over all units, then each unit's step with the
     clipped gradient and its all-gathers. The units' buffers must stay
-    allocated (the units are kept alive here)."""
+    allocated (the units are kept alive here). workspace: another plan's, to
+    work in where it is large enough (their launches then have to be in order)."""
 
     def __init__(self, units, gathers: int = 1, nonfinite_count: Optional[torch.Tensor] = None,
-                 config: Optional[StepConfig] = None, wait_timeouts: Optional[torch.Tensor] = None):
+                 config: Optional[StepConfig] = None, wait_timeouts: Optional[torch.Tensor] = None,
+                 workspace: Optional[Workspace] = None):
         self.descs = units if isinstance(units, UnitDescs) else UnitDescs(units)
         if config is None and not self.descs.adamw:
             raise ValueError("an AdamW model step needs fp32 master and AdamW state in every unit")
@@ -107,8 +109,10 @@ class ClipPlan:
             cfg = config.to_c()
             name, model = "fsdp_clip_plan_create_ex", (self.descs.array_ex, self.descs.n, ctypes.byref(cfg))
             _check(lib.fsdp_clip_plan_workspace_ex(*model, ctypes.byref(size)), "fsdp_clip_plan_workspace_ex")
-        self._ws = Workspace(size.value, torch.device("cuda", torch.cuda.current_device()), zeroed=True)
-        _check(getattr(lib, name)(*model, int(gathers), self._ws.buf.data_ptr(), self._ws.buf.numel(), nf, wt,
+        if workspace is None or workspace.buf.numel() < size.value:
+            workspace = Workspace(size.value, torch.device("cuda", torch.cuda.current_device()), zeroed=True)
+        self.workspace = workspace
+        _check(getattr(lib, name)(*model, int(gathers), workspace.buf.data_ptr(), workspace.buf.numel(), nf, wt,
                                   ctypes.byref(self._handle)), name)
 
     def launch(self, hparams, max_norm: float, norm: torch.Tensor,
@@ -117,7 +121,7 @@ class ClipPlan:
         optimizer); norm (fp32 CUDA scalar) receives the gradient's norm."""
         if not self._handle:
             raise RuntimeError("the model step was destroyed")
-        s = self._ws.on(stream)
+        s = self.workspace.on(stream)
         c = hparams.to_c()
         name = "fsdp_clip_plan_launch" if self.config is None else "fsdp_clip_plan_launch_ex"
         _check(getattr(_lib.load(), name)(self._handle, ctypes.byref(c), float(max_norm), _scalar(norm, "norm"),

@@ -312,6 +312,7 @@ class UnitSequence:
         self._plan_key = None   # what it was made for
         self._clip_plan = None  # the last ClipPlan made by clip_step()
         self._clip_key = None
+        self._clip_kept = []    # workspaces of earlier ones that it does not share
 
     def _adamw_fused(self, hp) -> bool:
         return isinstance(hp, AdamWHParams) and all(not u.variant for u in self.units)
@@ -364,11 +365,16 @@ class UnitSequence:
             kind = config.optimizer
         key = (kind, config is None, int(gathers), ptr(nonfinite_count), ptr(wait_timeouts))
         if key != self._clip_key:
-            if self._clip_plan is not None:
-                self._clip_plan.close()
-                self._clip_plan, self._clip_key = None, None
-            self._clip_plan = ClipPlan(self.descs, gathers, nonfinite_count, config, wait_timeouts)
-            self._clip_key = key
+            # a captured graph of the earlier plan's steps still works in its
+            # workspace: the new plan shares it, or it is kept
+            old = self._clip_plan
+            plan = ClipPlan(self.descs, gathers, nonfinite_count, config, wait_timeouts,
+                            None if old is None else old.workspace)
+            if old is not None:
+                old.close()
+                if plan.workspace is not old.workspace:
+                    self._clip_kept.append(old.workspace)
+            self._clip_plan, self._clip_key = plan, key
         s = stream if stream is not None else torch.cuda.current_stream()
         if norm is None:
             with torch.cuda.stream(s):

@@ -378,6 +378,50 @@ def test_clipped_step_on_another_stream_and_repeated(F):
         assert torch.equal(a.master, b.master) and torch.equal(a.full[0], b.full[0])
 
 
+def test_a_captured_clipped_step_outlives_a_change_of_arguments(F):
+    """A captured graph of clipped steps keeps writing to the workspace that
+    they were captured with, whatever plan later calls make."""
+    units = make_units(F, [200_003, 512], 8, BF16, BF16, 18, n_full=1)
+    twin = make_units(F, [200_003, 512], 8, BF16, BF16, 18, n_full=1)
+    model, hp = F.UnitSequence(units), F.AdamWHParams(**HP)
+    norm = torch.empty((), device=DEV)
+    model.clip_step(hp, 0.05, norm=norm)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        model.clip_step(hp, 0.05, norm=norm)
+    nf = torch.zeros(1, dtype=torch.int32, device=DEV)
+    model.clip_step(hp, 0.05, nonfinite_count=nf)
+    model.clip_step(hp, 0.05, gathers=0)
+    torch.cuda.synchronize()
+    size = model._clip_plan.workspace.buf.numel()
+    assert size > 4 * 200_003
+    others = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(3)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(bool((o == 7).all()) for o in others)
+    other = F.UnitSequence(twin)
+    for _ in range(4):
+        n = other.clip_step(hp, 0.05)
+    torch.cuda.synchronize()
+    assert torch.equal(n, norm)
+    for a, b in zip(units, twin):
+        assert torch.equal(a.master, b.master) and torch.equal(a.full[0], b.full[0])
+
+
+def test_a_larger_plan_keeps_the_earlier_workspace(F):
+    # two ranks in 16 bits keep no average; the variant form keeps every one
+    model = F.UnitSequence(make_units(F, [50_003], 2, BF16, BF16, 19, n_full=1))
+    model.clip_step(F.AdamWHParams(**HP), 0.05)
+    first = model._clip_plan.workspace
+    model.clip_step(F.StepConfig("adamw", 1e-3, 0.9, 0.95, 1e-8, 0.1, 7), 0.05)
+    second = model._clip_plan.workspace
+    assert second is not first and any(k is first for k in model._clip_kept)
+    model.clip_step(F.AdamWHParams(**HP), 0.05)  # and the smaller plan works in the larger one's
+    assert model._clip_plan.workspace is second
+    torch.cuda.synchronize()
+
+
 def test_clipped_step_counts_and_shows_values_that_are_not_finite(F):
     units = make_units(F, [4099, 700], 8, BF16, BF16, 16, n_full=1)
     units[0].grads[3][100] = float("inf")
