@@ -25,9 +25,13 @@ class Workspace:
     def __init__(self, nbytes: int, device, alignment: int = 512, zeroed: bool = False):
         self.buf = take(nbytes, device, alignment, zeroed)
         self._device = self.buf.get_device()
-        made_on = torch.cuda.current_stream(self.buf.device)
-        self._made_on = made_on.cuda_stream
-        self._ready = made_on.record_event()
+        self._zeroed = zeroed
+        self._in_capture = torch.cuda.is_current_stream_capturing()
+        self._mark(torch.cuda.current_stream(self.buf.device))
+
+    def _mark(self, stream: torch.cuda.Stream) -> None:
+        self._made_on = stream.cuda_stream
+        self._ready = stream.record_event()
 
     def check_device(self) -> None:
         """The kernels run on the current device, which has to be the memory's."""
@@ -41,6 +45,14 @@ class Workspace:
         done."""
         self.check_device()
         s = stream if stream is not None else torch.cuda.current_stream()
+        if self._in_capture and not torch.cuda.is_current_stream_capturing():
+            # made within a capture: its zeroing and its event are the graph's,
+            # which may not have run yet
+            if self._zeroed:
+                with torch.cuda.stream(s):
+                    self.buf.zero_()
+            self._in_capture = False
+            self._mark(s)
         if s.cuda_stream != self._made_on:
             # (a capture starts after the device is idle and cannot wait for work outside it)
             if not torch.cuda.is_current_stream_capturing():

@@ -221,6 +221,30 @@ def test_captured_in_a_graph(F):
         assert torch.equal(out, (t.float() * factor(norm, 0.5)).to(BF16))
 
 
+def test_made_within_a_capture_and_used_outside_it(F):
+    t = rand(70_001, F32, 9)
+    u = make_units(F, [9001], 8, BF16, BF16, 15, n_full=1)
+    F.GradClip([t.clone()]).clip(1.0)
+    F.UnitSequence(make_units(F, [9001], 8, BF16, BF16, 15, n_full=1)).clip_step(F.AdamWHParams(**HP), 0.05)
+    want, step_want = norm64([t]), norm64([average(u[0], 1.0)])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        junk = torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV)
+        del junk  # (what the graph's memory holds is not 0)
+        clip, model = F.GradClip([t]), F.UnitSequence(u)
+        norm = clip.norm(torch.empty((), device=DEV))
+        step_norm = model.clip_step(F.AdamWHParams(**HP), 0.05)
+    assert_norm(clip.norm(), want)
+    assert_norm(model.clip_step(F.AdamWHParams(**HP), 0.05), step_want)
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        assert_norm(norm, want)
+        assert_norm(step_norm, step_want)
+    assert_norm(clip.norm(), want)
+
+
 def test_refusals(F):
     t = rand(100, F32, 0)
     with pytest.raises(ValueError):

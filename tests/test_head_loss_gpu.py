@@ -549,6 +549,25 @@ def test_captured_in_a_graph(F):
         check(reference(x, w, y), "bf16", D, (V, T), loss, tok, dx, dw)
 
 
+def test_made_within_a_capture_and_used_outside_it(F):
+    T, V, D = 200, 1200, 128
+    x, w, y = inputs(T, V, D, "bf16")
+    loss, tok = torch.empty((), device=DEV), torch.empty(T, device=DEV)
+    run(F, x, w, y, grad=False)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        head = F.HeadLoss(V, D, torch.bfloat16, T)
+        head.forward(x, w, y, loss=loss, token_loss=tok)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    l2, t2 = head.forward_backward(x, w, y, dx, dw)
+    g.replay()
+    torch.cuda.synchronize()
+    ref = reference(x, w, y)
+    check(ref, "bf16", D, (V, T), loss, tok)
+    check(ref, "bf16", D, (V, T), l2, t2, dx, dw)
+
+
 def test_results_longer_than_32_bits_of_elements(F):
     # the exponentials of one band pass 2^31 elements
     T, V, D = 16400, 131100, 8

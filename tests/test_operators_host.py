@@ -219,7 +219,7 @@ def test_a_workspace_of_another_device_is_refused(monkeypatch):
     import torch
     from sharded_fsdp_reduce_gb300.workspace import Workspace
     ws = Workspace.__new__(Workspace)
-    ws.buf, ws._device, ws._made_on, ws._ready = torch.zeros(8), 0, 5, None
+    ws.buf, ws._device, ws._made_on, ws._ready, ws._in_capture = torch.zeros(8), 0, 5, None, False
     s = types.SimpleNamespace(cuda_stream=5)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     assert ws.on(s) is s
