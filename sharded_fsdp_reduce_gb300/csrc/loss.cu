@@ -6,7 +6,7 @@
 //
 // The logits in fp32 live in tensor memory only. The logits product's epilogue
 // turns each span of 64 columns into exponentials against the span's own
-// maximum, and keeps their fp32 sum and that reference; a row kernel joins the
+// maximum, and keeps their fp32 sum and that maximum; a row kernel joins the
 // spans into lse. Without gradients that is all: X and W are read, a few bytes
 // per span are written. With gradients the exponentials of a band of tokens
 // are also stored, in 16 bits, and turned in place into d; the two gradient
@@ -23,7 +23,6 @@ namespace fsdp {
 namespace loss {
 namespace {
 
-constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 // fp16 gradients of the logits are held times 2^14: d is at most 1 in
 // magnitude, and a probability down to 2^-28 keeps all its bits.
@@ -38,7 +37,7 @@ struct RowArgs {
     const float *target_logit;
     const int64_t *targets;
     int64_t rows, vocab, ignore;
-    float2 *row_state;       // {reference, sum}: the row's exponentials add up to sum * 2^reference
+    float2 *row_state;       // {largest logit, sum of the exponentials against it}
     float *token_loss;       // or NULL
     // the loss over all bands: block sums, joined by the last block
     double *part_sum;
@@ -61,11 +60,14 @@ __device__ long long warp_sum(long long x) {
     return x;
 }
 
-// (top, sum): sum * 2^top. Joins another pair into it.
+// e^x; e^0 is exactly 1.
+__device__ __forceinline__ float exp_of(float x) { return exp2f(x * kLog2e); }
+
+// (top, sum): sum * e^top. Joins another pair into it.
 __device__ __forceinline__ void join(float &top, float &sum, float other_top, float other_sum) {
     const float most = fmaxf(top, other_top);
     if (most == -INFINITY) return;  // both empty
-    sum = sum * exp2f(top - most) + other_sum * exp2f(other_top - most);
+    sum = sum * exp_of(top - most) + other_sum * exp_of(other_top - most);
     top = most;
 }
 
@@ -107,9 +109,9 @@ __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowA
                 float most = top;
 #pragma unroll
                 for (int i = 0; i < kRowLoads; ++i) most = fmaxf(most, o[i]);
-                sum *= exp2f(top - most);
+                sum *= exp_of(top - most);
 #pragma unroll
-                for (int i = 0; i < kRowLoads; ++i) sum += x[i] * exp2f(o[i] - most);
+                for (int i = 0; i < kRowLoads; ++i) sum += x[i] * exp_of(o[i] - most);
                 top = most;
             }
         }
@@ -134,13 +136,11 @@ __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowA
                 const int64_t y = a.targets[row];
                 if (y != a.ignore) {
                     valid = 1;
-                    // log sum - (target - reference), in one rounding after the
-                    // logarithm: both are small for a row that is sure of its
-                    // target. A target outside the vocabulary has no loss: it
-                    // shows as NaN.
-                    t = y >= 0 && y < a.vocab
-                            ? fmaf(-kLn2, fmaf(a.target_logit[row], kLog2e, -top), logf(sum))
-                            : NAN;
+                    // log sum + (top - target): the sum is at least 1, the
+                    // target at most top, and both terms are small for a row
+                    // that is sure of its target. A target outside the
+                    // vocabulary has no loss: it shows as NaN.
+                    t = y >= 0 && y < a.vocab ? logf(sum) + (top - a.target_logit[row]) : NAN;
                 }
                 if (a.token_loss != nullptr) a.token_loss[row] = t;
             }
@@ -249,25 +249,27 @@ template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __gri
     const int64_t row0 = int64_t(block % a.row_blocks) * kGradRows;
     const int64_t col0 = int64_t(block / a.row_blocks) * kGradCols;
     constexpr float kGain = DT == FSDP_F16 ? kHalfGain : 1.0f;
+    constexpr float kFactor = DT == FSDP_F32 ? kGain : kGain / kExpGain;
     wait_previous();
     allow_next();
     for (int i = threadIdx.x; i < kGradRows * (kGradCols / kSpan); i += 256) {
         const int r = i % kGradRows, s = i / kGradRows;
         const int64_t row = row0 + r, span = col0 / kSpan + s;
         if (row < a.rows) {
-            // e * 2^(off - reference) / sum is the probability; a target outside
-            // the vocabulary makes the row's gradient NaN, as its loss is
+            // e times e^(the span's largest - the row's) / sum is the
+            // probability; a target outside the vocabulary makes the row's
+            // gradient NaN, as its loss is
             const int64_t y = a.targets[row], at = y - col0;
             const bool bad = y != a.ignore && (y < 0 || y >= a.vocab);
             const float2 state = a.row_state[row];
             if (span * kSpan < a.vocab)
-                factor[s][r] = bad ? NAN : kGain * exp2f(a.off[span * a.ld_rows + row] - state.x) / state.y;
+                factor[s][r] = bad ? NAN : kFactor * exp_of(a.off[span * a.ld_rows + row] - state.x) / state.y;
             if (s == 0) {
                 hit[r] = y == a.ignore ? -2 : at >= 0 && at < kGradCols ? static_cast<int32_t>(at) : -1;
                 // the target's own d from its fp32 logit: near 1 the stored
                 // exponential's rounding would be all that is left of p - 1
                 if (hit[r] >= 0 && at + col0 < a.vocab)
-                    at_target[r] = kGain * (exp2f(fmaf(a.target_logit[row], kLog2e, -state.x)) / state.y - 1.0f);
+                    at_target[r] = kGain * (exp_of(a.target_logit[row] - state.x) / state.y - 1.0f);
             }
         }
     }

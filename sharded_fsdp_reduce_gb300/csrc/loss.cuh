@@ -13,12 +13,15 @@ namespace loss {
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kBlockK = 64;
-// Columns whose exponentials share one reference (one epilogue warp's).
+// Columns whose exponentials share one reference (one epilogue warp's), their
+// largest logit.
 constexpr int kSpan = 64;
+// What exponentials are stored times in fp16.
+constexpr float kExpGain = 32768.0f;
 
 // What a product's epilogue does with the accumulator.
 enum Epilogue {
-    kStats = 0,   // per row and span: exponent reference and sum (nothing stored)
+    kStats = 0,   // per row and span: largest logit and sum of exponentials (nothing stored)
     kExp = 1,     // kStats, and the exponentials stored (fp16, or fp32 for an fp32 head)
     kScale = 2,   // store scale * (accumulator + earlier bands)
 };
@@ -84,7 +87,7 @@ struct FewArgs {
 
 struct FewGradArgs {
     const float *hidden, *weight, *logits;
-    const float2 *row_state;  // {reference, sum} of the row's exponentials
+    const float2 *row_state;  // {largest logit, sum of the exponentials against it}
     int64_t ld_hidden, ld_weight, ld_logits, rows, vocab, dim;
     const int64_t *targets;
     int64_t ignore;

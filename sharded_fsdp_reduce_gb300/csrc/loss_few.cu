@@ -7,7 +7,7 @@
 // them with up to eight rows' hidden values (cached in L1: a few KB that all
 // warps read) in fp32, and adds up over its lanes; more rows go in groups of
 // eight whose blocks run side by side and share the weight in L2. Softmax
-// statistics run along in registers; a block leaves one (reference, sum) per
+// statistics run along in registers; a block leaves one (largest, sum) per
 // row, which the row kernel joins as it joins the spans of the matrix product.
 // fp32 heads and rows off 16 bytes are read as they are, where the product
 // would pack them first. One row of 50257 x 768 bf16: 12 us in the kernel (6.4
@@ -28,15 +28,18 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kTake = 4;  // vocabulary rows of a warp's step
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// sum * 2^top with one more term 2^(logit log2(e)).
+// e^x; e^0 is exactly 1.
+__device__ __forceinline__ float exp_of(float x) { return exp2f(x * kLog2e); }
+
+// sum * e^top with one more term e^logit.
 __device__ __forceinline__ void take(float &top, float &sum, float logit) {
-    const float most = fmaxf(top, logit * kLog2e);
-    sum = sum * exp2f(top - most) + exp2f(fmaf(logit, kLog2e, -most));
+    const float most = fmaxf(top, logit);
+    sum = sum * exp_of(top - most) + exp_of(logit - most);
     top = most;
 }
 __device__ __forceinline__ void join(float &top, float &sum, float other_top, float other_sum) {
     const float most = fmaxf(top, other_top);
-    sum = sum * exp2f(top - most) + other_sum * exp2f(other_top - most);
+    sum = sum * exp_of(top - most) + other_sum * exp_of(other_top - most);
     top = most;
 }
 
@@ -200,7 +203,7 @@ __device__ __forceinline__ float d_of(const FewGradArgs &a, int64_t t, int64_t v
     if (y == a.ignore) return 0.0f;
     if (y < 0 || y >= a.vocab) return NAN;
     const float2 state = a.row_state[t];
-    const float p = exp2f(fmaf(a.logits[t * a.ld_logits + v], kLog2e, -state.x)) / state.y;
+    const float p = exp_of(a.logits[t * a.ld_logits + v] - state.x) / state.y;
     return v == y ? p - 1.0f : p;
 }
 

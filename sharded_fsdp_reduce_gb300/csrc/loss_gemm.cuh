@@ -203,10 +203,14 @@ __device__ __forceinline__ void store_exponentials(const CUtensorMap *map, uint8
     }
 }
 
-// Softmax statistics (and exponentials) of one warp's 32 rows x 64 columns.
-// With l2 = logit * log2(e), a span's exponentials are e = 2^(l2 - off), off =
-// max(l2) - 15: at most 2^15, so that fp16 holds them with 11 bits down to
-// 2^-29 of the span's largest (what is smaller is below 2^-40 of it).
+// Softmax statistics (and exponentials) of one warp's 32 rows x 64 columns. A
+// span's exponentials are against its own largest logit, subtracted as it is:
+// the largest one is then exactly 1, the sum at least 1 and a row's loss
+// neither negative nor, for a row that is sure of its target, the difference
+// of two roundings (log2(e) times the largest would be rounded once more, and
+// past 2^31 by more than exponentials can hold). In fp16 they are stored times
+// 2^15: 11 bits down to 2^-29 of the span's largest (what is smaller is below
+// 2^-40 of it).
 template <int EP, int DT>
 __device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMap *map, uint8_t *box, int lane,
                                              float *v, int64_t row0, int64_t col0, int64_t target) {
@@ -233,10 +237,10 @@ __device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMa
         t0 = fmaxf(t0, v[j]);
         t1 = fmaxf(t1, v[j + 1]);
     }
-    const float off = fmaxf(fmaxf(t0, t1) * kLog2e, -FLT_MAX) - 15.0f;
+    const float top = fmaxf(t0, t1);
     float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kSpan; ++j) v[j] = exp2_fast(fmaf(v[j], kLog2e, -off));
+    for (int j = 0; j < kSpan; ++j) v[j] = exp2_fast((v[j] - top) * kLog2e);
 #pragma unroll
     for (int j = 0; j < kSpan; j += 4) {
         s0 += v[j];
@@ -246,8 +250,12 @@ __device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMa
     }
     if (live) {
         const int64_t to = col0 / kSpan * g.ld_rows + row;
-        g.off[to] = off;
+        g.off[to] = top;
         g.sum[to] = (s0 + s1) + (s2 + s3);
+    }
+    if constexpr (EP == kExp && DT == FSDP_F16) {
+#pragma unroll
+        for (int j = 0; j < kSpan; ++j) v[j] *= kExpGain;
     }
     if constexpr (EP == kExp) store_exponentials<DT>(map, box, lane, row0, col0, v);
 }

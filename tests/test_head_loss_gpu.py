@@ -387,6 +387,53 @@ def test_one_column_has_no_gradient(F, T, dt):
     assert bool((dw.double().abs() <= d * more * x.double().abs().sum(0) + least).all())
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("T", [1, 4, 25, 300])
+def test_one_column_has_no_loss(F, T, grad, dt):
+    """Exactly none: the only exponential is 1, and so is the sum."""
+    x, w, _ = inputs(T, 1, 64, dt, std=4.0, ignored=None, seed=T)
+    y = torch.zeros(T, dtype=torch.int64, device=DEV)
+    assert bool((run(F, x, w, y, grad=grad)[1] == 0).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("T", [4, 25, 300])
+def test_losses_of_rows_that_are_sure_of_their_target(F, T, grad, dt):
+    """From about 0.2 down to nothing. A loss is the logarithm of 1 and a few
+    small terms: never negative, 0 where they are beyond fp32. Each term is good
+    to both logits' errors and 2^-17 (the exponent, below 2^6, is rounded twice
+    by 2^-24 of itself), and a row's sum of these 700 takes at most 32 roundings
+    of 2^-24 beside the 1: 2^-19."""
+    V, D = 700, 128
+    x, w, y = inputs(T, V, D, dt, ignored=None, seed=V)
+    lift = torch.linspace(8, 40, T, device=DEV)[:, None]
+    toward = w[y].float()
+    x = (x.float() * 0.05 + lift * toward / toward.square().sum(1, keepdim=True)).to(DT[dt])
+    ref = reference(x, w, y)
+    tok = run(F, x, w, y, grad=grad)[1]
+    assert bool((tok >= 0).all()) and bool((tok[ref["tok"] < 1e-12] == 0).all())
+    le = 8 * math.sqrt(D) * 2.0 ** -23 * ref["a"]
+    bound = (2 * le + 2.0 ** -17) * ref["tok"] + 2.0 ** -19
+    assert bool(((tok.double() - ref["tok"]).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [4, 25, 300])
+@pytest.mark.parametrize("size", [1e6, 1e10, 1e30])
+def test_logits_of_any_finite_size(F, T, size, dt):
+    V, D = 700, 64
+    x, w, y = inputs(T, V, D, dt, ignored="some")
+    x *= size
+    ref = reference(x, w, y)
+    loss, tok, _, _ = run(F, x, w, y, grad=False)
+    check(ref, dt, D, (V, T), loss, tok)
+    loss, tok, dx, dw = run(F, x, w, y)
+    check(ref, dt, D, (V, T), loss, tok)
+    assert bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dw).all())
+
+
 def test_gradients_against_differences(F):
     # the loss along a direction, in fp32: (L(x + h d) - L(x - h d)) / 2h = dx . d
     T, V, D = 12, 300, 64
