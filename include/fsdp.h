@@ -502,8 +502,8 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  * columns before that, but for the target's entry, which comes from its fp32
  * logit: p - 1 is good to a few 2^-24 beside the logit's own error. A p that
  * differs from 1 by less than that shows as 1. fp32 heads: every operand as three bf16 parts, the
- * products as exact as fp32's (an infinite operand counts as the largest
- * bf16 value). A few tokens (4, or 24 of an fp32 head, for losses alone; 8
+ * products as exact as fp32's. Infinities and NaN come out as fp32 arithmetic
+ * has them, in every type and at any number of tokens. A few tokens (4, or 24 of an fp32 head, for losses alone; 8
  * of an fp32 head with gradients) are plain fp32 dot products.
  *   hidden       device, tokens rows of dim elements at stride ld_hidden.
  *   weight       device, vocab rows of dim elements at stride ld_weight.

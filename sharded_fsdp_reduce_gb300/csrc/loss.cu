@@ -223,17 +223,21 @@ struct GradArgs {
     uint32_t row_blocks;
 };
 
-// x in three bf16 parts: each takes the next 8 bits. An infinite x counts as
-// bf16's largest value: its products with another operand's lower parts,
-// which may be 0 or of the other sign, would be NaN.
+// x in three bf16 parts: each takes the next 8 bits. An infinite x is in the
+// last part alone, which is multiplied with the other operand's first one and
+// no other: the sums then see infinity times a number of that operand's sign
+// (or times 0), as they would in fp32. In the first part it would also meet
+// the other's lower parts, which may be 0 or of the other sign.
 __device__ __forceinline__ void split3(float x, float &hi, float &mid, float &lo) {
-    constexpr float kMost = 3.38953139e38f;
-    hi = __bfloat162float(__float2bfloat16_rn(x));
+    constexpr float kMost = 3.38953139e38f;  // bf16's largest: what rounds past it
+    const bool infinite = isinf(x);
+    const float y = infinite ? 0.0f : x;
+    hi = __bfloat162float(__float2bfloat16_rn(y));
     if (hi > kMost) hi = kMost;
     if (hi < -kMost) hi = -kMost;
-    const float r = isinf(x) ? 0.0f : x - hi;
+    const float r = y - hi;
     mid = __bfloat162float(__float2bfloat16_rn(r));
-    lo = r - mid;
+    lo = infinite ? x : r - mid;
 }
 
 constexpr int kGradCols = 512, kGradRows = 64;

@@ -275,6 +275,51 @@ def test_nan_in_a_row_stays_in_its_row(F, T):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [4, 8, 24, 25, 300])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_counted_row_that_is_not_finite(F, T, bad, dt):
+    """An infinite hidden value makes some logit +inf or NaN, or all -inf: its
+    row has no loss in any type and at any number of rows, nor has the sum."""
+    V, D = 500, 64
+    x, w, y = inputs(T, V, D, dt, ignored=None)
+    good = run(F, x, w, y, grad=False)[1]
+    x[3, 5] = bad
+    keep = torch.arange(T, device=DEV) != 3
+    loss, tok, _, _ = run(F, x, w, y, grad=False)
+    assert math.isnan(float(loss)) and math.isnan(float(tok[3]))
+    assert torch.equal(tok[keep], good[keep])
+    loss, tok, dx, dw = run(F, x, w, y)
+    assert math.isnan(float(loss)) and math.isnan(float(tok[3]))
+    assert bool(torch.isnan(dx[3]).all()) and bool(torch.isnan(dw).all())
+    assert not bool(torch.isnan(dx[keep]).any()) and not bool(torch.isnan(tok[keep]).any())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [4, 8, 24, 25, 300])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+def test_a_weight_that_is_infinite(F, T, bad, dt):
+    """Rows whose logit it makes +inf have no loss; for the others, at -inf,
+    its column is as if it were not there. With infinities of both signs in a
+    logit's products, nothing has a loss."""
+    V, D = 500, 64
+    x, w, y = inputs(T, V, D, dt, ignored=None)
+    y[y == 77] = 78
+    w[77, 9] = bad
+    x[0, 9], x[1, 9] = 0.5, -0.5  # (few rows might all have one sign)
+    up = x[:, 9] * bad > 0
+    assert bool(up.any()) and bool((~up).any())
+    cols = torch.arange(V, device=DEV) != 77
+    ref = reference(x[~up], w[cols], torch.where(y > 77, y - 1, y)[~up])
+    logit = 8 * math.sqrt(D) * 2.0 ** -23 * ref["a"] + 2.0 ** -20 * ref["lse"].abs().clamp(min=1)
+    for grad in (False, True):
+        tok = run(F, x, w, y, grad=grad)[1]
+        assert bool(torch.isnan(tok[up]).all())
+        assert bool(((tok[~up].double() - ref["tok"]).abs() <= logit).all())
+    w[300:310] = bad
+    assert bool(torch.isnan(run(F, x, w, y, grad=False)[1]).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("T,band", [(3, 0), (64, 0), (65, 0), (300, 0), (600, 256)])
 def test_what_lies_in_ignored_rows_does_not_matter(F, T, band, dt):
     V, D = 700, 136
