@@ -518,9 +518,9 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  *   loss         device fp32 scalar. token_loss: device fp32, tokens, or NULL.
  *   d_hidden, d_weight   device, or NULL: that gradient is not formed; with
  *                both NULL only the losses are.
- *   wait_timeouts  device uint32 or NULL: incremented by each bounded wait of
- *                this call that gave up (see "Bounded waits" above; this
- *                call's waits show here only).
+ *   wait_timeouts  device uint32 or NULL: incremented by each bounded wait (a
+ *                warp's) of this call whose time ran out (see "Bounded waits"
+ *                above; this call's waits show here only).
  * No output may overlap an input or another output. tokens may be 0. hidden
  * and weight in host memory are refused (FSDP_ERR_INVALID_ARG). */
 typedef enum { FSDP_LOSS_MEAN = 0, FSDP_LOSS_SUM = 1 } fsdp_loss_reduction;
@@ -666,6 +666,17 @@ fsdp_status fsdp_take_wait_timeouts(uint32_t *count_out);
  * usable. Asynchronous. limit_cycles must be in [1, 2^31]
  * (FSDP_ERR_INVALID_ARG otherwise, nothing launched). */
 fsdp_status fsdp_check_bounded_wait(int64_t limit_cycles, uint32_t *wait_timeouts, void *stream);
+
+/* The same for the bounded wait of fsdp_head_loss's matrix products, which a
+ * whole warp makes together: one CTA of which four warps wait for an arrival
+ * that comes after about `arrive_after_cycles` SM clock cycles (never, if
+ * negative). outcomes (device, 128 int32): per thread 1 if its wait saw the
+ * arrival and 0 if it gave up; the same within each group of 32, however
+ * close the two times are. wait_timeouts: incremented by each warp whose time
+ * ran out. Asynchronous. limit_cycles must be in [1, 2^31] and
+ * arrive_after_cycles at most 2^31 (FSDP_ERR_INVALID_ARG otherwise). */
+fsdp_status fsdp_check_head_loss_wait(int64_t limit_cycles, int64_t arrive_after_cycles, int32_t *outcomes,
+                                      uint32_t *wait_timeouts, void *stream);
 
 #ifdef __cplusplus
 }

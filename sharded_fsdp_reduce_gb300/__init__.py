@@ -9,7 +9,7 @@ from .fsdp import (OPTIMIZERS, AdamWHParams, FsdpError, StepConfig, StepGraph, S
                    fsdp_reduce_scatter_step, fsdp_status_string, fsdp_step_units, fsdp_step_units_ex,
                    fsdp_step_units_ex_launches, fsdp_step_units_launches, fsdp_take_wait_timeouts,
                    fsdp_unflatten_views)
-from .loss import HeadLoss, fsdp_head_loss
+from .loss import HeadLoss, fsdp_check_head_loss_wait, fsdp_head_loss
 from .unit import FlatParamUnit, UnitSequence
 
 __all__ = [
@@ -18,5 +18,5 @@ __all__ = [
     "fsdp_reduce_scatter_adam_cast_gather", "fsdp_reduce_scatter_step", "fsdp_all_gather",
     "fsdp_status_string", "fsdp_last_cuda_error", "fsdp_take_wait_timeouts", "fsdp_check_bounded_wait",
     "UnitDescs", "fsdp_step_units", "fsdp_step_units_ex", "StepGraph", "StepPlan", "fsdp_step_units_launches",
-    "fsdp_step_units_ex_launches", "HeadLoss", "fsdp_head_loss", "GradClip", "ClipPlan",
+    "fsdp_step_units_ex_launches", "HeadLoss", "fsdp_head_loss", "fsdp_check_head_loss_wait", "GradClip", "ClipPlan",
 ]

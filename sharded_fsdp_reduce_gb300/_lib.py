@@ -55,6 +55,7 @@ EXPORTS = (
     "fsdp_step_plan_destroy",
     "fsdp_head_loss_workspace",
     "fsdp_head_loss",
+    "fsdp_check_head_loss_wait",
     "fsdp_grad_norm_workspace",
     "fsdp_grad_norm",
     "fsdp_clip_grads",
@@ -163,6 +164,7 @@ def load() -> ctypes.CDLL:
             "fsdp_step_plan_launch_ex": (i32, [vp, ctypes.POINTER(FsdpStepConfig), vp]),
             "fsdp_step_plan_destroy": (i32, [vp]),
             "fsdp_head_loss_workspace": (i32, [ctypes.POINTER(FsdpHeadLossArgs), ctypes.POINTER(i64)]),
+            "fsdp_check_head_loss_wait": (i32, [i64, i64, vp, vp, vp]),
             "fsdp_head_loss": (i32, [ctypes.POINTER(FsdpHeadLossArgs), vp, i64, vp]),
             "fsdp_grad_norm_workspace": (i32, [vp, vp, i32, ctypes.POINTER(i64)]),
             "fsdp_grad_norm": (i32, [vp, vp, vp, i32, ctypes.c_float, vp, vp, i64, vp]),

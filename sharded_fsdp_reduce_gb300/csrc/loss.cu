@@ -1045,4 +1045,14 @@ FSDP_API fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *works
     return loss::run(a, p, static_cast<uint8_t *>(workspace), s);
 }
 
+FSDP_API fsdp_status fsdp_check_head_loss_wait(int64_t limit_cycles, int64_t arrive_after_cycles, int32_t *outcomes,
+                                               uint32_t *wait_timeouts, void *stream) {
+    constexpr int64_t kMost = int64_t(1) << 31;
+    if (limit_cycles < 1 || limit_cycles > kMost || arrive_after_cycles > kMost || !outcomes)
+        return FSDP_ERR_INVALID_ARG;
+    if (!aligned(outcomes, 4) || !aligned(wait_timeouts, 4)) return FSDP_ERR_ALIGNMENT;
+    return loss::launch_wait_check(limit_cycles, arrive_after_cycles, outcomes, wait_timeouts,
+                                   static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

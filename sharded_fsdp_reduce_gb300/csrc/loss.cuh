@@ -65,6 +65,12 @@ fsdp_status launch_grad_bf16(Orders o, const CUtensorMap &a, const CUtensorMap &
 fsdp_status launch_grad_f16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
 fsdp_status launch_grad_f32(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
 
+// Four warps wait, for at most `limit` cycles, for an arrival that comes after
+// `arrive_after` cycles (never, if negative). outcomes[128]: 1 per thread
+// whose wait saw it.
+fsdp_status launch_wait_check(long long limit, long long arrive_after, int32_t *outcomes, uint32_t *timeouts,
+                              cudaStream_t s);
+
 // A few rows (loss_few.cu): the statistics per block instead of per span of
 // columns. Up to where the matrix products take over: losses of 4 rows of
 // 50257 x 768 bf16 24 us against 27, of 8 rows 43 against 26. An fp32 weight is

@@ -114,18 +114,25 @@ __device__ __forceinline__ void k_range(const GemmArgs &g, int split, int &begin
     end = begin + g.k_each + (split < g.k_more ? 1 : 0);
 }
 
-// Bounded wait; false once any wait of this CTA has given up.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Barriers *b, uint32_t *timeouts) {
-    if (tma::mbar_try_wait(bar, parity)) return true;
+// Bounded wait of a whole warp: all of its lanes get the same answer, since
+// what follows (tensor-memory reads, elections) needs them together. False
+// once any wait of this CTA has given up; `timeouts` counts the warps whose
+// time ran out.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Barriers *b, uint32_t *timeouts,
+                                     long long limit = kWaitCycles) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    if (__all_sync(kAll, tma::mbar_try_wait(bar, parity))) return true;
     const long long t0 = clock64();
     volatile int32_t *gave_up = &b->gave_up;
-    while (!tma::mbar_try_wait(bar, parity)) {
-        if (*gave_up) return false;
-        if (clock64() - t0 > kWaitCycles) {
+    while (!__all_sync(kAll, tma::mbar_try_wait(bar, parity))) {
+        // one lane's flag and clock decide for all
+        const int state = __shfl_sync(kAll, *gave_up ? 1 : clock64() - t0 > limit ? 2 : 0, 0);
+        if (state == 0) continue;
+        if (state == 2 && threadIdx.x % 32 == 0) {
             *gave_up = 1;
             if (timeouts) atomicAdd(timeouts, 1u);
-            return false;
         }
+        return false;
     }
     return true;
 }

@@ -18,7 +18,7 @@ from . import _lib
 from .fsdp import _check, _counter, _on_current_device, dtype_code
 from .workspace import Workspace, take
 
-__all__ = ["HeadLoss", "fsdp_head_loss"]
+__all__ = ["HeadLoss", "fsdp_head_loss", "fsdp_check_head_loss_wait"]
 
 _REDUCTIONS = {"mean": _lib.FSDP_LOSS_MEAN, "sum": _lib.FSDP_LOSS_SUM}
 
@@ -114,6 +114,18 @@ def fsdp_head_loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
     with torch.cuda.stream(s):  # taken, and given back, in that stream's order
         ws = _workspace(_workspace_bytes(a), hidden.device)
     _check(_launch(a, ws.data_ptr(), ws.numel(), s), "fsdp_head_loss")
+
+
+def fsdp_check_head_loss_wait(limit_cycles: int, arrive_after_cycles: int, outcomes: torch.Tensor,
+                              wait_timeouts: Optional[torch.Tensor] = None,
+                              stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Self-test of the matrix products' bounded wait (see include/fsdp.h):
+    outcomes (int32 [128]) gets 1 per thread whose wait saw the arrival."""
+    at = _vector(outcomes, "outcomes", 128, torch.int32, torch.cuda.current_device())
+    s = stream if stream is not None else torch.cuda.current_stream()
+    _check(_lib.load().fsdp_check_head_loss_wait(int(limit_cycles), int(arrive_after_cycles), at,
+                                                 _counter(wait_timeouts, "wait_timeouts"), s.cuda_stream),
+           "fsdp_check_head_loss_wait")
 
 
 class HeadLoss:

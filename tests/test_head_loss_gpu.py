@@ -729,3 +729,37 @@ def test_a_workspace_too_small_is_refused(F):
     assert lib.fsdp_head_loss(ctypes.byref(a), ws.data_ptr(), need - 1, None) == _lib.FSDP_ERR_INVALID_ARG
     assert lib.fsdp_head_loss(ctypes.byref(a), ws.data_ptr() + 16, need, None) == _lib.FSDP_ERR_ALIGNMENT
     assert lib.fsdp_head_loss(ctypes.byref(a), None, need, None) == _lib.FSDP_ERR_INVALID_ARG
+
+
+def test_a_bounded_wait_has_one_outcome_per_warp(F):
+    """The products' waits, without a fault: an arrival that never comes runs
+    out and is counted, one in time is seen, and one that comes as the limit
+    passes has the same outcome in all lanes of a warp."""
+    out = torch.empty(128, dtype=torch.int32, device=DEV)
+    waits = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def check_wait(limit, arrive):
+        waits.zero_()
+        F.fsdp_check_head_loss_wait(limit, arrive, out, waits)
+        torch.cuda.synchronize()
+        warps = out.reshape(4, 32)
+        assert bool((warps == warps[:, :1]).all()), (limit, arrive, warps.tolist())
+        gave_up = int((warps[:, 0] == 0).sum())
+        assert (1 if gave_up else 0) <= int(waits) <= gave_up
+        return gave_up
+
+    assert check_wait(1 << 20, -1) == 4
+    assert check_wait(1 << 20, 1000) == 0
+    for k in range(200):
+        limit = 2000 + 97 * k
+        check_wait(limit, limit + 13 * (k % 41) - 250)
+    with pytest.raises(F.FsdpError):
+        F.fsdp_check_head_loss_wait(0, 10, out)
+    with pytest.raises(F.FsdpError):
+        F.fsdp_check_head_loss_wait(10, (1 << 31) + 1, out)
+    with pytest.raises(ValueError):
+        F.fsdp_check_head_loss_wait(10, 10, out[:64])
+    # the context still works
+    x, w, y = inputs(40, 300, 64, "bf16")
+    loss, tok, dx, dw = run(F, x, w, y)
+    check(reference(x, w, y), "bf16", 64, (300, 40), loss, tok, dx, dw)
