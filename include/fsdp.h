@@ -566,11 +566,12 @@ fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *workspace, int
 
 /* The global L2 norm of many tensors (device), in one pass:
  *   norm = |scale| * sqrt(sum over tensors and elements of x^2)
- * to *norm_out (device fp32). Squares are added in fp32 eight at a time and
- * in fp64 from there, in an order the sizes fix: the same bits every time,
- * and no overflow or underflow while the norm itself is a finite fp32. A
- * NaN element makes it NaN, an infinite one infinite. Empty tensors and an
- * empty list (norm 0) are fine.
+ * to *norm_out (device fp32). Up to 32 squares are added in fp32, those sums
+ * in pairs of floats (the sum and what its roundings lost) over a block, and
+ * in fp64 over the blocks, in an order the sizes fix: the same bits every
+ * time, within 2^-21 of the exact norm, and no overflow or underflow while
+ * the norm itself is a finite fp32. A NaN element makes it NaN, an infinite
+ * one infinite. Empty tensors and an empty list (norm 0) are fine.
  *   tensors, numels, dtypes  host arrays: device (or mapped host) addresses,
  *                element counts and fsdp_dtype values; any alignment.
  *   scale        what the gradients are multiplied by before they count (the

@@ -5,9 +5,10 @@
 //   norm = |scale| * sqrt(sum over all units and elements of g^2)
 //
 // Bound by HBM (708 M bf16 elements 231 us, 6.2 TB/s; 85 M of eight ranks with
-// the average written 252 us, 6.7 TB/s): N gradients are read (16-byte streaming loads) and, for the
-// clipped step of many ranks, the fp32 average is written. Squares of a
-// few values are added in fp32, those sums in pairs of floats (the sum and what
+// the average written 252 us, 6.7 TB/s): N gradients are read (16-byte
+// streaming loads) and, for the clipped step of many ranks, the fp32 average
+// is written. Up to 32 squares (chunks_together) are added in fp32, which is
+// within 9 roundings of 2^-24, those sums in pairs of floats (the sum and what
 // its rounding lost) per thread and warp, and in fp64 per block and call, in
 // an order fixed by the sizes, so the norm is the same bits every time: this
 // part's fp64 units take 64 cycles for a warp's add, and adds per chunk held a
