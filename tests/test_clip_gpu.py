@@ -402,6 +402,45 @@ def test_clipped_step_on_another_stream_and_repeated(F):
         assert torch.equal(a.master, b.master) and torch.equal(a.full[0], b.full[0])
 
 
+@pytest.mark.parametrize("world,gdt", [(8, BF16), (2, BF16), (1, F32)])
+def test_many_clipped_steps_in_a_row(F, world, gdt):
+    """Steps that start while the one before drains, on units that fill the
+    part: every step reads the state that the one before has written."""
+    sizes = [3_000_007, 700_003, 1_000_000, 5]
+    a = make_units(F, sizes, world, gdt, BF16, 20, n_full=1)
+    b = make_units(F, sizes, world, gdt, BF16, 20, n_full=1)
+    clipped, plain = F.UnitSequence(a), F.UnitSequence(b)
+    clipped.clip_step(F.AdamWHParams(**dict(HP, step=1)), float("inf"))
+    plain.step(F.AdamWHParams(**dict(HP, step=1)))
+    torch.cuda.synchronize()
+    norm = torch.empty((), device=DEV)
+    for t in range(2, 60):
+        clipped.clip_step(F.AdamWHParams(**dict(HP, step=t)), float("inf"), norm=norm)
+    for t in range(2, 60):
+        plain.step(F.AdamWHParams(**dict(HP, step=t)))
+    torch.cuda.synchronize()
+    for ua, ub in zip(a, b):
+        for name in ("master", "exp_avg", "exp_avg_sq"):
+            assert torch.equal(getattr(ua, name).view(torch.int32), getattr(ub, name).view(torch.int32)), name
+        assert torch.equal(ua.full[0], ub.full[0])
+    assert_norm(norm, norm64([average(u, 1.0) for u in a]))
+
+
+def test_many_clips_in_a_row(F):
+    ts = [rand(n, BF16, 40 + n % 7) for n in (2_000_003, 17, 900_001)]
+    ref = [t.clone() for t in ts]
+    clip = F.GradClip(ts, scale=0.75)
+    norms = torch.empty(30, device=DEV)
+    for k in range(30):
+        clip.norm(norms[k])
+        clip.clip(float("inf"), norms[k])
+    torch.cuda.synchronize()
+    for k in range(30):
+        assert_norm(norms[k], norm64(ref, 0.75))
+        ref = [(r.float() * 0.75).to(BF16) for r in ref]
+    assert all(torch.equal(t, r) for t, r in zip(ts, ref))
+
+
 def test_a_captured_clipped_step_outlives_a_change_of_arguments(F):
     """A captured graph of clipped steps keeps writing to the workspace that
     they were captured with, whatever plan later calls make."""
