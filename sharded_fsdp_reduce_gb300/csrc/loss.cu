@@ -14,6 +14,14 @@
 // instead of the four that forming the logits again would take, for one pass
 // over the band (4 bytes an element): with D = 8192 a product's operations
 // take 8 times that pass, with D = 768 about as long.
+//
+// What has fewer than 32 bits, for 16-bit heads: the stored exponentials (fp16)
+// and d (the head's type, fp16 times 2^14), because the tensor cores take 16-bit
+// operands and the pass is bound by its bytes. The gradients' error against 64
+// bits is then 1.9e-3 for bf16 and 2.4e-4 for fp16 (1021 x 50257 x 768, 4096 x
+// 50257 x 1280), where rounding nothing but the result leaves 1.7e-3 and 2.1e-4.
+// Losses, sums, statistics and the target's p - 1 are fp32; fp32 heads keep
+// fp32 exponentials and d in three parts.
 #include <math.h>
 #include <string.h>
 

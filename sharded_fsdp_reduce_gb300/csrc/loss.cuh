@@ -72,11 +72,14 @@ fsdp_status launch_wait_check(long long limit, long long arrive_after, int32_t *
                               cudaStream_t s);
 
 // A few rows (loss_few.cu): the statistics per block instead of per span of
-// columns. Up to where the matrix products take over: losses of 4 rows of
-// 50257 x 768 bf16 24 us against 27, of 8 rows 43 against 26. An fp32 weight is
-// packed first for the products: losses of 24 rows of 32000 x 4096 324 us
-// against 433, of 50257 x 768 137 against 142; gradients of 4 rows 362 against
-// 756 and 141 against 256, of 16 rows 950 against 762.
+// columns. Up to about where the matrix products take over, dot products
+// against those (us on the device, at 50257 x 768 / 32000 x 4096 / 128000 x
+// 8192): bf16 losses of 4 rows 25 to 26 / 64 to 63 / 376 to 403, of 5 rows 55 to
+// 26 / 123 to 69 / 716 to 382. An fp32 weight is packed first for the products:
+// losses of 16 rows 108 to 134 / 269 to 416 / 2207 to 3037, of 24 rows 156 to
+// 134 / 336 to 420 / 3171 to 3034, of 32 rows 200 to 134 / 445 to 421 / 3977 to
+// 3044; gradients of 8 rows 207 to 242 / 608 to 732 / 4365 to 5286, of 12 rows
+// 316 to 245 / 836 to 734 / 6363 to 5291.
 inline int64_t few_rows(int dtype, bool grad) { return dtype == FSDP_F32 ? (grad ? 8 : 24) : (grad ? 0 : 4); }
 
 struct FewArgs {

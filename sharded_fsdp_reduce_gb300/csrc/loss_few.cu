@@ -10,8 +10,9 @@
 // statistics run along in registers; a block leaves one (largest, sum) per
 // row, which the row kernel joins as it joins the spans of the matrix product.
 // fp32 heads and rows off 16 bytes are read as they are, where the product
-// would pack them first. One row of 50257 x 768 bf16: 12 us in the kernel (6.4
-// TB/s); of 32000 x 4096 49 us with the row kernel (5.4 TB/s).
+// would pack them first. One row of 50257 x 768 bf16: 10 us in the kernel where
+// the weight is partly in L2, 20 where it is not (3.9 TB/s), 15.5 with the row
+// kernel in a loop; of 32000 x 4096 49 us with it (5.4 TB/s).
 //
 // Gradients of up to eight rows of an fp32 head go the same way (few_dx_kernel,
 // few_dw_kernel), from the logits that this pass leaves: the products' way

@@ -16,10 +16,10 @@
 // deliver. Persistent: one CTA per SM, tiles taken in a fixed order that keeps
 // the reused operand in L2.
 //
-// Bound by the tensor pipes where K is long (2048 x 32000 x 5120: 353 us, 97.8 %
-// active, 1.90 PFLOP/s; under the power cap 4096 x 128000 x 8192 runs at 1.65 to
+// Bound by the tensor pipes where K is long (2048 x 32000 x 5120: 354 us, 97.9 %
+// active, 1.90 PFLOP/s; under the power cap 4096 x 128000 x 8192 runs at 1.50 to
 // 1.70), by the operands' latency where a tile has few K blocks (1021 x 50257 x
-// 768: 60 us, 65 % active).
+// 768: 59 us, 67 % active).
 //
 // Roles by warp: 0 loads A and 3 loads B, 1 issues the products, 2 owns tensor
 // memory, 4-19 are the epilogue: warp w reads lanes 32 (w % 4) .. + 31 (one
@@ -47,18 +47,19 @@ namespace loss {
 
 constexpr int kThreads = 640;
 constexpr int kEpilogueWarps = 16;
-// Stages of operands in shared memory. More would fit (6 and 7), and take a
-// little off products of few tiles, but cost long ones: 4096 x 128000 x 8192
-// with its gradients 15.7 ms with these, 15.9 with one more each; the hidden
-// gradient of 1021 x 50257 x 768 wants 6 (54 against 57 us with 5).
+// Stages of operands in shared memory. One more each would fit: 4096 x 128000 x
+// 8192 with its gradients takes 15.4 to 15.6 ms either way, the hidden gradient
+// of 1021 x 50257 x 768, a split product of few tiles, 62 us with these and 55
+// with one more (of 215 in all), its other products the same.
 constexpr int stages(int epilogue, int planes) { return planes == 3 ? 2 : epilogue == kExp ? 5 : 6; }
 constexpr int kMaxStages = 6;
 // K blocks summed in tensor memory before the sum moves to registers. The
 // tensor cores' own sum loses bits at every K = 16 (a chain of 5120 / 16 adds
 // left a loss 2.4e-6 off, 64 bits against it); chains of 512 / 16 joined by
 // rounded fp32 adds do not show in fp32 results, chains of 2048 / 16 not in
-// 16-bit ones. A move every 8 blocks costs about 4 % against every 16 (4096 x
-// 128000 x 8192: 5.43 ms a product against 5.20).
+// 16-bit ones. A move every 8 blocks costs up to 4 % against every 16 where K
+// is split (the hidden gradient of 4096 x 50257 x 1280 358 us against 344) and
+// nothing that shows elsewhere (4096 x 128000 x 8192 15.4 to 15.6 ms in all).
 constexpr int chunk_blocks(int epilogue, int dtype, int planes) {
     return planes == 3 ? 1 : epilogue == kScale && dtype != FSDP_F32 ? 32 : 8;  // (a block of planes is 24 adds)
 }
