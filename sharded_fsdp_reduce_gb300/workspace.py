@@ -8,11 +8,13 @@ import torch
 __all__ = ["Workspace", "take"]
 
 
-def take(nbytes: int, device, alignment: int = 512, zeroed: bool = False) -> torch.Tensor:
+def take(nbytes: int, device, alignment: int = 256, zeroed: bool = False) -> torch.Tensor:
     """nbytes of the allocator's memory at a multiple of `alignment`, in the
     current stream's order."""
-    room = alignment if alignment > 512 else 0  # torch aligns allocations to 512 bytes
-    whole = (torch.zeros if zeroed else torch.empty)(nbytes + room, dtype=torch.uint8, device=device)
+    make = torch.zeros if zeroed else torch.empty
+    if alignment <= 256:  # every CUDA allocation's
+        return make(nbytes, dtype=torch.uint8, device=device)
+    whole = make(nbytes + alignment, dtype=torch.uint8, device=device)
     return whole.narrow(0, -whole.data_ptr() % alignment, nbytes)
 
 
@@ -22,7 +24,7 @@ class Workspace:
     have had another user on the stream it is taken on, whose work is still
     queued there: other streams wait for that."""
 
-    def __init__(self, nbytes: int, device, alignment: int = 512, zeroed: bool = False):
+    def __init__(self, nbytes: int, device, alignment: int = 256, zeroed: bool = False):
         self.buf = take(nbytes, device, alignment, zeroed)
         self._device = self.buf.get_device()
         self._zeroed = zeroed

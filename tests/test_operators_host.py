@@ -212,6 +212,19 @@ def test_binding_refuses_tensors_that_are_not_on_the_gpu():
         F.HeadLoss(10, 8, torch.bfloat16, 4, reduction="none")
 
 
+def test_workspace_memory_at_any_base():
+    """The memory is found at its alignment wherever the allocator's block begins."""
+    from sharded_fsdp_reduce_gb300.workspace import take
+    held = []
+    for n in (0, 1, 100, 4096, 70_001):
+        for k in range(8):
+            buf = take(n, "cpu", alignment=1024, zeroed=k % 2 == 0)
+            assert buf.numel() == n and (n == 0 or buf.data_ptr() % 1024 == 0)
+            assert k % 2 or not bool(buf.any())
+            assert take(n, "cpu", zeroed=True).numel() == n
+            held.append((buf, bytearray(100 + 16 * k)))
+
+
 def test_a_workspace_of_another_device_is_refused(monkeypatch):
     """An object made on one GPU and called with another one current, its
     tensors there: the workspace would reach the kernels as a foreign address."""
