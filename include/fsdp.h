@@ -564,6 +564,72 @@ fsdp_status fsdp_head_loss_workspace(const fsdp_head_loss_args *args, int64_t *b
  * nothing is kept in it between calls. */
 fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* The token embedding (device): rows of a table, times a factor,
+ *   out[t] = scale * weight[tokens[t]],
+ * formed in fp32 and rounded once to dtype. A token equal to ignore_index has a
+ * row of zeros; any other one outside [0, vocab) a row of NaN.
+ *   tokens       device int64, count (which may be 0).
+ *   weight       device, vocab rows of dim elements at stride ld_weight.
+ *   out          device, count rows of dim elements at stride ld_out; overlaps
+ *                no input.
+ *   dtype        fsdp_dtype of weight and out. Any alignment; rows that are
+ *                16-byte aligned on both sides take the vectorised path.
+ *   scale        finite; 1 if none. */
+typedef struct {
+    const int64_t *tokens;
+    int64_t count;
+    int64_t vocab;
+    int64_t dim;
+    int64_t ignore_index;
+    const void *weight;
+    int64_t ld_weight;
+    void *out;
+    int64_t ld_out;
+    int32_t dtype;        /* fsdp_dtype */
+    float scale;
+    int32_t reserved;     /* must be 0 */
+} fsdp_embed_args;
+
+fsdp_status fsdp_embed(const fsdp_embed_args *args, void *stream);
+
+/* Its gradient (device):
+ *   d_weight[v] = scale * (sum of d_out[t] over the tokens t equal to v)
+ * The rows of one token add up in fp32, in groups that the sizes fix and in the
+ * tokens' order (the same bits every time), and the result is rounded once to
+ * dtype. Tokens equal to ignore_index, or outside [0, vocab), count nowhere;
+ * their rows of d_out are not read.
+ *   accumulate   0: the whole table is written, with zeros where no token
+ *                points. 1: the sums are added (in fp32, rounded once) to what
+ *                d_weight holds, rows that no token uses stay as they are: a
+ *                table tied to the head, whose gradient is there already, or
+ *                another micro-batch.
+ *   d_out        device, count rows of dim elements at stride ld_d_out.
+ *   d_weight     device, vocab rows of dim elements at stride ld_d_weight, such
+ *                as a parameter's view of a flat gradient buffer; overlaps no
+ *                input.
+ *   workspace    device, fsdp_embed_grad_workspace's bytes, 256-byte aligned,
+ *                overlapping no buffer of the call; its contents before the
+ *                call do not matter and nothing is kept in it between calls.
+ *                The bytes are enough for every call of fewer tokens too, all
+ *                else but addresses and strides alike. */
+typedef struct {
+    const int64_t *tokens;
+    int64_t count;
+    int64_t vocab;
+    int64_t dim;
+    int64_t ignore_index;
+    const void *d_out;
+    int64_t ld_d_out;
+    void *d_weight;
+    int64_t ld_d_weight;
+    int32_t dtype;        /* fsdp_dtype of d_out and d_weight */
+    float scale;
+    int32_t accumulate;
+} fsdp_embed_grad_args;
+
+fsdp_status fsdp_embed_grad_workspace(const fsdp_embed_grad_args *args, int64_t *bytes_out);
+fsdp_status fsdp_embed_grad(const fsdp_embed_grad_args *args, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* The global L2 norm of many tensors (device), in one pass:
  *   norm = |scale| * sqrt(sum over tensors and elements of x^2)
  * to *norm_out (device fp32). Up to 32 squares are added in fp32, those sums

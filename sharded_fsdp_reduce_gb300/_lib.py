@@ -56,6 +56,9 @@ EXPORTS = (
     "fsdp_head_loss_workspace",
     "fsdp_head_loss",
     "fsdp_check_head_loss_wait",
+    "fsdp_embed",
+    "fsdp_embed_grad_workspace",
+    "fsdp_embed_grad",
     "fsdp_grad_norm_workspace",
     "fsdp_grad_norm",
     "fsdp_clip_grads",
@@ -112,6 +115,20 @@ class FsdpHeadLossArgs(ctypes.Structure):
                 ("d_weight", ctypes.c_void_p), ("ld_d_weight", ctypes.c_int64), ("wait_timeouts", ctypes.c_void_p)]
 
 
+class FsdpEmbedArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("count", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("ignore_index", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("ld_weight", ctypes.c_int64), ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class FsdpEmbedGradArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("count", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("ignore_index", ctypes.c_int64), ("d_out", ctypes.c_void_p),
+                ("ld_d_out", ctypes.c_int64), ("d_weight", ctypes.c_void_p), ("ld_d_weight", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("accumulate", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -166,6 +183,9 @@ def load() -> ctypes.CDLL:
             "fsdp_head_loss_workspace": (i32, [ctypes.POINTER(FsdpHeadLossArgs), ctypes.POINTER(i64)]),
             "fsdp_check_head_loss_wait": (i32, [i64, i64, vp, vp, vp]),
             "fsdp_head_loss": (i32, [ctypes.POINTER(FsdpHeadLossArgs), vp, i64, vp]),
+            "fsdp_embed": (i32, [ctypes.POINTER(FsdpEmbedArgs), vp]),
+            "fsdp_embed_grad_workspace": (i32, [ctypes.POINTER(FsdpEmbedGradArgs), ctypes.POINTER(i64)]),
+            "fsdp_embed_grad": (i32, [ctypes.POINTER(FsdpEmbedGradArgs), vp, i64, vp]),
             "fsdp_grad_norm_workspace": (i32, [vp, vp, i32, ctypes.POINTER(i64)]),
             "fsdp_grad_norm": (i32, [vp, vp, vp, i32, ctypes.c_float, vp, vp, i64, vp]),
             "fsdp_clip_grads": (i32, [vp, vp, vp, vp, i32, vp, ctypes.c_float, ctypes.c_float, vp]),
