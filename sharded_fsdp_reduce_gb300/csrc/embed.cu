@@ -16,7 +16,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 template <int DT, bool VEC> __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
-    using S = Slice<DT, VEC>;
+    using S = Slice<DT, VEC, kLookupWords>;
     wait_previous();
     allow_next();
     const int64_t at = int64_t(blockIdx.x) * kWarps + threadIdx.x / 32;
@@ -62,7 +62,7 @@ template <int DT> fsdp_status launch_type(LookupArgs a, cudaStream_t s) {
     // whole words: both sides aligned, and rows of whole words
     const bool vec = aligned(a.weight, 16) && aligned(a.out, 16) && a.weight_bytes % 16 == 0 && a.out_bytes % 16 == 0 &&
                      a.dim * Dtype<DT>::kSize % 16 == 0;
-    const int64_t cols = slice_cols(DT, vec);
+    const int64_t cols = slice_cols(kLookupWords, DT, vec);
     a.slices = (a.dim + cols - 1) / cols;
     const int64_t blocks = (a.n * a.slices + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
@@ -102,39 +102,17 @@ fsdp_status check(int dtype, int64_t n, int64_t vocab, int64_t dim, const void *
 
 struct Plan {
     bool vec;
-    int32_t passes, bits, chunk;
-    int64_t chunks, slices, ld_part;
+    int32_t passes, bits;
+    int32_t block;
+    int64_t blocks, slices, ld_part;
     // byte offsets into the workspace
-    int64_t key[2], pos[2], part, bytes;
+    int64_t key[2], pos[2], tickets, part, bytes;
 };
 
 bool vectors(const fsdp_embed_grad_args &a) {
     const int size = dtype_size(a.dtype);
     return aligned(a.d_out, 16) && aligned(a.d_weight, 16) && a.ld_d_out * size % 16 == 0 &&
            a.ld_d_weight * size % 16 == 0 && a.dim * size % 16 == 0;
-}
-
-// Sorted entries that a warp adds up: many make few sums that cross from one
-// warp to the next, few make enough warps for every SM (16 resident each).
-int32_t chunk_of(int64_t n, int64_t slices) {
-    const int64_t warps = int64_t(sm_count() > 0 ? sm_count() : 1) * 16;
-    for (int32_t c = 32; c > 8; c /= 2)
-        if (ceil_div(n, c) * slices >= warps) return c;
-    return 8;
-}
-
-// The most chunks of any call of at most n tokens: fewer tokens may be cut
-// into smaller ones, each size's up to where the next size takes over.
-int64_t most_chunks(int64_t n, int64_t slices) {
-    const int64_t warps = int64_t(sm_count() > 0 ? sm_count() : 1) * 16;
-    const int32_t last = chunk_of(n, slices);
-    int64_t most = ceil_div(n, last);
-    for (int32_t c = 8; c < last; c *= 2) {
-        const int64_t below = ceil_div(warps, slices) * 2 * c;
-        const int64_t chunks = ceil_div(n < below ? n : below, c);
-        most = chunks > most ? chunks : most;
-    }
-    return most;
 }
 
 // p.bytes is enough for every call of no more tokens, however aligned.
@@ -146,10 +124,14 @@ Plan make_plan(const fsdp_embed_grad_args &a) {
     while ((a.vocab >> bits) != 0) ++bits;
     p.passes = (bits + kMostBits - 1) / kMostBits;
     p.bits = (bits + p.passes - 1) / p.passes;
-    const int64_t cols = slice_cols(a.dtype, p.vec);
-    p.slices = ceil_div(a.dim, cols);
-    p.chunk = chunk_of(n, p.slices);
-    p.chunks = ceil_div(n, p.chunk);
+    p.slices = ceil_div(a.dim, slice_cols(kSumWords, a.dtype, p.vec));
+    // long blocks where there are enough of them: eight for each place of the
+    // four on an SM
+    const int64_t ctas = int64_t(sm_count() > 0 ? sm_count() : 1) * 32;
+    p.block = kMostBlock;
+    while (p.block > kLeastBlock && ceil_div(n, p.block) * p.slices < ctas) p.block /= 2;
+    p.blocks = ceil_div(n, p.block);
+    const int64_t most_blocks = ceil_div(n, kLeastBlock);
     p.ld_part = round_up(a.dim, 8);
     int64_t at = 0;
     auto take = [&at](int64_t bytes) {
@@ -161,9 +143,8 @@ Plan make_plan(const fsdp_embed_grad_args &a) {
         p.key[i] = take(4 * n);
         p.pos[i] = take(4 * n);
     }
-    const int64_t aligned_slices = ceil_div(a.dim, slice_cols(a.dtype, a.dim * dtype_size(a.dtype) % 16 == 0));
-    const int64_t one = most_chunks(n, p.slices), other = most_chunks(n, aligned_slices);
-    p.part = take(8 * (one > other ? one : other) * p.ld_part);
+    p.tickets = take(4 * most_blocks * ceil_div(a.dim, slice_cols(kSumWords, a.dtype, false)));  // (the shortest slices)
+    p.part = take(8 * most_blocks * p.ld_part);
     p.bytes = at;
     return p;
 }
@@ -182,6 +163,8 @@ fsdp_status run_grad(const fsdp_embed_grad_args &a, const Plan &p, uint8_t *ws, 
         o.key[i] = reinterpret_cast<uint32_t *>(ws + p.key[i]);
         o.pos[i] = reinterpret_cast<uint32_t *>(ws + p.pos[i]);
     }
+    o.tickets = reinterpret_cast<uint32_t *>(ws + p.tickets);
+    o.n_tickets = static_cast<uint32_t>(p.blocks * p.slices);
     if (a.count > 0 && (st = launch_sort(o, s)) != FSDP_OK) return st;
     if (!a.accumulate) {
         // rows that no token uses, while a few SMs sort
@@ -203,8 +186,9 @@ fsdp_status run_grad(const fsdp_embed_grad_args &a, const Plan &p, uint8_t *ws, 
     r.weight_bytes = a.ld_d_weight * size;
     r.part = reinterpret_cast<float *>(ws + p.part);
     r.ld_part = p.ld_part;
-    r.chunk = p.chunk;
-    r.chunks = static_cast<uint32_t>(p.chunks);
+    r.tickets = o.tickets;
+    r.blocks = static_cast<uint32_t>(p.blocks);
+    r.block = p.block;
     r.slices = static_cast<uint32_t>(p.slices);
     r.accumulate = a.accumulate;
     r.scale = a.scale;
@@ -262,6 +246,7 @@ FSDP_API fsdp_status fsdp_embed_grad(const fsdp_embed_grad_args *args, void *wor
     const fsdp_embed_grad_args &a = *args;
     const embed::Plan p = embed::make_plan(a);
     if (a.count > 0) {
+        if (p.blocks * p.slices > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
         if (!workspace || workspace_bytes < p.bytes) return FSDP_ERR_INVALID_ARG;
         if (!aligned(workspace, 256)) return FSDP_ERR_ALIGNMENT;
         const int size = dtype_size(a.dtype);

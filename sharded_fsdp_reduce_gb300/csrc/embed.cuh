@@ -9,12 +9,16 @@ namespace embed {
 
 // A warp's slice of a row: 32 lanes times this many words of 16 bytes, or of
 // one element where rows are not 16-byte aligned.
-template <int DT, bool VEC> struct Slice {
+template <int DT, bool VEC, int WORDS> struct Slice {
     static constexpr int kSize = Dtype<DT>::kSize;
     static constexpr int kElems = VEC ? 16 / kSize : 1;  // of a word
-    static constexpr int kWords = VEC ? 4 : 16;          // of a lane
+    static constexpr int kWords = VEC ? WORDS : 4 * WORDS;  // of a lane
     static constexpr int kCols = 32 * kWords * kElems;
 };
+constexpr int kLookupWords = 4, kSumWords = 2;
+
+// Columns of a warp's slice.
+inline int64_t slice_cols(int words, int dtype, bool vec) { return vec ? 512 * words / dtype_size(dtype) : 128 * words; }
 
 // kElems consecutive values as fp32, and back (rounded once).
 template <int DT, bool VEC> struct Word;
@@ -77,7 +81,9 @@ struct SortArgs {
     int64_t ignore;
     uint32_t n, vocab;
     int32_t passes, bits;
-    uint32_t *key[2], *pos[2];  // pass p writes the p % 2-th
+    uint32_t *key[2], *pos[2];  // a pass writes the p % 2-th (few entries: the last pass alone)
+    uint32_t *tickets;          // cleared for the sums
+    uint32_t n_tickets;
 };
 
 struct FillArgs {
@@ -89,6 +95,10 @@ struct FillArgs {
     int64_t ignore;
 };
 
+// Sorted entries whose sums are formed without parts in memory: those of a CTA's
+// warps, 4, 8 or 16 each.
+constexpr int kSumWarps = 8, kLeastBlock = 4 * kSumWarps, kMostBlock = 16 * kSumWarps;
+
 struct SumArgs {
     const uint32_t *key, *pos;  // tokens in order, and where they stood; key >= vocab: not a token
     uint32_t n, vocab;
@@ -96,10 +106,11 @@ struct SumArgs {
     const uint8_t *d_out;
     uint8_t *d_weight;
     int64_t out_bytes, weight_bytes;
-    float *part;        // [chunks][2][ld_part]: sums of runs that cross a chunk's first or last entry
+    float *part;        // [blocks][2][ld_part]: sums of runs that cross a block's first or last entry
     int64_t ld_part;
-    int32_t chunk;      // entries of a warp: 8, 16 or 32
-    uint32_t chunks, slices;
+    uint32_t *tickets;  // [blocks][slices]: parts that are there of the run that crosses the block's end
+    uint32_t blocks, slices;
+    int32_t block;      // entries of one
     int32_t accumulate;
     float scale;
 };
@@ -107,9 +118,6 @@ struct SumArgs {
 fsdp_status launch_sort(const SortArgs &a, cudaStream_t s);
 fsdp_status launch_fill(const FillArgs &a, cudaStream_t s);
 fsdp_status launch_sums(const SumArgs &a, int dtype, bool vec, cudaStream_t s);
-
-// Columns of a warp's slice.
-inline int64_t slice_cols(int dtype, bool vec) { return vec ? 2048 / dtype_size(dtype) : 512; }
 
 }  // namespace embed
 }  // namespace fsdp
