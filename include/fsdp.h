@@ -564,6 +564,65 @@ fsdp_status fsdp_head_loss_workspace(const fsdp_head_loss_args *args, int64_t *b
  * nothing is kept in it between calls. */
 fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* The loss of a linear head against a teacher's top logits (distillation) and
+ * its gradients (device), at temperature tau:
+ *   p[t] = softmax of teacher_logits[t] / tau over the row's entries
+ *   q[t] = softmax of hidden[t] . weight / tau over the vocabulary
+ *   token_loss[t] = tau^2 * sum over the entries k of p[t,k] (log p[t,k] - log q[t,teacher_ids[t,k]])
+ *   *loss = sum of token_loss / (FSDP_LOSS_MEAN: the rows that count, 1 if none; FSDP_LOSS_SUM: 1)
+ *   d_hidden, d_weight = the gradients of grad_scale * *loss.
+ * tau^2 keeps the gradients' size whatever the temperature. An entry does not
+ * count if its id is -1 or its logit minus infinity (a teacher that kept fewer
+ * than `top`); a row without any has a token loss of 0 and no gradients, and
+ * what its hidden values are does not matter. A token that a row names more
+ * than once has all of its entries' probability. A row with an id outside the
+ * vocabulary (-1 aside), or a counting entry whose logit is NaN or plus
+ * infinity, has a NaN loss and NaN gradients.
+ *   hidden, weight, dtype, band, reduction, grad_scale, loss, token_loss, d_*,
+ *   wait_timeouts, the precision of it all, the few rows that are plain dot
+ *   products, and the workspace's rules: as fsdp_head_loss.
+ *   teacher_logits  device, tokens rows of top values of teacher_dtype at
+ *                stride ld_teacher_logits, in any order.
+ *   teacher_ids  device, tokens rows of top int32 or int64 (id_bits 32 or 64)
+ *                at stride ld_teacher_ids.
+ *   top          entries of a row, at most FSDP_MAX_TEACHER_TOP.
+ *   temperature  tau, in [1e-3, 1e3].
+ * No output may overlap an input or another output. tokens may be 0. */
+#define FSDP_MAX_TEACHER_TOP 1024
+
+typedef struct {
+    const void *hidden;
+    int64_t ld_hidden;
+    const void *weight;
+    int64_t ld_weight;
+    const void *teacher_logits;
+    int64_t ld_teacher_logits;
+    const void *teacher_ids;
+    int64_t ld_teacher_ids;
+    int64_t tokens;
+    int64_t vocab;
+    int64_t dim;
+    int64_t top;
+    int64_t band;
+    int32_t dtype;          /* fsdp_dtype of hidden, weight and both gradients */
+    int32_t teacher_dtype;  /* fsdp_dtype of teacher_logits */
+    int32_t id_bits;        /* 32 or 64 (FSDP_ERR_UNSUPPORTED_DTYPE otherwise) */
+    int32_t reduction;      /* fsdp_loss_reduction */
+    float temperature;
+    float grad_scale;       /* the loss scale the gradients carry; 1 if none */
+    int32_t reserved;       /* must be 0 */
+    float *loss;
+    float *token_loss;
+    void *d_hidden;
+    int64_t ld_d_hidden;
+    void *d_weight;
+    int64_t ld_d_weight;
+    uint32_t *wait_timeouts;
+} fsdp_head_distill_args;
+
+fsdp_status fsdp_head_distill_workspace(const fsdp_head_distill_args *args, int64_t *bytes_out);
+fsdp_status fsdp_head_distill(const fsdp_head_distill_args *args, void *workspace, int64_t workspace_bytes, void *stream);
+
 /* The token embedding (device): rows of a table, times a factor,
  *   out[t] = scale * weight[tokens[t]],
  * formed in fp32 and rounded once to dtype. A token equal to ignore_index has a

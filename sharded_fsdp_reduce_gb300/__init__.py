@@ -3,6 +3,7 @@ AdamW + cast, all-gather and unflatten, as hand-written sm_103a CUDA behind a
 C ABI (include/fsdp.h). This package is the thin Python binding over it.
 """
 from .clip import ClipPlan, GradClip
+from .distill import HeadDistill, fsdp_head_distill
 from .embedding import Embedding, fsdp_embed, fsdp_embed_grad
 from .fsdp import (OPTIMIZERS, AdamWHParams, FsdpError, StepConfig, StepGraph, StepPlan, UnitDescs, View, dtype_code,
                    fsdp_all_gather, fsdp_check_bounded_wait, fsdp_flatten_pad, fsdp_last_cuda_error,
@@ -21,4 +22,5 @@ __all__ = [
     "UnitDescs", "fsdp_step_units", "fsdp_step_units_ex", "StepGraph", "StepPlan", "fsdp_step_units_launches",
     "fsdp_step_units_ex_launches", "HeadLoss", "fsdp_head_loss", "fsdp_check_head_loss_wait", "GradClip", "ClipPlan",
     "Embedding", "fsdp_embed", "fsdp_embed_grad",
+    "HeadDistill", "fsdp_head_distill",
 ]

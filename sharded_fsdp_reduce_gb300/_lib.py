@@ -14,6 +14,7 @@ LIB_PATH = os.path.join(PKG, "libfsdpreduce.so")
 
 FSDP_MAX_WORLD = 64
 FSDP_MAX_NDIM = 8
+FSDP_MAX_TEACHER_TOP = 1024
 
 FSDP_OK = 0
 FSDP_ERR_INVALID_ARG = 1
@@ -56,6 +57,8 @@ EXPORTS = (
     "fsdp_head_loss_workspace",
     "fsdp_head_loss",
     "fsdp_check_head_loss_wait",
+    "fsdp_head_distill_workspace",
+    "fsdp_head_distill",
     "fsdp_embed",
     "fsdp_embed_grad_workspace",
     "fsdp_embed_grad",
@@ -113,6 +116,19 @@ class FsdpHeadLossArgs(ctypes.Structure):
                 ("grad_scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("loss", ctypes.c_void_p),
                 ("token_loss", ctypes.c_void_p), ("d_hidden", ctypes.c_void_p), ("ld_d_hidden", ctypes.c_int64),
                 ("d_weight", ctypes.c_void_p), ("ld_d_weight", ctypes.c_int64), ("wait_timeouts", ctypes.c_void_p)]
+
+
+class FsdpHeadDistillArgs(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_void_p), ("ld_hidden", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("ld_weight", ctypes.c_int64), ("teacher_logits", ctypes.c_void_p),
+                ("ld_teacher_logits", ctypes.c_int64), ("teacher_ids", ctypes.c_void_p),
+                ("ld_teacher_ids", ctypes.c_int64), ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("top", ctypes.c_int64), ("band", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("teacher_dtype", ctypes.c_int32), ("id_bits", ctypes.c_int32), ("reduction", ctypes.c_int32),
+                ("temperature", ctypes.c_float), ("grad_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("loss", ctypes.c_void_p), ("token_loss", ctypes.c_void_p), ("d_hidden", ctypes.c_void_p),
+                ("ld_d_hidden", ctypes.c_int64), ("d_weight", ctypes.c_void_p), ("ld_d_weight", ctypes.c_int64),
+                ("wait_timeouts", ctypes.c_void_p)]
 
 
 class FsdpEmbedArgs(ctypes.Structure):
@@ -183,6 +199,8 @@ def load() -> ctypes.CDLL:
             "fsdp_head_loss_workspace": (i32, [ctypes.POINTER(FsdpHeadLossArgs), ctypes.POINTER(i64)]),
             "fsdp_check_head_loss_wait": (i32, [i64, i64, vp, vp, vp]),
             "fsdp_head_loss": (i32, [ctypes.POINTER(FsdpHeadLossArgs), vp, i64, vp]),
+            "fsdp_head_distill_workspace": (i32, [ctypes.POINTER(FsdpHeadDistillArgs), ctypes.POINTER(i64)]),
+            "fsdp_head_distill": (i32, [ctypes.POINTER(FsdpHeadDistillArgs), vp, i64, vp]),
             "fsdp_embed": (i32, [ctypes.POINTER(FsdpEmbedArgs), vp]),
             "fsdp_embed_grad_workspace": (i32, [ctypes.POINTER(FsdpEmbedGradArgs), ctypes.POINTER(i64)]),
             "fsdp_embed_grad": (i32, [ctypes.POINTER(FsdpEmbedGradArgs), vp, i64, vp]),

@@ -22,6 +22,11 @@
 // 50257 x 1280), where rounding nothing but the result leaves 1.7e-3 and 2.1e-4.
 // Losses, sums, statistics and the target's p - 1 are fp32; fp32 heads keep
 // fp32 exponentials and d in three parts.
+//
+// Against a teacher's top logits (fsdp_head_distill, distill.cu) the same
+// kernels run with the exponentials of the logits over a temperature; the
+// logits of the teacher's entries leave the product in fp32, and take the place
+// of the target's in the row kernel and in d.
 #include <math.h>
 #include <string.h>
 
@@ -55,6 +60,13 @@ struct RowArgs {
     float *loss, *scale;
     float grad_scale;
     int32_t mean;
+    // against a teacher's distribution
+    const int32_t *ids;       // [rows][top]
+    const float2 *prob;
+    const float *at;          // [rows][top]: the entries' logits; NULL: among all logits
+    const float *logits;      // [rows][ld_logits]
+    int64_t top, ld_logits;
+    float temperature, inverse, log2e;
 };
 
 __device__ double warp_sum(double x) {
@@ -68,15 +80,38 @@ __device__ long long warp_sum(long long x) {
     return x;
 }
 
-// e^x; e^0 is exactly 1.
-__device__ __forceinline__ float exp_of(float x) { return exp2f(x * kLog2e); }
+__device__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// e^x, or of x over a temperature; e^0 is exactly 1.
+__device__ __forceinline__ float exp_of(float x, float log2e = kLog2e) { return exp2f(x * log2e); }
 
 // (top, sum): sum * e^top. Joins another pair into it.
-__device__ __forceinline__ void join(float &top, float &sum, float other_top, float other_sum) {
+__device__ __forceinline__ void join(float &top, float &sum, float other_top, float other_sum, float log2e) {
     const float most = fmaxf(top, other_top);
     if (most == -INFINITY) return;  // both empty
-    sum = sum * exp_of(top - most) + other_sum * exp_of(other_top - most);
+    sum = sum * exp_of(top - most, log2e) + other_sum * exp_of(other_top - most, log2e);
     top = most;
+}
+
+// What a row of SOFT loses: temperature^2 times the sum of p (log p - log q)
+// over the teacher's entries, by a warp. Differences first: each is as small
+// as the two distributions are close.
+__device__ __forceinline__ float soft_loss(const RowArgs &a, int64_t row, float top, float sum) {
+    const int lane = threadIdx.x % 32;
+    const float log_sum = logf(sum);
+    float t = 0.0f;
+    for (int64_t k = lane; k < a.top; k += 32) {
+        const int32_t id = a.ids[row * a.top + k];
+        if (id == kNoEntry) break;
+        const float2 p = a.prob[row * a.top + k];
+        const float logit = a.at != nullptr ? a.at[row * a.top + k] : a.logits[row * a.ld_logits + id];
+        t += p.x * (p.y - ((logit - top) * a.inverse - log_sum));
+    }
+    return a.temperature * a.temperature * warp_sum(t);
 }
 
 __device__ __forceinline__ void write_loss(const RowArgs &a, double sum, long long valid) {
@@ -93,7 +128,8 @@ constexpr int kRowLoads = 8;  // spans a thread reads at once
 // spans. Latency-bound: 2 x 4 bytes per span and row, eight loads in flight
 // per thread. The loss adds up per block, then over the blocks in one fixed
 // order, in fp64.
-__global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowArgs a) {
+template <bool SOFT> __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowArgs a) {
+    const float log2e = SOFT ? a.log2e : kLog2e;
     __shared__ float tops[32][kRows + 1], sums[32][kRows + 1];
     __shared__ double total[32];
     __shared__ long long count[32];
@@ -117,13 +153,13 @@ __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowA
                 float most = top;
 #pragma unroll
                 for (int i = 0; i < kRowLoads; ++i) most = fmaxf(most, o[i]);
-                sum *= exp_of(top - most);
+                sum *= exp_of(top - most, log2e);
 #pragma unroll
-                for (int i = 0; i < kRowLoads; ++i) sum += x[i] * exp_of(o[i] - most);
+                for (int i = 0; i < kRowLoads; ++i) sum += x[i] * exp_of(o[i] - most, log2e);
                 top = most;
             }
         }
-        join(top, sum, __shfl_xor_sync(0xffffffffu, top, kRows), __shfl_xor_sync(0xffffffffu, sum, kRows));
+        join(top, sum, __shfl_xor_sync(0xffffffffu, top, kRows), __shfl_xor_sync(0xffffffffu, sum, kRows), log2e);
         if (lane < kRows) {
             tops[warp][lane] = top;
             sums[warp][lane] = sum;
@@ -135,14 +171,21 @@ __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowA
         float top = tops[lane][warp], sum = sums[lane][warp];
 #pragma unroll
         for (int o = 16; o; o >>= 1)
-            join(top, sum, __shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o));
+            join(top, sum, __shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o), log2e);
+        float soft = 0.0f;
+        if constexpr (SOFT) {
+            if (row < a.rows && a.targets[row] == 0) soft = soft_loss(a, row, top, sum);
+        }
         if (lane == 0) {
             float t = 0.0f;
             long long valid = 0;
             if (row < a.rows) {
                 a.row_state[row] = make_float2(top, sum);
                 const int64_t y = a.targets[row];
-                if (y != a.ignore) {
+                if (SOFT && y != a.ignore) {
+                    valid = 1;
+                    t = y == 0 ? soft : NAN;
+                } else if (y != a.ignore) {
                     valid = 1;
                     // log sum + (top - target): the sum is at least 1, the
                     // target at most top, and both terms are small for a row
@@ -229,6 +272,13 @@ struct GradArgs {
     const int64_t *targets;
     int64_t ignore;
     uint32_t row_blocks;
+    // against a teacher's distribution
+    const uint16_t *first;   // [rows][ld_first]
+    const int32_t *ids;      // [rows][top]
+    const float2 *prob;
+    const float *at;
+    int64_t ld_first, top, spans;
+    float log2e;
 };
 
 // x in three bf16 parts: each takes the next 8 bits. An infinite x is in the
@@ -252,7 +302,10 @@ constexpr int kGradCols = 512, kGradRows = 64;
 
 // 64 rows x 512 columns per block, 8 columns per thread and row. Bound by HBM
 // (or L2, where the band fits): 4 bytes moved per element in 16-bit types.
-template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __grid_constant__ GradArgs a) {
+//
+// SOFT: the block then writes the teacher's entries among its columns, from
+// their fp32 logits, as the target's is.
+template <int DT, bool SOFT> __global__ void __launch_bounds__(256) grad_kernel(const __grid_constant__ GradArgs a) {
     __shared__ float factor[kGradCols / kSpan][kGradRows];
     __shared__ int32_t hit[kGradRows];  // the target's column in this block, or -1; -2: no gradient
     __shared__ float at_target[kGradRows];
@@ -262,6 +315,7 @@ template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __gri
     const int64_t col0 = int64_t(block / a.row_blocks) * kGradCols;
     constexpr float kGain = DT == FSDP_F16 ? kHalfGain : 1.0f;
     constexpr float kFactor = DT == FSDP_F32 ? kGain : kGain / kExpGain;
+    const float log2e = SOFT ? a.log2e : kLog2e;
     wait_previous();
     allow_next();
     for (int i = threadIdx.x; i < kGradRows * (kGradCols / kSpan); i += 256) {
@@ -275,12 +329,12 @@ template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __gri
             const bool bad = y != a.ignore && (y < 0 || y >= a.vocab);
             const float2 state = a.row_state[row];
             if (span * kSpan < a.vocab)
-                factor[s][r] = bad ? NAN : kFactor * exp_of(a.off[span * a.ld_rows + row] - state.x) / state.y;
+                factor[s][r] = bad ? NAN : kFactor * exp_of(a.off[span * a.ld_rows + row] - state.x, log2e) / state.y;
             if (s == 0) {
-                hit[r] = y == a.ignore ? -2 : at >= 0 && at < kGradCols ? static_cast<int32_t>(at) : -1;
+                hit[r] = y == a.ignore ? -2 : !SOFT && at >= 0 && at < kGradCols ? static_cast<int32_t>(at) : -1;
                 // the target's own d from its fp32 logit: near 1 the stored
                 // exponential's rounding would be all that is left of p - 1
-                if (hit[r] >= 0 && at + col0 < a.vocab)
+                if (!SOFT && hit[r] >= 0 && at + col0 < a.vocab)
                     at_target[r] = kGain * (exp_of(a.target_logit[row] - state.x) / state.y - 1.0f);
             }
         }
@@ -288,8 +342,8 @@ template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __gri
     __syncthreads();
     const int c = threadIdx.x % (kGradCols / 8) * 8;
     const int64_t col = col0 + c;
-    if (col >= a.vocab) return;
-    const int rows = static_cast<int>(min(int64_t(kGradRows), a.rows - row0));
+    if (!SOFT && col >= a.vocab) return;
+    const int rows = SOFT && col >= a.vocab ? 0 : static_cast<int>(min(int64_t(kGradRows), a.rows - row0));
 #pragma unroll 4
     for (int r = threadIdx.x / (kGradCols / 8); r < rows; r += 256 / (kGradCols / 8)) {
         const int64_t at = (row0 + r) * a.ld + col;
@@ -323,6 +377,34 @@ template <int DT> __global__ void __launch_bounds__(256) grad_kernel(const __gri
         } else {
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.e) + at) =
                 make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
+        }
+    }
+    if constexpr (SOFT) {
+        __syncthreads();
+        constexpr int kShare = 256 / kGradRows;  // threads of a row
+        const int64_t row = row0 + threadIdx.x / kShare;
+        if (row >= a.rows) return;
+        const uint16_t *first = a.first + row * a.ld_first + col0 / kSpan;
+        const int end = first[min(int64_t(kGradCols / kSpan), a.spans - col0 / kSpan)];
+        const int32_t *ids = a.ids + row * a.top;
+        const float2 state = a.row_state[row];
+        for (int k = first[0] + threadIdx.x % kShare; k < end; k += kShare) {
+            // (a token that the teacher names twice has both probabilities)
+            const int32_t id = ids[k];
+            if (k > 0 && ids[k - 1] == id) continue;
+            float p = a.prob[row * a.top + k].x;
+            for (int more = k + 1; more < a.top && ids[more] == id; ++more) p += a.prob[row * a.top + more].x;
+            const float x = kGain * (exp_of(a.at[row * a.top + k] - state.x, log2e) / state.y - p);
+            const int64_t at = row * a.ld + id;
+            if constexpr (DT == FSDP_F32) {
+                float hi, mid, lo;
+                split3(x, hi, mid, lo);
+                Dtype<FSDP_BF16>::store(a.planes[0], at, hi);
+                Dtype<FSDP_BF16>::store(a.planes[1], at, mid);
+                Dtype<FSDP_BF16>::store(a.planes[2], at, lo);
+            } else {
+                Dtype<DT>::store(a.e, at, x);
+            }
         }
     }
 }
@@ -415,6 +497,8 @@ struct Plan {
     int splits_x, splits_w;
     // byte offsets into the workspace
     int64_t scale, ticket, part_sum, part_count, row_state, target_logit, off, sum, x, w, e, d, part, sum_w, bytes;
+    // against a teacher's distribution of `top` entries
+    int64_t top, ld_first, targets, ids, prob, at, first;
 };
 
 constexpr int kMostSplits = 32;
@@ -463,10 +547,12 @@ int weight_splits(const fsdp_head_loss_args &a, int64_t rows) {
                          a.dtype == FSDP_F32 ? 6 : 1, a.vocab, round_up(a.dim, 64));
 }
 
-// How a call runs.
-Plan choose(const fsdp_head_loss_args &a) {
+// How a call runs (top: a teacher's entries of a row, or 0).
+Plan choose(const fsdp_head_loss_args &a, int64_t top) {
     Plan p;
     memset(&p, 0, sizeof(p));
+    p.top = top;
+    p.ld_first = round_up(ceil_div(a.vocab, kSpan) + 1, 8);
     p.f32 = a.dtype == FSDP_F32;
     p.grad = a.d_hidden != nullptr || a.d_weight != nullptr;
     // (the few rows' gradient kernels take up to 2^16 column tiles)
@@ -505,6 +591,7 @@ Plan choose(const fsdp_head_loss_args &a) {
 // What the workspace's parts hold.
 struct Room {
     int64_t blocks, band, stats, x, w, e, d, part, sum_w;  // counts of the first three, then bytes
+    int64_t targets;
 };
 
 int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
@@ -518,6 +605,8 @@ Room room_of(const fsdp_head_loss_args &a, const Plan &p) {
     r.stats = p.spans * p.band;
     if (p.pack_x) r.x = 2 * planes * a.tokens * p.ldd;
     if (p.pack_w) r.w = 2 * planes * a.vocab * p.ldd;
+    if (p.top) r.targets = 8 * a.tokens;
+    if (p.few && p.top) r.e = p.band * p.ldv * 4;  // the logits
     if (p.grad) {
         r.e = p.band * p.ldv * (p.f32 ? 4 : 2);
         if (p.f32 && !p.few) r.d = p.band * p.ldv * 6;
@@ -532,14 +621,14 @@ Room room_of(const fsdp_head_loss_args &a, const Plan &p) {
 // shorter call can need more of some than a longer one: it may cut a product
 // into more pieces, work in one band where the longer one takes two halves,
 // or run as a few rows.
-Room room_up_to(const fsdp_head_loss_args &a) {
-    const Plan p = choose(a);
+Room room_up_to(const fsdp_head_loss_args &a, int64_t top) {
+    const Plan p = choose(a, top);
     Room r = room_of(a, p);
     if (p.few) return r;  // (grows with the rows)
     fsdp_head_loss_args few = a;
     few.tokens = few_rows(a.dtype, p.grad);
     if (few.tokens > 0 && a.dim <= (1 << 22)) {
-        const Plan q = choose(few);
+        const Plan q = choose(few, top);
         const Room f = room_of(few, q);
         r.band = larger(r.band, f.band);
         r.stats = larger(r.stats, f.stats);
@@ -596,19 +685,26 @@ void place(Plan &p, const Room &r) {
     p.d = r.d > 0 ? take(r.d) : p.e;
     p.part = take(r.part);
     p.sum_w = take(r.sum_w);
+    if (p.top) {
+        p.targets = take(r.targets);
+        p.ids = take(4 * r.band * p.top);
+        p.prob = take(8 * r.band * p.top);
+        p.at = take(4 * r.band * p.top);
+        p.first = take(2 * r.band * p.ld_first);
+    }
     p.bytes = at;
 }
 
-Plan make_plan(const fsdp_head_loss_args &a) {
-    Plan p = choose(a);
+Plan make_plan(const fsdp_head_loss_args &a, int64_t top = 0) {
+    Plan p = choose(a, top);
     place(p, room_of(a, p));
     return p;
 }
 
 // The bytes that are enough for this call and for every shorter one.
-int64_t bytes_up_to(const fsdp_head_loss_args &a) {
-    Plan p = choose(a);
-    place(p, room_up_to(a));
+int64_t bytes_up_to(const fsdp_head_loss_args &a, int64_t top = 0) {
+    Plan p = choose(a, top);
+    place(p, room_up_to(a, top));
     return p.bytes;
 }
 
@@ -747,7 +843,7 @@ fsdp_status run_product(const Product &q, const Plan &p, const fsdp_head_loss_ar
     return launch_grad(q.out_dtype, q.orders, ma, mb, g, s);
 }
 
-fsdp_status run_few(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaStream_t s) {
+fsdp_status run_few(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, const SoftArgs *soft, cudaStream_t s) {
     FewArgs f;
     f.hidden = a.hidden;
     f.weight = a.weight;
@@ -763,14 +859,22 @@ fsdp_status run_few(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cu
     f.ld_rows = p.band;
     f.target_logit = reinterpret_cast<float *>(ws + p.target_logit);
     f.ticket = reinterpret_cast<uint32_t *>(ws + p.ticket);
-    f.logits = p.grad ? reinterpret_cast<float *>(ws + p.e) : nullptr;
+    f.logits = p.grad || soft ? reinterpret_cast<float *>(ws + p.e) : nullptr;
     f.ld_logits = p.ldv;
+    f.log2e = soft ? soft->log2e : kLog2e;
     return launch_few(f, a.dtype, s);
 }
 
 // The gradients of a few fp32 rows, from their logits and lse.
-fsdp_status run_few_grad(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaStream_t s) {
+fsdp_status run_few_grad(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, const SoftArgs *soft, cudaStream_t s) {
+    if (soft) {
+        const FewSoftArgs d{reinterpret_cast<float *>(ws + p.e), reinterpret_cast<const float2 *>(ws + p.row_state), p.ldv,
+                            a.tokens, a.vocab, p.top, a.targets, soft->ids, soft->prob, soft->log2e};
+        const fsdp_status st = launch_few_soft(d, s);
+        if (st != FSDP_OK) return st;
+    }
     FewGradArgs f;
+    f.soft = soft != nullptr;
     f.hidden = static_cast<const float *>(a.hidden);
     f.weight = static_cast<const float *>(a.weight);
     f.logits = reinterpret_cast<const float *>(ws + p.e);
@@ -802,8 +906,9 @@ fsdp_status run_few_grad(const fsdp_head_loss_args &a, const Plan &p, uint8_t *w
 
 // The rows' sums and losses, of one band.
 fsdp_status run_rows(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, int64_t row0, int64_t rows,
-                     int64_t &block, cudaStream_t s) {
+                     int64_t &block, const SoftArgs *soft, cudaStream_t s) {
     RowArgs r;
+    memset(&r, 0, sizeof(r));
     r.off = reinterpret_cast<const float *>(ws + p.off);
     r.sum = reinterpret_cast<const float *>(ws + p.sum);
     r.ld_rows = p.band;
@@ -826,15 +931,31 @@ fsdp_status run_rows(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, i
     r.mean = a.reduction == FSDP_LOSS_MEAN;
     const unsigned blocks = static_cast<unsigned>(ceil_div(rows, kRows));
     block += blocks;
-    return launch_chained(rows_kernel, blocks, 1024, 0, s, r);
+    if (soft) {
+        r.ids = soft->ids;
+        r.prob = soft->prob;
+        r.at = p.few ? nullptr : reinterpret_cast<const float *>(ws + p.at);
+        r.logits = reinterpret_cast<const float *>(ws + p.e);
+        r.ld_logits = p.ldv;
+        r.top = p.top;
+        r.temperature = soft->temperature;
+        r.inverse = soft->inverse;
+        r.log2e = soft->log2e;
+        return launch_chained(rows_kernel<true>, blocks, 1024, 0, s, r);
+    }
+    return launch_chained(rows_kernel<false>, blocks, 1024, 0, s, r);
 }
 
-fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaStream_t s) {
+// soft: against a teacher's distribution (a.targets are then the workspace's,
+// and a.grad_scale has the temperature).
+fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, SoftArgs *soft, cudaStream_t s) {
     int64_t block = 0;
     if (p.few) {
-        fsdp_status few = run_few(a, p, ws, s);
-        if (few == FSDP_OK) few = run_rows(a, p, ws, 0, a.tokens, block, s);
-        return few == FSDP_OK && p.grad ? run_few_grad(a, p, ws, s) : few;
+        fsdp_status few = FSDP_OK;
+        if (soft) few = launch_prepare(*soft, 0, a.tokens, s);
+        if (few == FSDP_OK) few = run_few(a, p, ws, soft, s);
+        if (few == FSDP_OK) few = run_rows(a, p, ws, 0, a.tokens, block, soft, s);
+        return few == FSDP_OK && p.grad ? run_few_grad(a, p, ws, soft, s) : few;
     }
     const int64_t D = a.dim, V = a.vocab;
     const int size = dtype_size(a.dtype);
@@ -842,6 +963,12 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
     Operand x{static_cast<const uint8_t *>(a.hidden), a.ld_hidden, a.tokens * a.ld_hidden, 1};
     Operand w{static_cast<const uint8_t *>(a.weight), a.ld_weight, V * a.ld_weight, 1};
     fsdp_status st = FSDP_OK;
+    if (soft) {
+        // which rows count, before the first band
+        SoftArgs all = *soft;
+        if (p.bands > 1) all.ids = nullptr;
+        if ((st = launch_prepare(all, 0, a.tokens, s)) != FSDP_OK) return st;
+    }
     if (p.pack_x) {
         st = pack(a.hidden, p.f32, a.tokens, D, a.ld_hidden, ws + p.x, p.ldd, a.targets, a.ignore_index, s);
         x = Operand{ws + p.x, p.ldd, a.tokens * p.ldd, planes};
@@ -890,15 +1017,24 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         g.ld_rows = p.band;
         g.ticket = b == 0 ? reinterpret_cast<uint32_t *>(ws + p.ticket) : nullptr;
         g.timeouts = a.wait_timeouts;
+        if (soft) {
+            if (p.bands > 1 && (st = launch_prepare(*soft, row0, rows, s)) != FSDP_OK) return st;
+            g.first = soft->first;
+            g.ld_first = soft->ld_first;
+            g.ids = soft->ids;
+            g.at = reinterpret_cast<float *>(ws + p.at);
+            g.top = soft->top;
+            g.log2e = soft->log2e;
+        }
         e_out = x_k;
         if (p.grad) {
             st = make_map(&e_out, p.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + p.e,
                           p.ldv, rows, 1, p.ldv, rows * p.ldv, 32, 64);
             if (st != FSDP_OK) return st;
         }
-        st = launch_logits(p.grad ? kExp : kStats, p.f32, x_k, w_k, e_out, g, s);
+        st = (soft ? launch_soft_logits : launch_logits)(p.grad ? kExp : kStats, p.f32, x_k, w_k, e_out, g, s);
         if (st != FSDP_OK) return st;
-        if ((st = run_rows(a, p, ws, row0, rows, block, s)) != FSDP_OK) return st;
+        if ((st = run_rows(a, p, ws, row0, rows, block, soft, s)) != FSDP_OK) return st;
         if (!p.grad) continue;
         // d, then the two products
         GradArgs d;
@@ -920,9 +1056,22 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, cudaSt
         const int64_t all = ceil_div(V, kGradCols) * d.row_blocks;
         if (all > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
         const unsigned dgrid = static_cast<unsigned>(all);
-        auto grad = a.dtype == FSDP_BF16  ? grad_kernel<FSDP_BF16>
-                    : a.dtype == FSDP_F16 ? grad_kernel<FSDP_F16>
-                                          : grad_kernel<FSDP_F32>;
+        auto grad = a.dtype == FSDP_BF16  ? grad_kernel<FSDP_BF16, false>
+                    : a.dtype == FSDP_F16 ? grad_kernel<FSDP_F16, false>
+                                          : grad_kernel<FSDP_F32, false>;
+        if (soft) {
+            d.first = soft->first;
+            d.ld_first = soft->ld_first;
+            d.ids = soft->ids;
+            d.prob = soft->prob;
+            d.at = g.at;
+            d.top = soft->top;
+            d.spans = soft->spans;
+            d.log2e = soft->log2e;
+            grad = a.dtype == FSDP_BF16  ? grad_kernel<FSDP_BF16, true>
+                   : a.dtype == FSDP_F16 ? grad_kernel<FSDP_F16, true>
+                                         : grad_kernel<FSDP_F32, true>;
+        }
         if ((st = launch_chained(grad, dgrid, 256, 0, s, d)) != FSDP_OK) return st;
         if (a.d_hidden) {
             CUtensorMap d_k;
@@ -955,8 +1104,52 @@ size_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int size) {
     return rows > 0 ? static_cast<size_t>(((rows - 1) * ld + cols) * size) : 0;
 }
 
+// The cross entropy's: the targets are its one input beside the matrices.
 fsdp_status check(const fsdp_head_loss_args *a) {
     if (!a) return FSDP_ERR_INVALID_ARG;
+    const void *targets = a->targets;
+    const size_t bytes = static_cast<size_t>(a->tokens) * 8;
+    const fsdp_status st = check_head(*a, &targets, &bytes, 1);
+    if (st != FSDP_OK) return st;
+    return aligned(a->targets, 8) ? FSDP_OK : FSDP_ERR_ALIGNMENT;
+}
+
+// No rows: a loss of 0 and a zero weight gradient.
+fsdp_status no_rows(const fsdp_head_loss_args &a, cudaStream_t s) {
+    cudaError_t e = cudaMemsetAsync(a.loss, 0, 4, s);
+    if (e == cudaSuccess && a.d_weight) {
+        const size_t size = static_cast<size_t>(dtype_size(a.dtype));
+        e = cudaMemset2DAsync(a.d_weight, a.ld_d_weight * size, 0, a.dim * size, a.vocab, s);
+    }
+    return cuda_status(e);
+}
+
+// The workspace of a call against the buffers of it.
+fsdp_status check_workspace(const fsdp_head_loss_args &a, const Plan &p, const void *workspace, int64_t workspace_bytes) {
+    if (!workspace || workspace_bytes < p.bytes) return FSDP_ERR_INVALID_ARG;
+    if (!aligned(workspace, 1024)) return FSDP_ERR_ALIGNMENT;
+    const int size = dtype_size(a.dtype);
+    const void *used[7] = {a.hidden, a.weight, a.targets, a.loss, a.token_loss, a.d_hidden, a.d_weight};
+    const size_t bytes[7] = {span_bytes(a.tokens, a.dim, a.ld_hidden, size),
+                             span_bytes(a.vocab, a.dim, a.ld_weight, size),
+                             a.targets ? static_cast<size_t>(a.tokens) * 8 : 0,
+                             4,
+                             a.token_loss ? static_cast<size_t>(a.tokens) * 4 : 0,
+                             a.d_hidden ? span_bytes(a.tokens, a.dim, a.ld_d_hidden, size) : 0,
+                             a.d_weight ? span_bytes(a.vocab, a.dim, a.ld_d_weight, size) : 0};
+    for (int i = 0; i < 7; ++i)
+        if (overlaps(used[i], bytes[i], workspace, static_cast<size_t>(p.bytes))) return FSDP_ERR_INVALID_ARG;
+    // the operands' tiles are bulk copies between device buffers
+    if (host_resident(a.hidden) || host_resident(a.weight)) return FSDP_ERR_INVALID_ARG;
+    return FSDP_OK;
+}
+
+}  // namespace
+
+// Sizes, matrices and outputs, and the inputs beside hidden and weight (at
+// least their addresses: `inputs`).
+fsdp_status check_head(const fsdp_head_loss_args &args, const void *const *inputs, const size_t *input_bytes, int n_inputs) {
+    const fsdp_head_loss_args *a = &args;
     if (!dtype_valid(a->dtype)) return FSDP_ERR_UNSUPPORTED_DTYPE;
     constexpr int64_t kMost = int64_t(1) << 30;  // tile coordinates are 32-bit
     if (a->tokens < 0 || a->tokens > kMost || a->vocab < 1 || a->vocab > kMost || a->dim < 1 || a->dim > kMost)
@@ -983,27 +1176,59 @@ fsdp_status check(const fsdp_head_loss_args *a) {
         if (x.ld < a->dim || x.ld > kMostLd || x.rows > kMostArea / x.ld) return FSDP_ERR_INVALID_ARG;
         if (!aligned(x.p, size)) return FSDP_ERR_ALIGNMENT;
     }
-    if (!a->loss || (a->tokens > 0 && !a->targets)) return FSDP_ERR_INVALID_ARG;
-    if (!aligned(a->loss, 4) || !aligned(a->token_loss, 4) || !aligned(a->targets, 8) || !aligned(a->wait_timeouts, 4))
-        return FSDP_ERR_ALIGNMENT;
+    if (!a->loss) return FSDP_ERR_INVALID_ARG;
+    for (int i = 0; i < n_inputs; ++i)
+        if (a->tokens > 0 && !inputs[i]) return FSDP_ERR_INVALID_ARG;
+    if (!aligned(a->loss, 4) || !aligned(a->token_loss, 4) || !aligned(a->wait_timeouts, 4)) return FSDP_ERR_ALIGNMENT;
     // no output overlaps an input or another output
-    const void *in[3] = {a->hidden, a->weight, a->targets};
-    const size_t nin[3] = {span_bytes(a->tokens, a->dim, a->ld_hidden, size),
-                           span_bytes(a->vocab, a->dim, a->ld_weight, size), static_cast<size_t>(a->tokens) * 8};
     const void *out[4] = {a->loss, a->token_loss, a->d_hidden, a->d_weight};
     const size_t nout[4] = {4, a->token_loss ? static_cast<size_t>(a->tokens) * 4 : 0,
                             a->d_hidden ? span_bytes(a->tokens, a->dim, a->ld_d_hidden, size) : 0,
                             a->d_weight ? span_bytes(a->vocab, a->dim, a->ld_d_weight, size) : 0};
     for (int i = 0; i < 4; ++i) {
-        for (int k = 0; k < 3; ++k)
-            if (overlaps(out[i], nout[i], in[k], nin[k])) return FSDP_ERR_INVALID_ARG;
+        if (overlaps(out[i], nout[i], a->hidden, span_bytes(a->tokens, a->dim, a->ld_hidden, size)) ||
+            overlaps(out[i], nout[i], a->weight, span_bytes(a->vocab, a->dim, a->ld_weight, size)))
+            return FSDP_ERR_INVALID_ARG;
+        for (int k = 0; k < n_inputs; ++k)
+            if (overlaps(out[i], nout[i], inputs[k], input_bytes[k])) return FSDP_ERR_INVALID_ARG;
         for (int k = i + 1; k < 4; ++k)
             if (overlaps(out[i], nout[i], out[k], nout[k])) return FSDP_ERR_INVALID_ARG;
     }
     return FSDP_OK;
 }
 
-}  // namespace
+fsdp_status soft_workspace(const fsdp_head_loss_args &args, int64_t top, int64_t *bytes_out) {
+    if (!bytes_out) return FSDP_ERR_INVALID_ARG;
+    *bytes_out = args.tokens == 0 ? 0 : bytes_up_to(args, top);
+    return FSDP_OK;
+}
+
+fsdp_status soft_run(fsdp_head_loss_args a, SoftArgs soft, void *workspace, int64_t workspace_bytes, cudaStream_t s) {
+    if (a.tokens == 0) return no_rows(a, s);
+    const Plan p = make_plan(a, soft.top);
+    a.targets = nullptr;
+    const fsdp_status st = check_workspace(a, p, workspace, workspace_bytes);
+    if (st != FSDP_OK) return st;
+    const size_t entry = soft.teacher_dtype == FSDP_F32 ? 4 : 2, token = soft.wide ? 8 : 4;
+    if (overlaps(soft.teacher, ((a.tokens - 1) * soft.ld_teacher + soft.top) * entry, workspace,
+                 static_cast<size_t>(p.bytes)) ||
+        overlaps(soft.given, ((a.tokens - 1) * soft.ld_given + soft.top) * token, workspace,
+                 static_cast<size_t>(p.bytes)))
+        return FSDP_ERR_INVALID_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    soft.vocab = a.vocab;
+    soft.spans = ceil_div(a.vocab, kSpan);
+    soft.ids = reinterpret_cast<int32_t *>(ws + p.ids);
+    soft.prob = reinterpret_cast<float2 *>(ws + p.prob);
+    soft.first = p.few ? nullptr : reinterpret_cast<uint16_t *>(ws + p.first);
+    soft.ld_first = p.ld_first;
+    soft.targets = reinterpret_cast<int64_t *>(ws + p.targets);
+    a.targets = soft.targets;
+    a.ignore_index = kIgnored;
+    a.grad_scale *= soft.temperature;
+    return run(a, p, ws, &soft, s);
+}
+
 }  // namespace loss
 }  // namespace fsdp
 
@@ -1025,32 +1250,11 @@ FSDP_API fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *works
     if (st != FSDP_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const fsdp_head_loss_args &a = *args;
-    if (a.tokens == 0) {
-        // no rows: a loss of 0 and a zero weight gradient
-        cudaError_t e = cudaMemsetAsync(a.loss, 0, 4, s);
-        if (e == cudaSuccess && a.d_weight) {
-            const size_t size = static_cast<size_t>(dtype_size(a.dtype));
-            e = cudaMemset2DAsync(a.d_weight, a.ld_d_weight * size, 0, a.dim * size, a.vocab, s);
-        }
-        return cuda_status(e);
-    }
+    if (a.tokens == 0) return loss::no_rows(a, s);
     const loss::Plan p = loss::make_plan(a);
-    if (!workspace || workspace_bytes < p.bytes) return FSDP_ERR_INVALID_ARG;
-    if (!aligned(workspace, 1024)) return FSDP_ERR_ALIGNMENT;
-    const void *used[7] = {a.hidden, a.weight, a.targets, a.loss, a.token_loss, a.d_hidden, a.d_weight};
-    const size_t size = static_cast<size_t>(dtype_size(a.dtype));
-    const size_t bytes[7] = {((a.tokens - 1) * a.ld_hidden + a.dim) * size,
-                             ((a.vocab - 1) * a.ld_weight + a.dim) * size,
-                             static_cast<size_t>(a.tokens) * 8,
-                             4,
-                             a.token_loss ? static_cast<size_t>(a.tokens) * 4 : 0,
-                             a.d_hidden ? ((a.tokens - 1) * a.ld_d_hidden + a.dim) * size : 0,
-                             a.d_weight ? ((a.vocab - 1) * a.ld_d_weight + a.dim) * size : 0};
-    for (int i = 0; i < 7; ++i)
-        if (overlaps(used[i], bytes[i], workspace, static_cast<size_t>(p.bytes))) return FSDP_ERR_INVALID_ARG;
-    // the operands' tiles are bulk copies between device buffers
-    if (host_resident(a.hidden) || host_resident(a.weight)) return FSDP_ERR_INVALID_ARG;
-    return loss::run(a, p, static_cast<uint8_t *>(workspace), s);
+    const fsdp_status fits = loss::check_workspace(a, p, workspace, workspace_bytes);
+    if (fits != FSDP_OK) return fits;
+    return loss::run(a, p, static_cast<uint8_t *>(workspace), nullptr, s);
 }
 
 FSDP_API fsdp_status fsdp_check_head_loss_wait(int64_t limit_cycles, int64_t arrive_after_cycles, int32_t *outcomes,

@@ -43,6 +43,13 @@ struct GemmArgs {
     float *off, *sum;      // [spans][ld_rows]
     float *target_logit;   // [rows]
     int64_t ld_rows;
+    // the same against a teacher's distribution (targets and target_logit are not used)
+    const uint16_t *first;  // [rows][ld_first]: a row's entries before each span, and all of them
+    int64_t ld_first;
+    const int32_t *ids;     // [rows][top], in order
+    float *at;              // [rows][top]: their logits
+    int64_t top;
+    float log2e;            // log2(e) / temperature
     // kScale
     const float *scale;    // device scalar, or NULL for 1
     float scale_const;     // and this constant factor
@@ -61,6 +68,8 @@ struct GemmArgs {
 // `exponentials`: where they go (used with kExp).
 fsdp_status launch_logits(Epilogue ep, bool f32, const CUtensorMap &a, const CUtensorMap &b,
                           const CUtensorMap &exponentials, const GemmArgs &g, cudaStream_t s);
+fsdp_status launch_soft_logits(Epilogue ep, bool f32, const CUtensorMap &a, const CUtensorMap &b,
+                               const CUtensorMap &exponentials, const GemmArgs &g, cudaStream_t s);
 fsdp_status launch_grad_bf16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
 fsdp_status launch_grad_f16(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
 fsdp_status launch_grad_f32(Orders o, const CUtensorMap &a, const CUtensorMap &b, const GemmArgs &g, cudaStream_t s);
@@ -82,6 +91,46 @@ fsdp_status launch_wait_check(long long limit, long long arrive_after, int32_t *
 // 316 to 245 / 836 to 734 / 6363 to 5291.
 inline int64_t few_rows(int dtype, bool grad) { return dtype == FSDP_F32 ? (grad ? 8 : 24) : (grad ? 0 : 4); }
 
+// ---------------------------------------------------------------- a teacher's distribution
+
+constexpr int64_t kIgnored = -100;        // target of a row without entries
+constexpr int32_t kNoEntry = 0x7fffffff;  // id behind a row's last entry
+
+// The teacher's entries, a row's in the order of their tokens: each one's
+// probability over the entries and its logarithm.
+struct SoftArgs {
+    const void *teacher, *given;  // logits and tokens as the caller has them
+    int64_t ld_teacher, ld_given;
+    int32_t teacher_dtype, wide;  // wide: 64-bit tokens
+    int64_t top, vocab;
+    float temperature, inverse, log2e;  // 1 / temperature, log2(e) / temperature
+    int32_t *ids;                 // [band][top]; NULL: the targets alone
+    float2 *prob;                 // [band][top]: {p, log p}
+    uint16_t *first;              // [band][ld_first], or NULL
+    int64_t ld_first, spans;
+    int64_t *targets;             // 0 for a row that counts, kIgnored, or vocab for one whose entries are wrong
+};
+
+fsdp_status launch_prepare(const SoftArgs &a, int64_t row0, int64_t rows, cudaStream_t s);
+
+// A few rows' logits to the gradients of them, in place.
+struct FewSoftArgs {
+    float *logits;
+    const float2 *row_state;
+    int64_t ld_logits, rows, vocab, top;
+    const int64_t *targets;
+    const int32_t *ids;
+    const float2 *prob;
+    float log2e;
+};
+fsdp_status launch_few_soft(const FewSoftArgs &a, cudaStream_t s);
+
+// The distillation loss: args as the cross entropy's (its targets are not
+// read), and the teacher's. In loss.cu.
+fsdp_status soft_workspace(const fsdp_head_loss_args &args, int64_t top, int64_t *bytes_out);
+fsdp_status soft_run(fsdp_head_loss_args args, SoftArgs soft, void *workspace, int64_t workspace_bytes, cudaStream_t s);
+fsdp_status check_head(const fsdp_head_loss_args &args, const void *const *inputs, const size_t *input_bytes, int n_inputs);
+
 struct FewArgs {
     const void *hidden, *weight;
     int64_t ld_hidden, ld_weight, rows, vocab, dim, blocks;
@@ -91,11 +140,13 @@ struct FewArgs {
     float *target_logit;
     float *logits;     // [rows][ld_logits], for the gradients, or NULL
     int64_t ld_logits;
+    float log2e;       // log2(e), over the temperature
     uint32_t *ticket;  // cleared for the row kernel
 };
 
 struct FewGradArgs {
-    const float *hidden, *weight, *logits;
+    const float *hidden, *weight, *logits;  // (soft: the gradients of the logits)
+    int32_t soft;
     const float2 *row_state;  // {largest logit, sum of the exponentials against it}
     int64_t ld_hidden, ld_weight, ld_logits, rows, vocab, dim;
     const int64_t *targets;

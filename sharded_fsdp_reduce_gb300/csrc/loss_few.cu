@@ -29,18 +29,18 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kTake = 4;  // vocabulary rows of a warp's step
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// e^x; e^0 is exactly 1.
-__device__ __forceinline__ float exp_of(float x) { return exp2f(x * kLog2e); }
+// e^x, or of x over a temperature; e^0 is exactly 1.
+__device__ __forceinline__ float exp_of(float x, float log2e = kLog2e) { return exp2f(x * log2e); }
 
 // sum * e^top with one more term e^logit.
-__device__ __forceinline__ void take(float &top, float &sum, float logit) {
+__device__ __forceinline__ void take(float &top, float &sum, float logit, float log2e) {
     const float most = fmaxf(top, logit);
-    sum = sum * exp_of(top - most) + exp_of(logit - most);
+    sum = sum * exp_of(top - most, log2e) + exp_of(logit - most, log2e);
     top = most;
 }
-__device__ __forceinline__ void join(float &top, float &sum, float other_top, float other_sum) {
+__device__ __forceinline__ void join(float &top, float &sum, float other_top, float other_sum, float log2e) {
     const float most = fmaxf(top, other_top);
-    sum = sum * exp_of(top - most) + other_sum * exp_of(other_top - most);
+    sum = sum * exp_of(top - most, log2e) + other_sum * exp_of(other_top - most, log2e);
     top = most;
 }
 
@@ -156,7 +156,7 @@ template <int DT, int R, bool VEC> __global__ void __launch_bounds__(kThreads, 2
             if (v < a.vocab) {
                 if (first && v == target[t]) a.target_logit[row0 + t] = logit;
                 if (first && a.logits != nullptr && t < rows) a.logits[(row0 + t) * a.ld_logits + v] = logit;
-                take(top[t], sum[t], logit);
+                take(top[t], sum[t], logit, a.log2e);
             }
         }
     }
@@ -164,7 +164,7 @@ template <int DT, int R, bool VEC> __global__ void __launch_bounds__(kThreads, 2
     for (int t = 0; t < R; ++t) {
 #pragma unroll
         for (int o = 16; o >= 32 / kTake; o >>= 1)
-            join(top[t], sum[t], __shfl_xor_sync(0xffffffffu, top[t], o), __shfl_xor_sync(0xffffffffu, sum[t], o));
+            join(top[t], sum[t], __shfl_xor_sync(0xffffffffu, top[t], o), __shfl_xor_sync(0xffffffffu, sum[t], o), a.log2e);
         if (lane == 0) {
             tops[warp][t] = top[t];
             sums[warp][t] = sum[t];
@@ -175,7 +175,7 @@ template <int DT, int R, bool VEC> __global__ void __launch_bounds__(kThreads, 2
     if (t < rows) {
         float m = tops[0][t], s = sums[0][t];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) join(m, s, tops[i][t], sums[i][t]);
+        for (int i = 1; i < kWarps; ++i) join(m, s, tops[i][t], sums[i][t], a.log2e);
         a.off[block * a.ld_rows + row0 + t] = m;
         a.sum[block * a.ld_rows + row0 + t] = s;
     }
@@ -200,6 +200,7 @@ template <int DT> fsdp_status launch_type(const FewArgs &a, cudaStream_t s) {
 // d[t, v] from a stored logit.
 __device__ __forceinline__ float d_of(const FewGradArgs &a, int64_t t, int64_t v) {
     if (t >= a.rows || v >= a.vocab) return 0.0f;
+    if (a.soft) return a.logits[t * a.ld_logits + v];
     const int64_t y = a.targets[t];
     if (y == a.ignore) return 0.0f;
     if (y < 0 || y >= a.vocab) return NAN;

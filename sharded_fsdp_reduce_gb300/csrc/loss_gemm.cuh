@@ -211,6 +211,23 @@ __device__ __forceinline__ void store_exponentials(const CUtensorMap *map, uint8
     }
 }
 
+// v[j] of 64 registers: a tree of selections, group after group, so that few
+// of them wait.
+__device__ __forceinline__ float pick(const float *v, int j) {
+    float group[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float *x = v + 8 * i;
+        const float a = j & 1 ? x[1] : x[0], b = j & 1 ? x[3] : x[2], c = j & 1 ? x[5] : x[4], d = j & 1 ? x[7] : x[6];
+        const float e = j & 2 ? b : a, f = j & 2 ? d : c;
+        group[i] = j & 4 ? f : e;
+    }
+    const float a = j & 8 ? group[1] : group[0], b = j & 8 ? group[3] : group[2];
+    const float c = j & 8 ? group[5] : group[4], d = j & 8 ? group[7] : group[6];
+    const float e = j & 16 ? b : a, f = j & 16 ? d : c;
+    return j & 32 ? f : e;
+}
+
 // Softmax statistics (and exponentials) of one warp's 32 rows x 64 columns. A
 // span's exponentials are against its own largest logit, subtracted as it is:
 // the largest one is then exactly 1, the sum at least 1 and a row's loss
@@ -219,19 +236,34 @@ __device__ __forceinline__ void store_exponentials(const CUtensorMap *map, uint8
 // past 2^31 by more than exponentials can hold). In fp16 they are stored times
 // 2^15: 11 bits down to 2^-29 of the span's largest (what is smaller is below
 // 2^-40 of it).
-template <int EP, int DT>
+//
+// SOFT: the exponentials are of the logits over a temperature, and the logits
+// of the teacher's entries are stored. `target` holds the row's first entry of
+// the span and the first one after it, id the first one's token.
+template <int EP, int DT, bool SOFT>
 __device__ __forceinline__ void softmax_span(const GemmArgs &g, const CUtensorMap *map, uint8_t *box, int lane,
-                                             float *v, int64_t row0, int64_t col0, int64_t target) {
-    constexpr float kLog2e = 1.44269504088896340736f;
+                                             float *v, int64_t row0, int64_t col0, int64_t target, int id) {
+    const float kLog2e = SOFT ? g.log2e : 1.44269504088896340736f;
     const int64_t row = row0 + lane;
     const bool live = row < g.M;
-    const int64_t at = target - col0;
-    if (at >= 0 && at < kSpan && at + col0 < g.N) {
-        float t = 0.0f;
+    if constexpr (SOFT) {
+        const uint32_t end = static_cast<uint32_t>(target) >> 16;
+        const int32_t *ids = g.ids + row * g.top;
+        float *to = g.at + row * g.top;
+#pragma unroll 1
+        for (uint32_t k = static_cast<uint32_t>(target) & 0xffffu; k < end;) {
+            to[k] = pick(v, id - static_cast<int>(col0));
+            if (++k < end) id = ids[k];
+        }
+    } else {
+        const int64_t at = target - col0;
+        if (at >= 0 && at < kSpan && at + col0 < g.N) {
+            float t = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kSpan; ++j)
-            if (at == j) t = v[j];
-        g.target_logit[row] = t;
+            for (int j = 0; j < kSpan; ++j)
+                if (at == j) t = v[j];
+            g.target_logit[row] = t;
+        }
     }
     if (col0 + kSpan > g.N) {
         const int cols = static_cast<int>(g.N - col0);
@@ -398,7 +430,7 @@ __device__ __forceinline__ void issue_products(const GemmArgs &g, uint8_t *smem,
     }
 }
 
-template <int AMN, int BMN, int EP, int DT, int P>
+template <int AMN, int BMN, int EP, int DT, int P, bool SOFT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_out, const __grid_constant__ GemmArgs g) {
@@ -464,8 +496,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             k_range(g, x.split, k0, k1);
             const int64_t row0 = int64_t(x.m) * kTileM + rank * 128 + quarter * 32;
             const int64_t col0 = int64_t(x.n) * kTileN + part * kSpan;
-            int64_t target = -1;  // loaded while the products run
-            if constexpr (EP != kScale) {
+            int64_t target = SOFT ? 0 : -1;  // loaded while the products run
+            int id = 0;
+            if constexpr (EP != kScale && SOFT) {
+                if (row0 + lane < g.M && col0 < g.N) {
+                    const uint16_t *first = g.first + (row0 + lane) * g.ld_first + col0 / kSpan;
+                    const uint32_t begin = first[0], end = first[1];
+                    target = static_cast<uint32_t>(begin | end << 16);
+                    if (begin < end) id = g.ids[(row0 + lane) * g.top + begin];
+                }
+            } else if constexpr (EP != kScale) {
                 if (row0 + lane < g.M) target = g.targets[row0 + lane];
             }
             float v[kSpan];
@@ -494,7 +534,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if constexpr (EP == kScale)
                     scaled_span<DT>(g, v, row0 + lane, col0, x.split, scale);
                 else
-                    softmax_span<EP, DT>(g, &map_out, boxes + (warp - 4) * kBoxBytes, lane, v, row0, col0, target);
+                    softmax_span<EP, DT, SOFT>(g, &map_out, boxes + (warp - 4) * kBoxBytes, lane, v, row0, col0, target,
+                                               id);
             }
         }
     }
@@ -515,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 2) tc::free_pair(tensor, kTensorCols);
 }
 
-template <int AMN, int BMN, int EP, int DT, int P>
+template <int AMN, int BMN, int EP, int DT, int P, bool SOFT = false>
 fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, GemmArgs g,
                           cudaStream_t s) {
     g.k_each = g.kblocks / g.splits;
@@ -523,7 +564,7 @@ fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUte
     static PerDeviceOnce once;
     const int dev = current_device();
     if (!once.is_done(dev)) {
-        const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<AMN, BMN, EP, DT, P>,
+        const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<AMN, BMN, EP, DT, P, SOFT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem_bytes(EP, P)));
         if (e != cudaSuccess) return cuda_status(e);
@@ -533,7 +574,7 @@ fsdp_status launch_kernel(const CUtensorMap &a, const CUtensorMap &b, const CUte
     if (total < 1 || total > 0x3fffffff) return FSDP_ERR_INVALID_ARG;  // (the kernel's tile counter adds to it)
     const int64_t pairs = sm_count() / 2;
     const unsigned grid = static_cast<unsigned>(2 * (total < pairs ? total : (pairs > 0 ? pairs : 1)));
-    return launch_chained(gemm_kernel<AMN, BMN, EP, DT, P>, grid, kThreads, smem_bytes(EP, P), s, a, b, out, g);
+    return launch_chained(gemm_kernel<AMN, BMN, EP, DT, P, SOFT>, grid, kThreads, smem_bytes(EP, P), s, a, b, out, g);
 }
 
 }  // namespace loss

@@ -128,7 +128,88 @@ def fsdp_check_head_loss_wait(limit_cycles: int, arrive_after_cycles: int, outco
            "fsdp_check_head_loss_wait")
 
 
-class HeadLoss:
+class Head:
+    """The workspace that a head's loss calls share, whatever the loss."""
+
+    def _start(self, vocab, dim, dtype, max_tokens, grad, band, reduction, device) -> None:
+        if reduction not in _REDUCTIONS:
+            raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
+        self.vocab, self.dim, self.dtype = int(vocab), int(dim), dtype
+        self.max_tokens, self.grad, self.band = int(max_tokens), bool(grad), int(band)
+        self.reduction = reduction
+        self.device = torch.device(device)
+        self._kept = []
+        odd = self.dim % 8 != 0  # (contiguous rows are then not aligned)
+        self._forms = (self.grad, odd, odd)
+        self._allocate(self._need(*self._forms))
+
+    def _sized(self, step: int):
+        """Arguments of a call of max_tokens rows, but for hidden, weight and
+        the gradients; addresses are multiples of step and not read."""
+        raise NotImplementedError
+
+    def _bytes(self, a) -> int:
+        raise NotImplementedError
+
+    def _enqueue(self, a, stream: torch.cuda.Stream) -> int:
+        raise NotImplementedError
+
+    def _need(self, grad: bool, odd_hidden: bool, odd_weight: bool) -> int:
+        """Workspace of every call of up to max_tokens rows: with gradients or
+        not, hidden and weight 16-byte aligned or not (addresses are not read)."""
+        step, off = 1 << 56, self.dtype.itemsize
+        a = self._sized(step)
+        a.dtype = dtype_code(self.dtype)
+        a.tokens, a.vocab, a.dim, a.band = self.max_tokens, self.vocab, self.dim, self.band
+        a.hidden, a.weight = step + (off if odd_hidden else 0), 2 * step + (off if odd_weight else 0)
+        a.loss = 4 * step
+        a.ld_hidden = a.ld_weight = a.ld_d_hidden = a.ld_d_weight = -(-self.dim // 8) * 8
+        a.grad_scale = 1.0
+        need = self._bytes(a)
+        if grad:
+            a.d_hidden, a.d_weight = 5 * step, 6 * step
+            need = max(need, self._bytes(a))
+        return need
+
+    def _allocate(self, nbytes: int) -> None:
+        self._ws = Workspace(nbytes, self.device, alignment=1024)
+        self._ws_at, self._ws_bytes = self._ws.buf.data_ptr(), nbytes
+
+    def _grow(self, a) -> None:
+        """A larger workspace, for a call's form and all the earlier ones."""
+        odd = [p % 16 != 0 or ld % 8 != 0 for p, ld in ((a.hidden, a.ld_hidden), (a.weight, a.ld_weight))]
+        new = (a.d_hidden is not None or a.d_weight is not None, *odd)
+        self._forms = tuple(x or y for x, y in zip(self._forms, new))
+        self._kept.append(self._ws)
+        self._allocate(self._need(*self._forms))
+
+    def _check_operands(self, hidden, weight) -> None:
+        if hidden.dim() != 2 or hidden.shape[0] > self.max_tokens or hidden.shape[1] != self.dim:
+            raise ValueError(f"hidden must be [at most {self.max_tokens}, {self.dim}]")
+        if hidden.dtype != self.dtype or tuple(weight.shape) != (self.vocab, self.dim):
+            raise ValueError(f"hidden must be {self.dtype} and weight [{self.vocab}, {self.dim}]")
+
+    @staticmethod
+    def _results(hidden, loss, token_loss, stream):
+        if loss is None or token_loss is None:
+            with torch.cuda.stream(stream):  # new results belong to the call's stream
+                if loss is None:
+                    loss = torch.empty((), dtype=torch.float32, device=hidden.device)
+                if token_loss is None:
+                    token_loss = torch.empty(hidden.shape[0], dtype=torch.float32, device=hidden.device)
+        return loss, token_loss
+
+    def _launch(self, a, stream: torch.cuda.Stream, name: str) -> None:
+        self._ws.on(stream)
+        status = self._enqueue(a, stream)
+        if status == _lib.FSDP_ERR_INVALID_ARG and self._bytes(a) > self._ws_bytes:
+            with torch.cuda.stream(stream):
+                self._grow(a)
+            status = self._enqueue(a, stream)
+        _check(status, name)
+
+
+class HeadLoss(Head):
     """A head's loss with the workspace its calls share.
 
     vocab, dim, dtype: the weight's shape and the dtype of hidden, weight and
@@ -146,45 +227,19 @@ class HeadLoss:
 
     def __init__(self, vocab: int, dim: int, dtype: torch.dtype, max_tokens: int, grad: bool = True, band: int = 0,
                  ignore_index: int = -100, reduction: str = "mean", device="cuda"):
-        if reduction not in _REDUCTIONS:
-            raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
-        self.vocab, self.dim, self.dtype = int(vocab), int(dim), dtype
-        self.max_tokens, self.grad, self.band = int(max_tokens), bool(grad), int(band)
-        self.ignore_index, self.reduction = int(ignore_index), reduction
-        self.device = torch.device(device)
-        self._kept = []
-        odd = self.dim % 8 != 0  # (contiguous rows are then not aligned)
-        self._forms = (self.grad, odd, odd)
-        self._allocate(self._need(*self._forms))
+        self.ignore_index = int(ignore_index)
+        self._start(vocab, dim, dtype, max_tokens, grad, band, reduction, device)
 
-    def _need(self, grad: bool, odd_hidden: bool, odd_weight: bool) -> int:
-        """Workspace of every call of up to max_tokens rows: with gradients or
-        not, hidden and weight 16-byte aligned or not (addresses are not read)."""
+    def _sized(self, step: int) -> _lib.FsdpHeadLossArgs:
         a = _lib.FsdpHeadLossArgs()
-        a.dtype = dtype_code(self.dtype)
-        a.tokens, a.vocab, a.dim, a.band = self.max_tokens, self.vocab, self.dim, self.band
-        step, off = 1 << 56, self.dtype.itemsize
-        a.hidden, a.weight = step + (off if odd_hidden else 0), 2 * step + (off if odd_weight else 0)
-        a.targets, a.loss = 3 * step, 4 * step
-        a.ld_hidden = a.ld_weight = a.ld_d_hidden = a.ld_d_weight = -(-self.dim // 8) * 8
-        a.grad_scale = 1.0
-        need = _workspace_bytes(a)
-        if grad:
-            a.d_hidden, a.d_weight = 5 * step, 6 * step
-            need = max(need, _workspace_bytes(a))
-        return need
+        a.targets = 3 * step
+        return a
 
-    def _allocate(self, nbytes: int) -> None:
-        self._ws = Workspace(nbytes, self.device, alignment=1024)
-        self._ws_at, self._ws_bytes = self._ws.buf.data_ptr(), nbytes
+    def _bytes(self, a: _lib.FsdpHeadLossArgs) -> int:
+        return _workspace_bytes(a)
 
-    def _grow(self, a: _lib.FsdpHeadLossArgs) -> None:
-        """A larger workspace, for a call's form and all the earlier ones."""
-        odd = [p % 16 != 0 or ld % 8 != 0 for p, ld in ((a.hidden, a.ld_hidden), (a.weight, a.ld_weight))]
-        new = (a.d_hidden is not None or a.d_weight is not None, *odd)
-        self._forms = tuple(x or y for x, y in zip(self._forms, new))
-        self._kept.append(self._ws)
-        self._allocate(self._need(*self._forms))
+    def _enqueue(self, a: _lib.FsdpHeadLossArgs, stream: torch.cuda.Stream) -> int:
+        return _launch(a, self._ws_at, self._ws_bytes, stream)
 
     def forward(self, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                 loss: Optional[torch.Tensor] = None, token_loss: Optional[torch.Tensor] = None,
@@ -205,24 +260,10 @@ class HeadLoss:
                          wait_timeouts)
 
     def _run(self, hidden, weight, targets, d_hidden, d_weight, grad_scale, loss, token_loss, stream, wait_timeouts):
-        if hidden.dim() != 2 or hidden.shape[0] > self.max_tokens or hidden.shape[1] != self.dim:
-            raise ValueError(f"hidden must be [at most {self.max_tokens}, {self.dim}]")
-        if hidden.dtype != self.dtype or tuple(weight.shape) != (self.vocab, self.dim):
-            raise ValueError(f"hidden must be {self.dtype} and weight [{self.vocab}, {self.dim}]")
+        self._check_operands(hidden, weight)
         s = stream if stream is not None else torch.cuda.current_stream()
-        if loss is None or token_loss is None:
-            with torch.cuda.stream(s):  # new results belong to the call's stream
-                if loss is None:
-                    loss = torch.empty((), dtype=torch.float32, device=hidden.device)
-                if token_loss is None:
-                    token_loss = torch.empty(hidden.shape[0], dtype=torch.float32, device=hidden.device)
+        loss, token_loss = self._results(hidden, loss, token_loss, s)
         a = _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, self.ignore_index, self.reduction,
                   grad_scale, self.band, wait_timeouts)
-        self._ws.on(s)
-        status = _launch(a, self._ws_at, self._ws_bytes, s)
-        if status == _lib.FSDP_ERR_INVALID_ARG and _workspace_bytes(a) > self._ws_bytes:
-            with torch.cuda.stream(s):
-                self._grow(a)
-            status = _launch(a, self._ws_at, self._ws_bytes, s)
-        _check(status, "fsdp_head_loss")
+        self._launch(a, s, "fsdp_head_loss")
         return loss, token_loss
