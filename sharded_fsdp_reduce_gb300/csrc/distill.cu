@@ -52,89 +52,127 @@ __device__ __forceinline__ float warp_max(float x) {
     return x;
 }
 
-// A warp puts `size` (a power of two, at least 64) values in order.
-__device__ __forceinline__ void sort_warp(uint64_t *list, int size) {
+// A warp puts its 32 N values in order: the i-th of lane l is the (32 i + l)-th.
+template <int N> __device__ __forceinline__ void sort_warp(uint64_t (&x)[N]) {
     const int lane = threadIdx.x % 32;
-    for (int run = 2; run <= size; run *= 2) {
-        for (int apart = run / 2; apart > 0; apart /= 2) {
-            for (int i = lane; i < size / 2; i += 32) {
-                const int lo = i / apart * 2 * apart + i % apart, hi = lo + apart;
-                const uint64_t x = list[lo], y = list[hi];
-                if ((x > y) == ((lo & run) == 0)) {
-                    list[lo] = y;
-                    list[hi] = x;
-                }
+#pragma unroll
+    for (int run = 2; run <= 32 * N; run *= 2) {
+#pragma unroll
+        for (int apart = run / 2; apart >= 32; apart /= 2) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int o = i ^ (apart / 32);
+                if (o < i) continue;
+                const bool up = ((32 * i) & run) == 0;  // (run > 32: the same for all lanes)
+                const uint64_t a = x[i], b = x[o];
+                x[i] = (a > b) == up ? b : a;
+                x[o] = (a > b) == up ? a : b;
             }
-            __syncwarp();
+        }
+#pragma unroll
+        for (int apart = run / 2 < 32 ? run / 2 : 16; apart > 0; apart /= 2) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const bool up = ((32 * i + lane) & run) == 0, low = (lane & apart) == 0;
+                const uint64_t a = x[i], b = __shfl_xor_sync(kAll, a, apart);
+                x[i] = (a > b) == (up == low) ? b : a;
+            }
         }
     }
 }
 
-// A warp per row. An entry that does not count: token -1, or a logit of minus
-// infinity, or one so small that its probability is 0.
+// A warp per row of at most 32 N entries, N a power of two. An entry that does
+// not count: token -1, or a logit of minus infinity, or one so small that its
+// probability is 0. `late`: the kernel before this one on the stream does not
+// touch what it reads or writes, and what came before that has ended; so this
+// one waits for it last.
+template <int N>
 __global__ void __launch_bounds__(kThreads)
-    prepare_kernel(const __grid_constant__ SoftArgs a, int64_t row0, int64_t rows, int size) {
+    prepare_kernel(const __grid_constant__ SoftArgs a, int64_t row0, int64_t rows, bool late) {
     extern __shared__ uint64_t lists[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    uint64_t *list = lists + warp * size;
+    uint64_t *list = lists + warp * 32 * N;
     const int64_t r = int64_t(blockIdx.x) * kWarps + warp, row = row0 + r;
-    wait_previous();
-    allow_next();
-    if (r >= rows) return;
-    bool bad = false, any = false;
-    float most = -INFINITY;
-    for (int k = lane; k < size; k += 32) {
-        uint64_t entry = kNone;
-        if (k < a.top) {
-            const int64_t token = teacher_token(a, row * a.ld_given + k);
-            if (token < 0 || token >= a.vocab) {
-                bad |= token != -1;
-            } else {
-                const float x = teacher_logit(a, row * a.ld_teacher + k);
-                if (x != -INFINITY) {
-                    bad |= !(x < INFINITY);
-                    any = true;
-                    most = fmaxf(most, x);
-                    entry = entry_of(static_cast<uint64_t>(token), x);
+    if (!late) {
+        wait_previous();
+        allow_next();
+    }
+    if (r < rows) {
+        int64_t token[N];
+        float logit[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = 32 * i + lane;
+            token[i] = k < a.top ? teacher_token(a, row * a.ld_given + k) : -1;
+            logit[i] = k < a.top ? teacher_logit(a, row * a.ld_teacher + k) : -INFINITY;
+        }
+        bool bad = false, any = false;
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool of_vocab = token[i] >= 0 && token[i] < a.vocab;
+            if (!of_vocab) {
+                bad |= token[i] != -1;
+                logit[i] = -INFINITY;
+            }
+            if (logit[i] != -INFINITY) {
+                bad |= !(logit[i] < INFINITY);
+                any = true;
+                most = fmaxf(most, logit[i]);
+            }
+        }
+        bad = __any_sync(kAll, bad);
+        any = __any_sync(kAll, any);
+        if (lane == 0) a.targets[row] = bad ? a.vocab : any ? 0 : kIgnored;
+        if (a.ids != nullptr) {
+            most = warp_max(most);
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (logit[i] != -INFINITY) sum += expf((logit[i] - most) * a.inverse);
+            sum = warp_sum(sum);
+            const float log_sum = logf(sum), least = bad || !any ? INFINITY : 0.0f;
+            uint64_t entry[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const bool counts = logit[i] != -INFINITY && expf((logit[i] - most) * a.inverse) / sum > least;
+                entry[i] = counts ? entry_of(static_cast<uint64_t>(token[i]), logit[i]) : kNone;
+            }
+            sort_warp<N>(entry);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int k = 32 * i + lane;
+                list[k] = entry[i];
+                if (k < a.top) {
+                    const bool there = entry[i] != kNone;
+                    const float x = (logit_of(entry[i]) - most) * a.inverse;
+                    a.ids[r * a.top + k] = there ? static_cast<int32_t>(entry[i] >> 32) : kNoEntry;
+                    a.prob[r * a.top + k] = there ? make_float2(expf(x) / sum, x - log_sum) : make_float2(0.0f, 0.0f);
+                }
+            }
+            __syncwarp();
+            if (a.first != nullptr) {
+                // entries before column 64 s, four spans of a lane at a time
+                uint16_t *first = a.first + r * a.ld_first;
+                for (int64_t s0 = lane; s0 <= a.spans; s0 += 4 * 32) {
+                    int at[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int step = 32 * N / 2; step > 0; step /= 2)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (list[at[u] + step - 1] < static_cast<uint64_t>((s0 + 32 * u) * kSpan) << 32) at[u] += step;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint64_t limit = static_cast<uint64_t>((s0 + 32 * u) * kSpan) << 32;
+                        if (s0 + 32 * u <= a.spans) first[s0 + 32 * u] = static_cast<uint16_t>(at[u] + (list[at[u]] < limit));
+                    }
                 }
             }
         }
-        list[k] = entry;
     }
-    bad = __any_sync(kAll, bad);
-    any = __any_sync(kAll, any);
-    if (lane == 0) a.targets[row] = bad ? a.vocab : any ? 0 : kIgnored;
-    if (a.ids == nullptr) return;
-    most = warp_max(most);
-    const bool counts = any && !bad;
-    float sum = 0.0f;
-    for (int k = lane; k < size; k += 32)
-        if (list[k] != kNone) sum += expf((logit_of(list[k]) - most) * a.inverse);
-    sum = warp_sum(sum);
-    for (int k = lane; k < size; k += 32)
-        if (!counts || (list[k] != kNone && expf((logit_of(list[k]) - most) * a.inverse) / sum == 0.0f)) list[k] = kNone;
-    __syncwarp();
-    if (counts) sort_warp(list, size);
-    const float log_sum = logf(sum);
-    for (int k = lane; k < a.top; k += 32) {
-        const bool there = list[k] != kNone;
-        const float x = (logit_of(list[k]) - most) * a.inverse;
-        a.ids[r * a.top + k] = there ? static_cast<int32_t>(list[k] >> 32) : kNoEntry;
-        a.prob[r * a.top + k] = there ? make_float2(expf(x) / sum, x - log_sum) : make_float2(0.0f, 0.0f);
-    }
-    if (a.first == nullptr) return;
-    for (int64_t s = lane; s <= a.spans; s += 32) {
-        // entries before column 64 s
-        const uint64_t limit = static_cast<uint64_t>(s * kSpan) << 32;
-        int lo = 0, hi = size;
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (list[mid] < limit)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        a.first[r * a.ld_first + s] = static_cast<uint16_t>(lo);
+    if (late) {
+        wait_previous();
+        allow_next();
     }
 }
 
@@ -213,20 +251,31 @@ fsdp_status check(const fsdp_head_distill_args *d) {
 
 }  // namespace
 
-fsdp_status launch_prepare(const SoftArgs &a, int64_t row0, int64_t rows, cudaStream_t s) {
-    int size = 64;
-    while (size < a.top) size *= 2;
-    const size_t smem = static_cast<size_t>(size) * kWarps * sizeof(uint64_t);
+namespace {
+
+template <int N> fsdp_status prepare(const SoftArgs &a, int64_t row0, int64_t rows, bool late, cudaStream_t s) {
+    constexpr size_t kShared = 32 * N * kWarps * sizeof(uint64_t);
     static PerDeviceOnce once;
     const int dev = current_device();
     if (!once.is_done(dev)) {
-        const cudaError_t e = cudaFuncSetAttribute(prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(kMostTop * kWarps * sizeof(uint64_t)));
+        const cudaError_t e = cudaFuncSetAttribute(prepare_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(kShared));
         if (e != cudaSuccess) return cuda_status(e);
         once.mark(dev);
     }
-    return launch_chained(prepare_kernel, static_cast<unsigned>((rows + kWarps - 1) / kWarps), kThreads, smem, s, a, row0,
-                          rows, size);
+    return launch_chained(prepare_kernel<N>, static_cast<unsigned>((rows + kWarps - 1) / kWarps), kThreads, kShared, s, a,
+                          row0, rows, late);
+}
+
+}  // namespace
+
+fsdp_status launch_prepare(const SoftArgs &a, int64_t row0, int64_t rows, bool late, cudaStream_t s) {
+    return a.top <= 32    ? prepare<1>(a, row0, rows, late, s)
+           : a.top <= 64  ? prepare<2>(a, row0, rows, late, s)
+           : a.top <= 128 ? prepare<4>(a, row0, rows, late, s)
+           : a.top <= 256 ? prepare<8>(a, row0, rows, late, s)
+           : a.top <= 512 ? prepare<16>(a, row0, rows, late, s)
+                          : prepare<32>(a, row0, rows, late, s);
 }
 
 fsdp_status launch_few_soft(const FewSoftArgs &a, cudaStream_t s) {

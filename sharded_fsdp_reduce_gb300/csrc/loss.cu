@@ -853,7 +853,7 @@ fsdp_status run_few(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, co
     f.vocab = a.vocab;
     f.dim = a.dim;
     f.blocks = p.spans;
-    f.targets = a.targets;
+    f.targets = soft ? nullptr : a.targets;
     f.off = reinterpret_cast<float *>(ws + p.off);
     f.sum = reinterpret_cast<float *>(ws + p.sum);
     f.ld_rows = p.band;
@@ -951,9 +951,8 @@ fsdp_status run_rows(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, i
 fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, SoftArgs *soft, cudaStream_t s) {
     int64_t block = 0;
     if (p.few) {
-        fsdp_status few = FSDP_OK;
-        if (soft) few = launch_prepare(*soft, 0, a.tokens, s);
-        if (few == FSDP_OK) few = run_few(a, p, ws, soft, s);
+        fsdp_status few = run_few(a, p, ws, soft, s);
+        if (few == FSDP_OK && soft) few = launch_prepare(*soft, 0, a.tokens, true, s);  // beside the dot products
         if (few == FSDP_OK) few = run_rows(a, p, ws, 0, a.tokens, block, soft, s);
         return few == FSDP_OK && p.grad ? run_few_grad(a, p, ws, soft, s) : few;
     }
@@ -967,7 +966,7 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, SoftAr
         // which rows count, before the first band
         SoftArgs all = *soft;
         if (p.bands > 1) all.ids = nullptr;
-        if ((st = launch_prepare(all, 0, a.tokens, s)) != FSDP_OK) return st;
+        if ((st = launch_prepare(all, 0, a.tokens, false, s)) != FSDP_OK) return st;
     }
     if (p.pack_x) {
         st = pack(a.hidden, p.f32, a.tokens, D, a.ld_hidden, ws + p.x, p.ldd, a.targets, a.ignore_index, s);
@@ -1018,7 +1017,7 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, SoftAr
         g.ticket = b == 0 ? reinterpret_cast<uint32_t *>(ws + p.ticket) : nullptr;
         g.timeouts = a.wait_timeouts;
         if (soft) {
-            if (p.bands > 1 && (st = launch_prepare(*soft, row0, rows, s)) != FSDP_OK) return st;
+            if (p.bands > 1 && (st = launch_prepare(*soft, row0, rows, false, s)) != FSDP_OK) return st;
             g.first = soft->first;
             g.ld_first = soft->ld_first;
             g.ids = soft->ids;

@@ -111,7 +111,8 @@ struct SoftArgs {
     int64_t *targets;             // 0 for a row that counts, kIgnored, or vocab for one whose entries are wrong
 };
 
-fsdp_status launch_prepare(const SoftArgs &a, int64_t row0, int64_t rows, cudaStream_t s);
+// late: may run beside the kernel before it, whose predecessors have ended.
+fsdp_status launch_prepare(const SoftArgs &a, int64_t row0, int64_t rows, bool late, cudaStream_t s);
 
 // A few rows' logits to the gradients of them, in place.
 struct FewSoftArgs {
@@ -134,7 +135,7 @@ fsdp_status check_head(const fsdp_head_loss_args &args, const void *const *input
 struct FewArgs {
     const void *hidden, *weight;
     int64_t ld_hidden, ld_weight, rows, vocab, dim, blocks;
-    const int64_t *targets;
+    const int64_t *targets;  // NULL: none
     float *off, *sum;  // [blocks][ld_rows]
     int64_t ld_rows;
     float *target_logit;

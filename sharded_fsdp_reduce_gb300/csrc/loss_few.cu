@@ -90,7 +90,7 @@ template <int DT, int R, bool VEC> __global__ void __launch_bounds__(kThreads, 2
     const int rows = static_cast<int>(min(int64_t(R), a.rows - row0));
     const uint8_t *x = static_cast<const uint8_t *>(a.hidden) + row0 * a.ld_hidden * kSize;
     const uint8_t *w = static_cast<const uint8_t *>(a.weight);
-    if (threadIdx.x < R) target[threadIdx.x] = threadIdx.x < rows ? a.targets[row0 + threadIdx.x] : -1;
+    if (threadIdx.x < R) target[threadIdx.x] = threadIdx.x < rows && a.targets != nullptr ? a.targets[row0 + threadIdx.x] : -1;
     __syncthreads();
     float top[R], sum[R];
 #pragma unroll

@@ -24,28 +24,35 @@ __all__ = ["HeadDistill", "fsdp_head_distill"]
 _ID_BITS = {torch.int32: 32, torch.int64: 64}
 
 
-def _args(hidden, weight, teacher_logits, teacher_ids, loss, token_loss, d_hidden, d_weight, temperature, reduction,
-          grad_scale, band, wait_timeouts) -> _lib.FsdpHeadDistillArgs:
+def _blank(temperature: float, reduction: str, band: int) -> _lib.FsdpHeadDistillArgs:
+    """A call's arguments that do not change from one to the next."""
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
+    a = _lib.FsdpHeadDistillArgs()
+    a.temperature, a.reduction, a.band, a.grad_scale = float(temperature), _REDUCTIONS[reduction], int(band), 1.0
+    return a
+
+
+def _fill(a: _lib.FsdpHeadDistillArgs, hidden, weight, teacher_logits, teacher_ids, loss, token_loss, d_hidden, d_weight,
+          grad_scale, wait_timeouts) -> int:
+    """The tensors of a call; the device."""
     for t, name in ((hidden, "hidden"), (weight, "weight"), (teacher_logits, "teacher_logits"),
                     (teacher_ids, "teacher_ids")):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise ValueError(f"{name} must be a matrix")
-    if reduction not in _REDUCTIONS:
-        raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
     if teacher_ids.dtype not in _ID_BITS:
         raise ValueError("teacher_ids must be int32 or int64")
-    T, D = hidden.shape
-    V, K = weight.shape[0], teacher_ids.shape[1]
-    dt = hidden.dtype
     if not hidden.is_cuda:
         _refuse_device(hidden, "hidden")
     cur = torch.cuda.current_device()
-    a = _lib.FsdpHeadDistillArgs()
-    a.dtype, a.teacher_dtype, a.id_bits = dtype_code(dt), dtype_code(teacher_logits.dtype), _ID_BITS[teacher_ids.dtype]
+    T, D = hidden.shape
+    V, K = weight.shape[0], teacher_ids.shape[1]
+    dt, tdt = hidden.dtype, teacher_logits.dtype
+    a.dtype, a.teacher_dtype, a.id_bits = dtype_code(dt), dtype_code(tdt), _ID_BITS[teacher_ids.dtype]
     a.tokens, a.vocab, a.dim, a.top = T, V, D, K
     a.hidden, a.ld_hidden = _matrix(hidden, "hidden", T, D, dt, cur)
     a.weight, a.ld_weight = _matrix(weight, "weight", V, D, dt, cur)
-    a.teacher_logits, a.ld_teacher_logits = _matrix(teacher_logits, "teacher_logits", T, K, teacher_logits.dtype, cur)
+    a.teacher_logits, a.ld_teacher_logits = _matrix(teacher_logits, "teacher_logits", T, K, tdt, cur)
     a.teacher_ids, a.ld_teacher_ids = _matrix(teacher_ids, "teacher_ids", T, K, teacher_ids.dtype, cur)
     a.loss = _vector(loss, "loss", 1, torch.float32, cur)
     if token_loss is not None:
@@ -54,13 +61,10 @@ def _args(hidden, weight, teacher_logits, teacher_ids, loss, token_loss, d_hidde
         a.d_hidden, a.ld_d_hidden = _matrix(d_hidden, "d_hidden", T, D, dt, cur)
     if d_weight is not None:
         a.d_weight, a.ld_d_weight = _matrix(d_weight, "d_weight", V, D, dt, cur)
-    a.temperature = float(temperature)
-    a.reduction = _REDUCTIONS[reduction]
     a.grad_scale = float(grad_scale)
-    a.band = int(band)
     if wait_timeouts is not None:
         a.wait_timeouts = _counter(wait_timeouts, "wait_timeouts")
-    return a
+    return cur
 
 
 def _workspace_bytes(a: _lib.FsdpHeadDistillArgs) -> int:
@@ -82,8 +86,8 @@ def fsdp_head_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_logits
     or int64 (rows contiguous; -1: no entry); loss fp32 scalar, token_loss fp32
     [T], d_hidden [T, D] and d_weight [V, D] of hidden's dtype are written (d_*
     None: not formed)."""
-    a = _args(hidden, weight, teacher_logits, teacher_ids, loss, token_loss, d_hidden, d_weight, temperature, reduction,
-              grad_scale, band, wait_timeouts)
+    a = _blank(temperature, reduction, band)
+    _fill(a, hidden, weight, teacher_logits, teacher_ids, loss, token_loss, d_hidden, d_weight, grad_scale, wait_timeouts)
     s = stream if stream is not None else torch.cuda.current_stream()
     with torch.cuda.stream(s):  # taken, and given back, in that stream's order
         ws = take(_workspace_bytes(a), hidden.device, alignment=1024)
@@ -105,20 +109,21 @@ class HeadDistill(Head):
     def __init__(self, vocab: int, dim: int, dtype: torch.dtype, max_tokens: int, top: int, temperature: float = 1.0,
                  grad: bool = True, band: int = 0, reduction: str = "mean", device="cuda"):
         self.top, self.temperature = int(top), float(temperature)
+        self._blank = _blank(temperature, reduction, band)
         self._start(vocab, dim, dtype, max_tokens, grad, band, reduction, device)
 
     def _sized(self, step: int) -> _lib.FsdpHeadDistillArgs:
-        a = _lib.FsdpHeadDistillArgs()
+        a = _lib.FsdpHeadDistillArgs.from_buffer_copy(self._blank)
         a.teacher_logits, a.teacher_ids = 3 * step, 7 * step
         a.top = a.ld_teacher_logits = a.ld_teacher_ids = self.top
-        a.teacher_dtype, a.id_bits, a.temperature = _lib.FSDP_F32, 64, self.temperature
+        a.teacher_dtype, a.id_bits = _lib.FSDP_F32, 64
         return a
 
     def _bytes(self, a: _lib.FsdpHeadDistillArgs) -> int:
         return _workspace_bytes(a)
 
-    def _enqueue(self, a: _lib.FsdpHeadDistillArgs, stream: torch.cuda.Stream) -> int:
-        return _lib.load().fsdp_head_distill(ctypes.byref(a), self._ws_at, self._ws_bytes, stream.cuda_stream)
+    def _enqueue(self, a: _lib.FsdpHeadDistillArgs, stream: int) -> int:
+        return _lib.load().fsdp_head_distill(ctypes.byref(a), self._ws_at, self._ws_bytes, stream)
 
     def forward(self, hidden: torch.Tensor, weight: torch.Tensor, teacher_logits: torch.Tensor,
                 teacher_ids: torch.Tensor, loss: Optional[torch.Tensor] = None,
@@ -146,9 +151,9 @@ class HeadDistill(Head):
         self._check_operands(hidden, weight)
         if teacher_ids.dim() != 2 or teacher_ids.shape[1] > self.top:
             raise ValueError(f"teacher_ids must be [{hidden.shape[0]}, at most {self.top}]")
-        s = stream if stream is not None else torch.cuda.current_stream()
-        loss, token_loss = self._results(hidden, loss, token_loss, s)
-        a = _args(hidden, weight, teacher_logits, teacher_ids, loss, token_loss, d_hidden, d_weight, self.temperature,
-                  self.reduction, grad_scale, self.band, wait_timeouts)
-        self._launch(a, s, "fsdp_head_distill")
+        loss, token_loss = self._results(hidden, loss, token_loss, stream)
+        a = _lib.FsdpHeadDistillArgs.from_buffer_copy(self._blank)
+        device = _fill(a, hidden, weight, teacher_logits, teacher_ids, loss, token_loss, d_hidden, d_weight, grad_scale,
+                       wait_timeouts)
+        self._launch(a, stream, device, "fsdp_head_distill")
         return loss, token_loss

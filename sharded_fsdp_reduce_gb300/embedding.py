@@ -16,41 +16,48 @@ import torch
 from . import _lib
 from .fsdp import _check, dtype_code
 from .loss import _matrix, _refuse_device, _vector
-from .workspace import Workspace, take
+from .workspace import Workspace, raw_stream, take
 
 __all__ = ["Embedding", "fsdp_embed", "fsdp_embed_grad"]
 
 
-def _sizes(tokens, rows, table, rows_name: str, table_name: str):
-    for t, name in ((rows, rows_name), (table, table_name)):
+def _matrices(*named) -> None:
+    for t, name in named:
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise ValueError(f"{name} must be a matrix")
-    if not isinstance(tokens, torch.Tensor) or not tokens.is_cuda:
-        _refuse_device(tokens, "tokens")
-    return tokens.numel(), table.shape[0], table.shape[1], table.dtype, torch.cuda.current_device()
 
 
-def _args(tokens, weight, out, scale, ignore_index) -> _lib.FsdpEmbedArgs:
-    n, V, D, dt, cur = _sizes(tokens, out, weight, "out", "weight")
-    a = _lib.FsdpEmbedArgs()
-    a.dtype = dtype_code(dt)
-    a.count, a.vocab, a.dim = n, V, D
-    a.tokens = _vector(tokens, "tokens", n, torch.int64, cur)
-    a.weight, a.ld_weight = _matrix(weight, "weight", V, D, dt, cur)
-    a.out, a.ld_out = _matrix(out, "out", n, D, dt, cur)
-    a.ignore_index, a.scale = int(ignore_index), float(scale)
+def _blank(kind, vocab: int, dim: int, dtype: torch.dtype, scale: float, ignore_index: int):
+    """A call's arguments that do not change from one to the next."""
+    a = kind()
+    a.dtype, a.vocab, a.dim = dtype_code(dtype), vocab, dim
+    a.scale, a.ignore_index = float(scale), int(ignore_index)
     return a
 
 
+def _fill(a, tokens, weight, out, dtype: torch.dtype, device: int) -> None:
+    if not isinstance(tokens, torch.Tensor):
+        _refuse_device(tokens, "tokens")
+    a.count = n = tokens.numel()
+    a.tokens = _vector(tokens, "tokens", n, torch.int64, device)
+    a.weight, a.ld_weight = _matrix(weight, "weight", a.vocab, a.dim, dtype, device)
+    a.out, a.ld_out = _matrix(out, "out", n, a.dim, dtype, device)
+
+
+def _fill_grad(a, tokens, d_out, d_weight, accumulate, dtype: torch.dtype, device: int) -> None:
+    if not isinstance(tokens, torch.Tensor):
+        _refuse_device(tokens, "tokens")
+    a.count = n = tokens.numel()
+    a.tokens = _vector(tokens, "tokens", n, torch.int64, device)
+    a.d_out, a.ld_d_out = _matrix(d_out, "d_out", n, a.dim, dtype, device)
+    a.d_weight, a.ld_d_weight = _matrix(d_weight, "d_weight", a.vocab, a.dim, dtype, device)
+    a.accumulate = 1 if accumulate else 0
+
+
 def _grad_args(tokens, d_out, d_weight, scale, ignore_index, accumulate) -> _lib.FsdpEmbedGradArgs:
-    n, V, D, dt, cur = _sizes(tokens, d_out, d_weight, "d_out", "d_weight")
-    a = _lib.FsdpEmbedGradArgs()
-    a.dtype = dtype_code(dt)
-    a.count, a.vocab, a.dim = n, V, D
-    a.tokens = _vector(tokens, "tokens", n, torch.int64, cur)
-    a.d_out, a.ld_d_out = _matrix(d_out, "d_out", n, D, dt, cur)
-    a.d_weight, a.ld_d_weight = _matrix(d_weight, "d_weight", V, D, dt, cur)
-    a.ignore_index, a.scale, a.accumulate = int(ignore_index), float(scale), int(bool(accumulate))
+    _matrices((d_out, "d_out"), (d_weight, "d_weight"))
+    a = _blank(_lib.FsdpEmbedGradArgs, *d_weight.shape, d_weight.dtype, scale, ignore_index)
+    _fill_grad(a, tokens, d_out, d_weight, accumulate, d_weight.dtype, torch.cuda.current_device())
     return a
 
 
@@ -66,7 +73,9 @@ def fsdp_embed(tokens: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, sc
 
     tokens int64 (any shape, contiguous; T of them), weight [V, D] and out
     [T, D] of its dtype (rows contiguous, any stride and alignment)."""
-    a = _args(tokens, weight, out, scale, ignore_index)
+    _matrices((weight, "weight"), (out, "out"))
+    a = _blank(_lib.FsdpEmbedArgs, *weight.shape, weight.dtype, scale, ignore_index)
+    _fill(a, tokens, weight, out, weight.dtype, torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
     _check(_lib.load().fsdp_embed(ctypes.byref(a), s.cuda_stream), "fsdp_embed")
 
@@ -100,31 +109,34 @@ class Embedding:
         self.vocab, self.dim, self.dtype = int(vocab), int(dim), dtype
         self.max_tokens, self.scale, self.ignore_index = int(max_tokens), float(scale), int(ignore_index)
         self.device = torch.device(device)
-        a = _lib.FsdpEmbedGradArgs()
-        a.dtype = dtype_code(dtype)
-        a.count, a.vocab, a.dim, a.scale = self.max_tokens, self.vocab, self.dim, self.scale
+        self._lookup = _blank(_lib.FsdpEmbedArgs, self.vocab, self.dim, dtype, self.scale, self.ignore_index)
+        self._grad = _blank(_lib.FsdpEmbedGradArgs, self.vocab, self.dim, dtype, self.scale, self.ignore_index)
+        a = _lib.FsdpEmbedGradArgs.from_buffer_copy(self._grad)
+        a.count = self.max_tokens
         step = 1 << 56  # (addresses are not read)
         a.tokens, a.d_out, a.d_weight = step, 2 * step, 3 * step
         a.ld_d_out = a.ld_d_weight = self.dim
         need = _workspace_bytes(a)  # checks the sizes too
         self._ws = Workspace(need, self.device) if grad else None
+        self._ws_at, self._ws_bytes = (self._ws.buf.data_ptr(), need) if grad else (0, 0)
 
     def _check(self, tokens, table, name: str) -> None:
         if not isinstance(tokens, torch.Tensor) or tokens.numel() > self.max_tokens:
             raise ValueError(f"tokens must hold at most {self.max_tokens}")
-        if not isinstance(table, torch.Tensor) or table.dtype != self.dtype or \
-                tuple(table.shape) != (self.vocab, self.dim):
+        if not isinstance(table, torch.Tensor) or table.dtype != self.dtype or table.shape != (self.vocab, self.dim):
             raise ValueError(f"{name} must be [{self.vocab}, {self.dim}] of {self.dtype}")
 
     def forward(self, tokens: torch.Tensor, weight: torch.Tensor, out: Optional[torch.Tensor] = None,
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """scale * weight[tokens], [T, dim]: written to out, or to a new tensor."""
         self._check(tokens, weight, "weight")
-        s = stream if stream is not None else torch.cuda.current_stream()
+        device = torch.cuda.current_device()
         if out is None:
-            with torch.cuda.stream(s):  # a new result belongs to the call's stream
+            with torch.cuda.stream(stream):  # a new result belongs to the call's stream
                 out = torch.empty(tokens.numel(), self.dim, dtype=self.dtype, device=weight.device)
-        fsdp_embed(tokens, weight, out, self.scale, self.ignore_index, s)
+        a = _lib.FsdpEmbedArgs.from_buffer_copy(self._lookup)
+        _fill(a, tokens, weight, out, self.dtype, device)
+        _check(_lib.load().fsdp_embed(ctypes.byref(a), raw_stream(stream, device)), "fsdp_embed")
         return out
 
     def backward(self, tokens: torch.Tensor, d_out: torch.Tensor, d_weight: torch.Tensor, accumulate: bool = False,
@@ -135,8 +147,9 @@ class Embedding:
         self._check(tokens, d_weight, "d_weight")
         if self._ws is None:
             raise ValueError("this Embedding was made without gradients (grad=False)")
-        a = _grad_args(tokens, d_out, d_weight, self.scale, self.ignore_index, accumulate)
-        s = self._ws.on(stream)
-        _check(_lib.load().fsdp_embed_grad(ctypes.byref(a), self._ws.buf.data_ptr(), self._ws.buf.numel(),
-                                           s.cuda_stream), "fsdp_embed_grad")
+        device = torch.cuda.current_device()
+        a = _lib.FsdpEmbedGradArgs.from_buffer_copy(self._grad)
+        _fill_grad(a, tokens, d_out, d_weight, accumulate, self.dtype, device)
+        raw = self._ws.enter(stream, device)
+        _check(_lib.load().fsdp_embed_grad(ctypes.byref(a), self._ws_at, self._ws_bytes, raw), "fsdp_embed_grad")
         return d_weight

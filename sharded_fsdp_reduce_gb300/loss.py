@@ -94,8 +94,8 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return take(nbytes, device, alignment=1024)
 
 
-def _launch(a: _lib.FsdpHeadLossArgs, address: int, nbytes: int, stream: torch.cuda.Stream) -> int:
-    return _lib.load().fsdp_head_loss(ctypes.byref(a), address, nbytes, stream.cuda_stream)
+def _launch(a: _lib.FsdpHeadLossArgs, address: int, nbytes: int, stream: int) -> int:
+    return _lib.load().fsdp_head_loss(ctypes.byref(a), address, nbytes, stream)
 
 
 def fsdp_head_loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, loss: torch.Tensor,
@@ -113,7 +113,7 @@ def fsdp_head_loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
     s = stream if stream is not None else torch.cuda.current_stream()
     with torch.cuda.stream(s):  # taken, and given back, in that stream's order
         ws = _workspace(_workspace_bytes(a), hidden.device)
-    _check(_launch(a, ws.data_ptr(), ws.numel(), s), "fsdp_head_loss")
+    _check(_launch(a, ws.data_ptr(), ws.numel(), s.cuda_stream), "fsdp_head_loss")
 
 
 def fsdp_check_head_loss_wait(limit_cycles: int, arrive_after_cycles: int, outcomes: torch.Tensor,
@@ -151,7 +151,7 @@ class Head:
     def _bytes(self, a) -> int:
         raise NotImplementedError
 
-    def _enqueue(self, a, stream: torch.cuda.Stream) -> int:
+    def _enqueue(self, a, stream: int) -> int:
         raise NotImplementedError
 
     def _need(self, grad: bool, odd_hidden: bool, odd_weight: bool) -> int:
@@ -199,13 +199,13 @@ class Head:
                     token_loss = torch.empty(hidden.shape[0], dtype=torch.float32, device=hidden.device)
         return loss, token_loss
 
-    def _launch(self, a, stream: torch.cuda.Stream, name: str) -> None:
-        self._ws.on(stream)
-        status = self._enqueue(a, stream)
+    def _launch(self, a, stream: Optional[torch.cuda.Stream], device: int, name: str) -> None:
+        raw = self._ws.enter(stream, device)
+        status = self._enqueue(a, raw)
         if status == _lib.FSDP_ERR_INVALID_ARG and self._bytes(a) > self._ws_bytes:
             with torch.cuda.stream(stream):
                 self._grow(a)
-            status = self._enqueue(a, stream)
+            status = self._enqueue(a, raw)
         _check(status, name)
 
 
@@ -238,7 +238,7 @@ class HeadLoss(Head):
     def _bytes(self, a: _lib.FsdpHeadLossArgs) -> int:
         return _workspace_bytes(a)
 
-    def _enqueue(self, a: _lib.FsdpHeadLossArgs, stream: torch.cuda.Stream) -> int:
+    def _enqueue(self, a: _lib.FsdpHeadLossArgs, stream: int) -> int:
         return _launch(a, self._ws_at, self._ws_bytes, stream)
 
     def forward(self, hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
@@ -261,9 +261,8 @@ class HeadLoss(Head):
 
     def _run(self, hidden, weight, targets, d_hidden, d_weight, grad_scale, loss, token_loss, stream, wait_timeouts):
         self._check_operands(hidden, weight)
-        s = stream if stream is not None else torch.cuda.current_stream()
-        loss, token_loss = self._results(hidden, loss, token_loss, s)
+        loss, token_loss = self._results(hidden, loss, token_loss, stream)
         a = _args(hidden, weight, targets, loss, token_loss, d_hidden, d_weight, self.ignore_index, self.reduction,
                   grad_scale, self.band, wait_timeouts)
-        self._launch(a, s, "fsdp_head_loss")
+        self._launch(a, stream, hidden.get_device(), "fsdp_head_loss")
         return loss, token_loss

@@ -5,7 +5,7 @@ from typing import Optional
 
 import torch
 
-__all__ = ["Workspace", "take"]
+__all__ = ["Workspace", "take", "raw_stream"]
 
 
 def take(nbytes: int, device, alignment: int = 256, zeroed: bool = False) -> torch.Tensor:
@@ -16,6 +16,12 @@ def take(nbytes: int, device, alignment: int = 256, zeroed: bool = False) -> tor
         return make(nbytes, dtype=torch.uint8, device=device)
     whole = make(nbytes + alignment, dtype=torch.uint8, device=device)
     return whole.narrow(0, -whole.data_ptr() % alignment, nbytes)
+
+
+def raw_stream(stream: Optional[torch.cuda.Stream], device: int) -> int:
+    """The handle of a call's stream, by default the device's current one. (A
+    Stream object for that costs as much as a small call's whole launch.)"""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
 class Workspace:
@@ -40,6 +46,13 @@ class Workspace:
         if torch.cuda.current_device() != self._device:
             raise ValueError(f"this object's workspace is on cuda:{self._device} but the current device is "
                              f"cuda:{torch.cuda.current_device()}")
+
+    def enter(self, stream: Optional[torch.cuda.Stream], device: int) -> int:
+        """on(), for a call whose current device is known: the stream's handle."""
+        raw = raw_stream(stream, device)
+        if device != self._device or raw != self._made_on or self._in_capture:
+            return self.on(stream).cuda_stream
+        return raw
 
     def on(self, stream: Optional[torch.cuda.Stream]) -> torch.cuda.Stream:
         """The stream of a call (the current one by default), ordered after
