@@ -16,7 +16,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 template <int DT, bool VEC> __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
-    using S = Slice<DT, VEC, kLookupWords>;
+    using S = Slice<DT, VEC>;
     wait_previous();
     allow_next();
     const int64_t at = int64_t(blockIdx.x) * kWarps + threadIdx.x / 32;
@@ -62,7 +62,7 @@ template <int DT> fsdp_status launch_type(LookupArgs a, cudaStream_t s) {
     // whole words: both sides aligned, and rows of whole words
     const bool vec = aligned(a.weight, 16) && aligned(a.out, 16) && a.weight_bytes % 16 == 0 && a.out_bytes % 16 == 0 &&
                      a.dim * Dtype<DT>::kSize % 16 == 0;
-    const int64_t cols = slice_cols(kLookupWords, DT, vec);
+    const int64_t cols = vec ? Slice<DT, true>::kCols : Slice<DT, false>::kCols;
     a.slices = (a.dim + cols - 1) / cols;
     const int64_t blocks = (a.n * a.slices + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
@@ -103,7 +103,7 @@ fsdp_status check(int dtype, int64_t n, int64_t vocab, int64_t dim, const void *
 struct Plan {
     bool vec;
     int32_t passes, bits;
-    int32_t block;
+    int32_t block, words;
     int64_t blocks, slices, ld_part;
     // byte offsets into the workspace
     int64_t key[2], pos[2], tickets, part, bytes;
@@ -124,10 +124,12 @@ Plan make_plan(const fsdp_embed_grad_args &a) {
     while ((a.vocab >> bits) != 0) ++bits;
     p.passes = (bits + kMostBits - 1) / kMostBits;
     p.bits = (bits + p.passes - 1) / p.passes;
-    p.slices = ceil_div(a.dim, slice_cols(kSumWords, a.dtype, p.vec));
-    // long blocks where there are enough of them: eight for each place of the
-    // four on an SM
-    const int64_t ctas = int64_t(sm_count() > 0 ? sm_count() : 1) * 32;
+    // the slices as even as whole words of the lanes make them
+    p.slices = ceil_div(a.dim * dtype_size(a.dtype), kSliceBytes);
+    const int64_t lane_words = ceil_div(ceil_div(a.dim, p.vec ? 16 / dtype_size(a.dtype) : 1), 32);
+    p.words = static_cast<int32_t>(ceil_div(lane_words, p.slices));
+    // long blocks where there are enough of them for the four places on an SM
+    const int64_t ctas = int64_t(sm_count() > 0 ? sm_count() : 1) * 4;
     p.block = kMostBlock;
     while (p.block > kLeastBlock && ceil_div(n, p.block) * p.slices < ctas) p.block /= 2;
     p.blocks = ceil_div(n, p.block);
@@ -143,7 +145,7 @@ Plan make_plan(const fsdp_embed_grad_args &a) {
         p.key[i] = take(4 * n);
         p.pos[i] = take(4 * n);
     }
-    p.tickets = take(4 * most_blocks * ceil_div(a.dim, slice_cols(kSumWords, a.dtype, false)));  // (the shortest slices)
+    p.tickets = take(4 * most_blocks * p.slices);
     p.part = take(8 * most_blocks * p.ld_part);
     p.bytes = at;
     return p;
@@ -165,16 +167,19 @@ fsdp_status run_grad(const fsdp_embed_grad_args &a, const Plan &p, uint8_t *ws, 
     }
     o.tickets = reinterpret_cast<uint32_t *>(ws + p.tickets);
     o.n_tickets = static_cast<uint32_t>(p.blocks * p.slices);
-    if (a.count > 0 && (st = launch_sort(o, s)) != FSDP_OK) return st;
-    if (!a.accumulate) {
+    const FillArgs f{a.tokens, a.count, a.vocab, a.dim, static_cast<uint8_t *>(a.d_weight), a.ld_d_weight * size, size,
+                     a.ignore_index};
+    const bool fill = !a.accumulate, place = can_place(a.count, a.vocab);
+    if (place) {
+        st = launch_place(o, f, fill, s);
+    } else {
+        if (a.count > 0) st = launch_sort(o, s);
         // rows that no token uses, while a few SMs sort
-        FillArgs f{a.tokens, a.count, a.vocab, a.dim, static_cast<uint8_t *>(a.d_weight), a.ld_d_weight * size, size,
-                   a.ignore_index};
-        if ((st = launch_fill(f, s)) != FSDP_OK) return st;
+        if (st == FSDP_OK && fill) st = launch_fill(f, s);
     }
-    if (a.count == 0) return FSDP_OK;
+    if (st != FSDP_OK || a.count == 0) return st;
     SumArgs r;
-    const int last = (p.passes - 1) % 2;
+    const int last = place ? 0 : (p.passes - 1) % 2;
     r.key = o.key[last];
     r.pos = o.pos[last];
     r.n = o.n;
@@ -189,10 +194,10 @@ fsdp_status run_grad(const fsdp_embed_grad_args &a, const Plan &p, uint8_t *ws, 
     r.tickets = o.tickets;
     r.blocks = static_cast<uint32_t>(p.blocks);
     r.block = p.block;
+    r.words = p.words;
     r.slices = static_cast<uint32_t>(p.slices);
-    r.accumulate = a.accumulate;
     r.scale = a.scale;
-    return launch_sums(r, a.dtype, p.vec, s);
+    return launch_sums(r, a.dtype, p.vec, a.accumulate != 0, s);
 }
 
 fsdp_status check_grad(const fsdp_embed_grad_args *a) {

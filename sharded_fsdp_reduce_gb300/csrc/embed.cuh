@@ -7,18 +7,14 @@
 namespace fsdp {
 namespace embed {
 
-// A warp's slice of a row: 32 lanes times this many words of 16 bytes, or of
-// one element where rows are not 16-byte aligned.
-template <int DT, bool VEC, int WORDS> struct Slice {
+// What the lookup's warp copies of a row: 32 lanes times this many words of 16
+// bytes, or of one element where rows are not 16-byte aligned.
+template <int DT, bool VEC> struct Slice {
     static constexpr int kSize = Dtype<DT>::kSize;
     static constexpr int kElems = VEC ? 16 / kSize : 1;  // of a word
-    static constexpr int kWords = VEC ? WORDS : 4 * WORDS;  // of a lane
+    static constexpr int kWords = VEC ? 4 : 16;          // of a lane
     static constexpr int kCols = 32 * kWords * kElems;
 };
-constexpr int kLookupWords = 4, kSumWords = 2;
-
-// Columns of a warp's slice.
-inline int64_t slice_cols(int words, int dtype, bool vec) { return vec ? 512 * words / dtype_size(dtype) : 128 * words; }
 
 // kElems consecutive values as fp32, and back (rounded once).
 template <int DT, bool VEC> struct Word;
@@ -97,6 +93,7 @@ struct FillArgs {
 
 // Sorted entries whose sums are formed without parts in memory: those of a CTA's
 // warps, 4, 8 or 16 each.
+constexpr int kSliceBytes = 1024;  // of a row, for a CTA
 constexpr int kSumWarps = 8, kLeastBlock = 4 * kSumWarps, kMostBlock = 16 * kSumWarps;
 
 struct SumArgs {
@@ -111,13 +108,16 @@ struct SumArgs {
     uint32_t *tickets;  // [blocks][slices]: parts that are there of the run that crosses the block's end
     uint32_t blocks, slices;
     int32_t block;      // entries of one
-    int32_t accumulate;
+    int32_t words;      // of a lane in a slice
     float scale;
 };
 
+// Few tokens: their order in key[0] and pos[0], and (fill) zeros in one launch.
+bool can_place(int64_t n, int64_t vocab);
+fsdp_status launch_place(const SortArgs &a, const FillArgs &f, bool fill, cudaStream_t s);
 fsdp_status launch_sort(const SortArgs &a, cudaStream_t s);
 fsdp_status launch_fill(const FillArgs &a, cudaStream_t s);
-fsdp_status launch_sums(const SumArgs &a, int dtype, bool vec, cudaStream_t s);
+fsdp_status launch_sums(const SumArgs &a, int dtype, bool vec, bool add, cudaStream_t s);
 
 }  // namespace embed
 }  // namespace fsdp

@@ -28,7 +28,7 @@ namespace {
 // holds one of these.
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kItems = 8;
 constexpr uint32_t kTile = kSortThreads * kItems;  // entries of a CTA in one go
-constexpr int kMostCtas = 8;                       // of the cluster (the portable limit)
+constexpr int kMostCtas = 16;                      // of the cluster (eight are portable)
 constexpr uint32_t kDigits = 1u << kMostBits;
 static_assert(kDigits <= 2 * kSortThreads && kTile < 65536, "a thread has two digits; counts of a tile fit 16 bits");
 
@@ -101,6 +101,7 @@ __device__ __forceinline__ void load_tile(const SortArgs &a, const SortShared &s
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const uint32_t at = t.first + 32 * i;
+        t.key[i] = 0;
         if (i >= t.items || at >= end) continue;
         if (pass == 0) {
             const int64_t token = a.tokens[at];
@@ -121,17 +122,31 @@ __device__ __forceinline__ void load_tile(const SortArgs &a, const SortShared &s
 // Every entry's digit and its place among the warp's; then, per digit, the
 // warps' counts become what comes before them. Returns the counts of this
 // thread's two digits over the tile.
-__device__ __forceinline__ uint2 rank_tile(SortShared &s, SortTile &t, int shift, uint32_t digits) {
+__device__ __forceinline__ uint2 rank_tile(SortShared &s, SortTile &t, int shift, int bits) {
+    const uint32_t digits = 1u << bits;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     uint16_t *count = reinterpret_cast<uint16_t *>(s.count[warp]);
     for (uint32_t d = lane; d < (digits + 1) / 2; d += 32) s.count[warp][d] = 0;
     __syncwarp();
+    // the lanes with the same digit, of every entry
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         if (i >= t.items) break;  // (the same for all)
+        uint32_t peers = __ballot_sync(0xffffffffu, t.first + 32 * i < t.end);
+#pragma unroll
+        for (int b = 0; b < kMostBits; ++b) {
+            if (b >= bits) break;
+            const bool one = t.key[i] >> (shift + b) & 1u;
+            const uint32_t ones = __ballot_sync(0xffffffffu, one);
+            peers &= one ? ones : ~ones;
+        }
+        t.spot[i] = peers;
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        if (i >= t.items) break;
         const bool live = t.first + 32 * i < t.end;
-        const uint32_t digit = live ? (t.key[i] >> shift) & (digits - 1) : 0xffffu;
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+        const uint32_t digit = (t.key[i] >> shift) & (digits - 1), peers = t.spot[i];
         uint32_t before = 0;
         if (live) before = count[digit];
         __syncwarp();
@@ -178,7 +193,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_kernel(const __grid_cons
         uint2 total = make_uint2(0, 0);
         for (uint32_t at = begin; at < end; at += kTile) {
             load_tile<LARGE>(a, s, pass, at, min(at + kTile, end), t);
-            const uint2 x = rank_tile(s, t, shift, digits);
+            const uint2 x = rank_tile(s, t, shift, a.bits);
             total.x += x.x;
             total.y += x.y;
             if constexpr (LARGE) __syncthreads();
@@ -207,7 +222,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_kernel(const __grid_cons
             uint2 here = make_uint2(0, 0);
             if constexpr (LARGE) {
                 load_tile<LARGE>(a, s, pass, at, min(at + kTile, end), t);
-                here = rank_tile(s, t, shift, digits);
+                here = rank_tile(s, t, shift, a.bits);
                 __syncthreads();
             }
             const uint16_t *count = reinterpret_cast<const uint16_t *>(s.count[threadIdx.x / 32]);
@@ -266,6 +281,12 @@ __device__ __forceinline__ void zero_row(uint8_t *row, int64_t bytes, int size, 
     }
 }
 
+// Set a row's bit.
+__device__ __forceinline__ void mark(uint32_t *used, int64_t row) {
+    const uint32_t bit = 1u << (row % 32);
+    if (!(*static_cast<volatile uint32_t *>(used + row / 32) & bit)) atomicOr(used + row / 32, bit);
+}
+
 // A CTA per SM, each with a stretch of the table: it marks the rows that the
 // tokens use and writes zeros to the others. Follows the sort on the stream but
 // needs nothing of it, so it waits for it last: when this kernel has ended, the
@@ -283,9 +304,7 @@ __global__ void __launch_bounds__(kFillThreads, 2) fill_kernel(const __grid_cons
 #pragma unroll 8
         for (int64_t i = threadIdx.x; i < a.n; i += kFillThreads) {
             const int64_t token = a.tokens[i], at = token - row0;
-            if (at < 0 || at >= rows || token == a.ignore) continue;
-            const uint32_t bit = 1u << (at % 32);
-            if (!(*static_cast<volatile uint32_t *>(&used[at / 32]) & bit)) atomicOr(&used[at / 32], bit);
+            if (at >= 0 && at < rows && token != a.ignore) mark(used, at);
         }
         __syncthreads();
         for (int64_t r = warp; r < rows; r += kFillThreads / 32)
@@ -297,61 +316,153 @@ __global__ void __launch_bounds__(kFillThreads, 2) fill_kernel(const __grid_cons
     allow_next();
 }
 
+// ---------------------------------------------------------------- few tokens: their order by counting, and the zeros
+
+// Up to 4096 tokens below 2^20 (or none: key `vocab`) are sorted by all CTAs at
+// once: an entry's place is the number of smaller ones, a token and its position
+// in one 32-bit word, which a warp counts in shared memory. 1024 entries take
+// 3.7 us (the radix sort's waits 8), 4096 8, 8192 14 (11).
+// Warps that have no entry to place fill rows with zeros meanwhile.
+constexpr uint32_t kPlaceBits = 12, kPlaceMost = 1u << kPlaceBits;
+constexpr int64_t kPlaceVocab = int64_t(1) << (32 - kPlaceBits);
+
+__global__ void __launch_bounds__(kFillThreads, 1)
+    place_kernel(const __grid_constant__ SortArgs a, const __grid_constant__ FillArgs f, bool fill) {
+    __shared__ __align__(16) uint32_t entry[kPlaceMost];
+    __shared__ uint32_t used[kWindow / 32];
+    __shared__ uint32_t next_row;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint32_t vocab = a.vocab, each = (vocab + gridDim.x - 1) / gridDim.x;
+    const uint32_t row0 = min(blockIdx.x * each, vocab), rows = min(each, vocab - row0);  // (within a window)
+    const uint32_t padded = (a.n + 127) / 128 * 128;
+    if (fill)
+        for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kFillThreads) used[i] = 0;
+    if (threadIdx.x == 0) next_row = 0;
+    wait_previous();
+    allow_next();
+    for (uint32_t i = blockIdx.x * kFillThreads + threadIdx.x; i < a.n_tickets; i += gridDim.x * kFillThreads)
+        a.tickets[i] = 0;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < padded; i += kFillThreads) {
+        uint32_t e = 0xffffffffu;
+        if (i < a.n) {
+            const int64_t token = a.tokens[i];
+            const bool none = token == a.ignore || token < 0 || token >= vocab;
+            const uint32_t key = none ? vocab : static_cast<uint32_t>(token);
+            if (fill && key - row0 < rows) mark(used, key - row0);
+            e = key << kPlaceBits | i;
+        }
+        entry[i] = e;
+    }
+    __syncthreads();
+    for (uint32_t i = blockIdx.x + gridDim.x * warp; i < a.n; i += 2 * kFillThreads / 32 * gridDim.x) {
+        const uint32_t other = i + kFillThreads / 32 * gridDim.x;  // two entries at a time
+        const uint32_t x = entry[i], y = other < a.n ? entry[other] : 0u;
+        uint32_t below_x = 0, below_y = 0;
+        for (uint32_t j = 4 * lane; j < padded; j += 128) {
+            const uint4 e = *reinterpret_cast<const uint4 *>(entry + j);
+            below_x += (e.x < x) + (e.y < x) + (e.z < x) + (e.w < x);
+            below_y += (e.x < y) + (e.y < y) + (e.z < y) + (e.w < y);
+        }
+        below_x = __reduce_add_sync(0xffffffffu, below_x);
+        below_y = __reduce_add_sync(0xffffffffu, below_y);
+        if (lane == 0) {
+            a.key[0][below_x] = x >> kPlaceBits;
+            a.pos[0][below_x] = i;
+            if (other < a.n) {
+                a.key[0][below_y] = y >> kPlaceBits;
+                a.pos[0][below_y] = other;
+            }
+        }
+    }
+    if (!fill) return;
+    const int64_t bytes = f.dim * f.size;
+    const uint32_t batch = bytes >= 4096 ? 1 : static_cast<uint32_t>(4096 / bytes);
+    for (;;) {
+        uint32_t r = 0;
+        if (lane == 0) r = atomicAdd(&next_row, batch);
+        r = __shfl_sync(0xffffffffu, r, 0);
+        if (r >= rows) break;
+        for (const uint32_t last = min(r + batch, rows); r < last; ++r)
+            if (!(used[r / 32] >> (r % 32) & 1u)) zero_row(f.d_weight + int64_t(row0 + r) * f.row_bytes, bytes, f.size, lane);
+    }
+}
+
 // ---------------------------------------------------------------- sums
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 static_assert(kWarps == kSumWarps, "the host cuts the entries for as many warps");
-constexpr int kSlots = 4;  // rows of a warp on their way
+// Rows of a warp on their way; fewer where the rows they are added to are too.
+constexpr int slots(bool add) { return add ? 3 : 4; }
 constexpr uint32_t kAll = 0xffffffffu;
 
-// What a warp keeps in shared memory: the rows on their way, and the sum of a
-// run that began before its entries. The sum of a run that goes on after them
-// takes the place of the rows, which have come by then.
-template <int DT, bool VEC> struct WarpShared {
-    using S = Slice<DT, VEC, kSumWords>;
+// A warp's slice of a row: 1 KB, in words of a lane of 16 bytes, or of one
+// element where rows are not 16-byte aligned (then with up to 16 bytes more, as
+// whole 16-byte granules are copied).
+template <int DT, bool VEC> struct SumSlice {
+    static constexpr int kSize = Dtype<DT>::kSize;
+    static constexpr int kElems = VEC ? 16 / kSize : 1;           // of a word
+    static constexpr int kWords = kSliceBytes / 32 / kSize / kElems;  // of a lane, at most
+    static constexpr int kBytes = kSliceBytes + (VEC ? 0 : 16);
+    using Sum = float[kWords][kElems];
+};
+
+// What a warp keeps in shared memory: the rows on their way, what their runs'
+// sums are added to, and the sum of a run that began before its entries. The
+// sum of a run that goes on after them takes the place of the rows, which have
+// come by then.
+template <int DT, bool VEC, bool ADD> struct WarpShared {
+    using S = SumSlice<DT, VEC>;
+    static constexpr int kSlots = slots(ADD);
     union {
-        Word<DT, VEC> rows[kSlots][S::kWords][32];
+        uint4 rows[kSlots][S::kBytes / 16];
         float tail[S::kWords][S::kElems][32];
     };
+    uint4 there[ADD ? kSlots : 1][S::kBytes / 16];
     float head[S::kWords][S::kElems][32];
     __device__ WarpShared() {}
 };
 
-// A lane's columns of one row's sum to the gradient: times scale, and added to
-// what is there.
-template <int DT, bool VEC>
-__device__ __forceinline__ void write_row(const SumArgs &a, uint32_t key, int64_t col0,
-                                          float (&sum)[Slice<DT, VEC, kSumWords>::kWords]
-                                                      [Slice<DT, VEC, kSumWords>::kElems]) {
-    using S = Slice<DT, VEC, kSumWords>;
-    uint8_t *row = a.d_weight + int64_t(key) * a.weight_bytes;
-    if (a.accumulate) {
-        Word<DT, VEC> there[S::kWords];
+// Copy up to 16 bytes to shared memory (zeros behind them).
+__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tma::smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A warp's copy of `bytes` of a row. Aligned rows: a lane copies what it will
+// read. Others: the granules that hold them, from the last 16-byte boundary (the
+// bytes before the first element are of the same allocation) to the last byte.
+template <int DT, bool VEC> __device__ __forceinline__ void copy_row(uint4 *dst, const uint8_t *src, int bytes) {
+    const int lane = threadIdx.x % 32;
+    if constexpr (VEC) {
 #pragma unroll
-        for (int j = 0; j < S::kWords; ++j) {
-            const int64_t col = col0 + j * 32 * S::kElems;
-            if (col < a.dim) there[j].load_coherent(row, col);
-        }
-#pragma unroll
-        for (int j = 0; j < S::kWords; ++j) {
-            const int64_t col = col0 + j * 32 * S::kElems;
-            if (col >= a.dim) continue;
-            float f[S::kElems];
-            there[j].widen(f);
-#pragma unroll
-            for (int e = 0; e < S::kElems; ++e) f[e] = fmaf(sum[j][e], a.scale, f[e]);
-            Word<DT, VEC>::store(row, col, f);
+        for (int j = 0; j < SumSlice<DT, VEC>::kWords; ++j) {
+            const int at = (j * 32 + lane) * 16;
+            if (at < bytes) copy_async(dst + j * 32 + lane, src + at, 16);
         }
     } else {
+        const int shift = reinterpret_cast<uintptr_t>(src) & 15;
 #pragma unroll
-        for (int j = 0; j < S::kWords; ++j) {
-            const int64_t col = col0 + j * 32 * S::kElems;
-            if (col >= a.dim) continue;
-            float f[S::kElems];
-#pragma unroll
-            for (int e = 0; e < S::kElems; ++e) f[e] = sum[j][e] * a.scale;
-            Word<DT, VEC>::store(row, col, f);
+        for (int j = 0; j < 3; ++j) {
+            const int at = (j * 32 + lane) * 16, left = shift + bytes - at;
+            if (left > 0) copy_async(dst + j * 32 + lane, src - shift + at, left < 16 ? left : 16);
         }
+    }
+}
+
+// A lane's j-th word of a copied row.
+template <int DT, bool VEC> __device__ __forceinline__ void read_word(const uint4 *row, int shift, int j, float *f) {
+    const int lane = threadIdx.x % 32;
+    if constexpr (!VEC) {
+        f[0] = Dtype<DT>::load(reinterpret_cast<const uint8_t *>(row) + shift, j * 32 + lane);
+    } else if constexpr (DT == FSDP_F32) {
+        const float4 x = *reinterpret_cast<const float4 *>(row + j * 32 + lane);
+        f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
+    } else {
+        unpack8<DT>(row[j * 32 + lane], f);
     }
 }
 
@@ -378,58 +489,43 @@ template <int N> __device__ __forceinline__ void add_floats(const float *p, floa
     }
 }
 
-__device__ __forceinline__ uint32_t key_at(const SumArgs &a, int64_t at) { return a.key[at]; }
-
-// The block that a run which block b's first entry continues begins in.
-__device__ __forceinline__ uint32_t first_block(const SumArgs &a, uint32_t b, uint32_t key) {
-    uint32_t hi = b - 1;  // (its last entry is of the run)
-    if (hi == 0 || key_at(a, int64_t(hi) * a.block - 1) != key) return hi;
-    uint32_t lo = 0;
-    --hi;
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (key_at(a, (int64_t(mid) + 1) * a.block - 1) == key)
-            hi = mid;
-        else
-            lo = mid + 1;
+// How many blocks the run of block b's first entry goes back over (its last
+// one: on after), beside the next one. A warp looks at 32 blocks at a time.
+__device__ __forceinline__ uint32_t more_blocks(const SumArgs &a, uint32_t b, uint32_t key, bool back) {
+    const int lane = threadIdx.x % 32;
+    uint32_t more = 0;
+    for (;;) {
+        // the last entry of the block before, the first one of the block after
+        const int64_t at = back ? (int64_t(b) - 1 - more - lane) * a.block - 1 : (int64_t(b) + 2 + more + lane) * a.block;
+        const uint32_t same = __ballot_sync(kAll, at >= 0 && at < a.n && a.key[at] == key);
+        if (same != kAll) return more + __ffs(~same) - 1;
+        more += 32;
     }
-    return lo;
 }
 
-// The last block that begins with a run which goes on after block b.
-__device__ __forceinline__ uint32_t last_block(const SumArgs &a, uint32_t b, uint32_t key) {
-    uint32_t lo = b + 1, hi = a.blocks - 1;
-    if (lo == hi || key_at(a, (int64_t(lo) + 1) * a.block) != key) return lo;
-    ++lo;
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo + 1) / 2;
-        if (key_at(a, int64_t(mid) * a.block) == key)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
-}
+// The columns of a CTA's slice.
+struct Columns {
+    int64_t first;
+    int count, words;  // words of a lane (the same for all slices)
+};
 
 // This run's part of block b to memory; true, with the whole run's sum, for
 // the warp that brings its last part.
 template <int DT, bool VEC>
-__device__ __forceinline__ bool join_parts(const SumArgs &a, uint32_t b, uint32_t slice, int64_t col0, uint32_t key, bool head,
-                                           bool tail,
-                                           float (&sum)[Slice<DT, VEC, kSumWords>::kWords]
-                                                       [Slice<DT, VEC, kSumWords>::kElems]) {
-    using S = Slice<DT, VEC, kSumWords>;
-    float *mine = a.part + (int64_t(b) * 2 + (head ? 0 : 1)) * a.ld_part;
+__device__ __forceinline__ bool join_parts(const SumArgs &a, uint32_t b, uint32_t slice, const Columns &c, bool head,
+                                           uint32_t from, uint32_t to, typename SumSlice<DT, VEC>::Sum &sum) {
+    using S = SumSlice<DT, VEC>;
+    const int lane = threadIdx.x % 32;
+    float *mine = a.part + (int64_t(b) * 2 + (head ? 0 : 1)) * a.ld_part + c.first;
 #pragma unroll
     for (int j = 0; j < S::kWords; ++j) {
-        const int64_t col = col0 + j * 32 * S::kElems;
-        if (col < a.dim) store_floats<S::kElems>(mine + col, sum[j]);
+        const int col = (j * 32 + lane) * S::kElems;
+        if (col < c.count) store_floats<S::kElems>(mine + col, sum[j]);
     }
-    const uint32_t from = head ? first_block(a, b, key) : b, to = tail ? last_block(a, b, key) : b;
     __threadfence();
     __syncwarp();
     uint32_t there = 0;
-    if (threadIdx.x % 32 == 0) there = atomicAdd(a.tickets + uint64_t(from) * a.slices + slice, 1u);
+    if (lane == 0) there = atomicAdd(a.tickets + uint64_t(from) * a.slices + slice, 1u);
     if (__shfl_sync(kAll, there, 0) != to - from) return false;
     __threadfence();
 #pragma unroll
@@ -438,23 +534,14 @@ __device__ __forceinline__ bool join_parts(const SumArgs &a, uint32_t b, uint32_
         for (int e = 0; e < S::kElems; ++e) sum[j][e] = 0.0f;
 #pragma unroll 4
     for (uint32_t i = from; i <= to; ++i) {
-        const float *part = a.part + (int64_t(i) * 2 + (i == from ? 1 : 0)) * a.ld_part;
+        const float *part = a.part + (int64_t(i) * 2 + (i == from ? 1 : 0)) * a.ld_part + c.first;
 #pragma unroll
         for (int j = 0; j < S::kWords; ++j) {
-            const int64_t col = col0 + j * 32 * S::kElems;
-            if (col < a.dim) add_floats<S::kElems>(part + col, sum[j]);
+            const int col = (j * 32 + lane) * S::kElems;
+            if (col < c.count) add_floats<S::kElems>(part + col, sum[j]);
         }
     }
     return true;
-}
-
-// Copy 16 bytes of a row to shared memory, for the thread that asks alone.
-__device__ __forceinline__ void copy_async(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tma::smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // A block of sorted entries, for one slice of the columns; each warp has 4 to 16
@@ -465,15 +552,23 @@ template <int N> __device__ __forceinline__ void copy_wait() {
 // run from before the block) adds them up in order. A run that crosses the
 // block's first or last entry leaves its part in memory; the warp that brings
 // the last part of it adds them up, again in order.
-template <int DT, bool VEC> __global__ void __launch_bounds__(kThreads, VEC ? 4 : 3) sum_kernel(const __grid_constant__ SumArgs a) {
-    using S = Slice<DT, VEC, kSumWords>;
+template <int DT, bool VEC, bool ADD>
+__global__ void __launch_bounds__(kThreads, ADD ? 3 : 4) sum_kernel(const __grid_constant__ SumArgs a) {
+    using S = SumSlice<DT, VEC>;
+    using Shared = WarpShared<DT, VEC, ADD>;
+    constexpr int kSlots = slots(ADD);
     extern __shared__ __align__(16) uint8_t raw[];
-    WarpShared<DT, VEC> *shared = reinterpret_cast<WarpShared<DT, VEC> *>(raw);
-    __shared__ bool opens[kWarps], through[kWarps];  // began before the warp's entries; and goes on after them
+    Shared *shared = reinterpret_cast<Shared *>(raw);
+    __shared__ bool through[kWarps];    // a run from before the warp's entries goes on after them
+    __shared__ uint32_t back, ahead;    // blocks that runs from before and after the block go over, beside the next one
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, each = a.block / kWarps;
     const uint32_t slice = blockIdx.x % a.slices, b = blockIdx.x / a.slices;
-    const int64_t col0 = int64_t(slice) * S::kCols + lane * S::kElems;
-    WarpShared<DT, VEC> &mine = shared[warp];
+    Columns c;
+    c.words = a.words;
+    c.first = int64_t(slice) * 32 * c.words * S::kElems;
+    c.count = static_cast<int>(min(int64_t(32 * c.words * S::kElems), a.dim - c.first));
+    const int64_t first_byte = c.first * S::kSize;
+    Shared &mine = shared[warp];
     wait_previous();
     allow_next();
     // the warp's entries in its lanes, and the ones before and after them
@@ -486,66 +581,80 @@ template <int DT, bool VEC> __global__ void __launch_bounds__(kThreads, VEC ? 4 
     const uint32_t ends = __ballot_sync(kAll, lane < count && next != key);  // an entry that is its run's last
     const bool open = count > 0 && before == __shfl_sync(kAll, key, 0);
     const bool goes_on = count > 0 && !(ends >> (count - 1) & 1u);  // (then count == each)
-    if (lane == 0) {
-        opens[warp] = open;
-        through[warp] = open && ends == 0;
-    }
-    auto issue = [&](int i) {  // row i to its slot
+    if (lane == 0) through[warp] = open && ends == 0;
+    auto row_of = [&](int i) { return a.d_out + int64_t(__shfl_sync(kAll, pos, i)) * a.out_bytes + first_byte; };
+    auto to_of = [&](int i) { return a.d_weight + int64_t(__shfl_sync(kAll, key, i)) * a.weight_bytes + first_byte; };
+    auto shift_of = [](const uint8_t *p) { return VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15); };
+    auto issue = [&](int i) {  // row i to its slot, and the row that its run's sum is added to
         if (i < count) {
-            const uint8_t *row = a.d_out + int64_t(__shfl_sync(kAll, pos, i)) * a.out_bytes;
-#pragma unroll
-            for (int j = 0; j < S::kWords; ++j) {
-                const int64_t col = col0 + j * 32 * S::kElems;
-                if (col < a.dim) copy_async(&mine.rows[i % kSlots][j][lane], row + col * S::kSize);
+            copy_row<DT, VEC>(mine.rows[i % kSlots], row_of(i), c.count * S::kSize);
+            if constexpr (ADD) {
+                if (ends >> i & 1u) copy_row<DT, VEC>(mine.there[i % kSlots], to_of(i), c.count * S::kSize);
             }
         }
         copy_commit();
     };
-    if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) issue(i);
+    for (int i = 0; i < kSlots; ++i) issue(i);
+    // (while the rows are on their way)
+    if (warp == 0 && open) {
+        const uint32_t n = more_blocks(a, b, __shfl_sync(kAll, key, 0), true);
+        if (lane == 0) back = n;
     }
-    float sum[S::kWords][S::kElems];
-    bool fresh = true, first = true;
-#pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-        if constexpr (VEC) {
-            copy_wait<kSlots - 1>();
-        } else if (i % kSlots == 0) {  // elements of any alignment: four rows at once
-            Word<DT, VEC> w[kSlots][S::kWords];
+    if (warp == kWarps - 1 && goes_on) {
+        const uint32_t n = more_blocks(a, b, __shfl_sync(kAll, key, each), false);
+        if (lane == 0) ahead = n;
+    }
+    typename S::Sum sum;
+    auto clear = [&] {
 #pragma unroll
-            for (int u = 0; u < kSlots; ++u) {
-                const uint8_t *row = a.d_out + int64_t(__shfl_sync(kAll, pos, min(i + u, count - 1))) * a.out_bytes;
+        for (int j = 0; j < S::kWords; ++j)
 #pragma unroll
-                for (int j = 0; j < S::kWords; ++j) {
-                    const int64_t col = col0 + j * 32 * S::kElems;
-                    if (col < a.dim) w[u][j].load(row, col);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kSlots; ++u)
-#pragma unroll
-                for (int j = 0; j < S::kWords; ++j) mine.rows[u][j][lane] = w[u][j];
-        }
+            for (int e = 0; e < S::kElems; ++e) sum[j][e] = 0.0f;
+    };
+    // a lane's columns of a row's sum to the gradient: times scale, and added to
+    // what is there, if `there` is not NULL
+    auto write_row = [&](uint8_t *to, const uint4 *there) {
 #pragma unroll
         for (int j = 0; j < S::kWords; ++j) {
+            const int col = (j * 32 + lane) * S::kElems;
+            if (col >= c.count) continue;
             float f[S::kElems];
-            mine.rows[i % kSlots][j][lane].widen(f);
+            if constexpr (ADD) read_word<DT, VEC>(there, shift_of(to), j, f);
 #pragma unroll
-            for (int e = 0; e < S::kElems; ++e) sum[j][e] = fresh ? f[e] : sum[j][e] + f[e];
+            for (int e = 0; e < S::kElems; ++e) f[e] = ADD ? fmaf(sum[j][e], a.scale, f[e]) : sum[j][e] * a.scale;
+            Word<DT, VEC>::store(to, col, f);
         }
-        if constexpr (VEC) issue(i + kSlots);
-        fresh = ends >> i & 1u;
-        if (!fresh) continue;
-        if (first && open) {
+    };
+    clear();
+    bool first = true;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+        copy_wait<kSlots - 1>();
+        if constexpr (!VEC) __syncwarp();  // (other lanes' granules)
+        const int shift = VEC ? 0 : shift_of(row_of(i));
 #pragma unroll
-            for (int j = 0; j < S::kWords; ++j)
+        for (int j = 0; j < S::kWords; ++j) {
+            if (j >= c.words) break;
+            float f[S::kElems];
+            read_word<DT, VEC>(mine.rows[i % kSlots], shift, j, f);
 #pragma unroll
-                for (int e = 0; e < S::kElems; ++e) mine.head[j][e][lane] = sum[j][e];
-        } else {
-            write_row<DT, VEC>(a, __shfl_sync(kAll, key, i), col0, sum);
+            for (int e = 0; e < S::kElems; ++e) sum[j][e] += f[e];
         }
-        first = false;
+        if (ends >> i & 1u) {
+            if (first && open) {
+#pragma unroll
+                for (int j = 0; j < S::kWords; ++j)
+#pragma unroll
+                    for (int e = 0; e < S::kElems; ++e) mine.head[j][e][lane] = sum[j][e];
+            } else {
+                write_row(to_of(i), mine.there[ADD ? i % kSlots : 0]);
+            }
+            first = false;
+            clear();
+        }
+        if constexpr (!VEC) __syncwarp();
+        issue(i + kSlots);
     }
     __syncwarp();  // (all lanes' rows have come and been read)
     if (goes_on) {
@@ -578,32 +687,48 @@ template <int DT, bool VEC> __global__ void __launch_bounds__(kThreads, VEC ? 4 
                 for (int e = 0; e < S::kElems; ++e) sum[j][e] += shared[other].head[j][e][lane];
             goes = through[other];
         }
-        const uint32_t k = __shfl_sync(kAll, key, which == 0 ? 0 : each - 1);
-        if ((which == 0 || goes) && !join_parts<DT, VEC>(a, b, slice, col0, k, which == 0, goes, sum)) continue;
-        write_row<DT, VEC>(a, k, col0, sum);
+        if (which == 0 || goes) {
+            const uint32_t from = which == 0 ? b - 1 - back : b, to = goes ? b + 1 + ahead : b;
+            if (!join_parts<DT, VEC>(a, b, slice, c, which == 0, from, to, sum)) continue;
+        }
+        uint8_t *to = to_of(which == 0 ? 0 : each - 1);
+        if constexpr (ADD) {
+            __syncwarp();
+            copy_row<DT, VEC>(mine.there[0], to, c.count * S::kSize);
+            copy_commit();
+            copy_wait<0>();
+            __syncwarp();
+        }
+        write_row(to, mine.there[0]);
     }
 }
 
-template <int DT, bool VEC> fsdp_status launch_type(const SumArgs &a, cudaStream_t s) {
-    constexpr size_t kShared = kWarps * sizeof(WarpShared<DT, VEC>);
+template <int DT, bool VEC, bool ADD> fsdp_status launch_type(const SumArgs &a, cudaStream_t s) {
+    constexpr size_t kShared = kWarps * sizeof(WarpShared<DT, VEC, ADD>);
     static PerDeviceOnce once;
     const int dev = current_device();
     if (!once.is_done(dev)) {
-        const cudaError_t e = cudaFuncSetAttribute(sum_kernel<DT, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(sum_kernel<DT, VEC, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(kShared));
         if (e != cudaSuccess) return cuda_status(e);
         once.mark(dev);
     }
     // (the blocks times the slices are below 2^31: a workspace of that many tickets)
-    return launch_chained(sum_kernel<DT, VEC>, a.blocks * a.slices, kThreads, kShared, s, a);
+    return launch_chained(sum_kernel<DT, VEC, ADD>, a.blocks * a.slices, kThreads, kShared, s, a);
+}
+
+template <int DT> fsdp_status launch_form(const SumArgs &a, bool vec, bool add, cudaStream_t s) {
+    if (vec) return add ? launch_type<DT, true, true>(a, s) : launch_type<DT, true, false>(a, s);
+    return add ? launch_type<DT, false, true>(a, s) : launch_type<DT, false, false>(a, s);
 }
 
 template <bool LARGE> fsdp_status launch_sort_kernel(const SortArgs &a, unsigned ctas, cudaStream_t s) {
     static PerDeviceOnce once;
     const int dev = current_device();
     if (!once.is_done(dev)) {
-        const cudaError_t e = cudaFuncSetAttribute(sort_kernel<LARGE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(sizeof(SortShared)));
+        cudaError_t e = cudaFuncSetAttribute(sort_kernel<LARGE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(sizeof(SortShared)));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(sort_kernel<LARGE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return cuda_status(e);
         once.mark(dev);
     }
@@ -626,10 +751,23 @@ template <bool LARGE> fsdp_status launch_sort_kernel(const SortArgs &a, unsigned
 }  // namespace
 
 fsdp_status launch_sort(const SortArgs &a, cudaStream_t s) {
-    // two entries a thread up to eight CTAs
+    // two entries a thread up to eight CTAs; sixteen where those do not hold them
     unsigned ctas = 1;
-    while (ctas < kMostCtas && ctas * 2 * kSortThreads < a.n) ctas *= 2;
+    while (ctas < 8 && ctas * 2 * kSortThreads < a.n) ctas *= 2;
+    if (a.n > ctas * kTile) ctas = kMostCtas;
     return a.n > kMostCtas * kTile ? launch_sort_kernel<true>(a, ctas, s) : launch_sort_kernel<false>(a, ctas, s);
+}
+
+bool can_place(int64_t n, int64_t vocab) { return n > 0 && n <= kPlaceMost && vocab < kPlaceVocab; }
+
+fsdp_status launch_place(const SortArgs &a, const FillArgs &f, bool fill, cudaStream_t s) {
+    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
+    const int64_t rows = fill ? (f.vocab + 31) / 32 : 0, entries = (int64_t(a.n) + 1) / 2;
+    int64_t grid = rows > entries ? rows : entries;
+    grid = grid < sms ? grid : sms;
+    const int64_t windows = (f.vocab + kWindow - 1) / kWindow;  // (a device of few SMs)
+    grid = fill && grid < windows ? windows : grid;
+    return launch_chained(place_kernel, static_cast<unsigned>(grid), kFillThreads, 0, s, a, f, fill);
 }
 
 fsdp_status launch_fill(const FillArgs &a, cudaStream_t s) {
@@ -644,11 +782,11 @@ fsdp_status launch_fill(const FillArgs &a, cudaStream_t s) {
     return launch_chained(fill_kernel, static_cast<unsigned>(sms < most ? sms : most), kFillThreads, kFillShared, s, a);
 }
 
-fsdp_status launch_sums(const SumArgs &a, int dtype, bool vec, cudaStream_t s) {
+fsdp_status launch_sums(const SumArgs &a, int dtype, bool vec, bool add, cudaStream_t s) {
     switch (dtype) {
-        case FSDP_BF16: return vec ? launch_type<FSDP_BF16, true>(a, s) : launch_type<FSDP_BF16, false>(a, s);
-        case FSDP_F16: return vec ? launch_type<FSDP_F16, true>(a, s) : launch_type<FSDP_F16, false>(a, s);
-        default: return vec ? launch_type<FSDP_F32, true>(a, s) : launch_type<FSDP_F32, false>(a, s);
+        case FSDP_BF16: return launch_form<FSDP_BF16>(a, vec, add, s);
+        case FSDP_F16: return launch_form<FSDP_F16>(a, vec, add, s);
+        default: return launch_form<FSDP_F32>(a, vec, add, s);
     }
 }
 
