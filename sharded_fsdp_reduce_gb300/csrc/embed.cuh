@@ -82,17 +82,6 @@ struct SortArgs {
     uint32_t n_tickets;
 };
 
-struct FillArgs {
-    const int64_t *tokens;
-    int64_t n, vocab, dim;
-    uint8_t *d_weight;
-    int64_t row_bytes;  // from one row to the next
-    int32_t size;
-    int64_t ignore;
-};
-
-// Sorted entries whose sums are formed without parts in memory: those of a CTA's
-// warps, 4, 8 or 16 each.
 constexpr int kSliceBytes = 1024;  // of a row, for a CTA
 constexpr int kSumWarps = 8, kLeastBlock = 4 * kSumWarps, kMostBlock = 16 * kSumWarps;
 
@@ -105,18 +94,24 @@ struct SumArgs {
     int64_t out_bytes, weight_bytes;
     float *part;        // [blocks][2][ld_part]: sums of runs that cross a block's first or last entry
     int64_t ld_part;
-    uint32_t *tickets;  // [blocks][slices]: parts that are there of the run that crosses the block's end
+    // [3][blocks][slices]: the parts that are there of the first group of a run
+    // that begins in the block, its groups, the parts of a group that begins there
+    uint32_t *tickets;
     uint32_t blocks, slices;
     int32_t block;      // entries of one
     int32_t words;      // of a lane in a slice
+    // zeros for the rows that no token uses, by this many CTAs more
+    uint32_t fill_ctas;
+    const int64_t *tokens;
+    int64_t ignore;
+    int32_t size;       // of an element
     float scale;
 };
 
-// Few tokens: their order in key[0] and pos[0], and (fill) zeros in one launch.
+// Few tokens: their order in key[0] and pos[0].
 bool can_place(int64_t n, int64_t vocab);
-fsdp_status launch_place(const SortArgs &a, const FillArgs &f, bool fill, cudaStream_t s);
+fsdp_status launch_place(const SortArgs &a, cudaStream_t s);
 fsdp_status launch_sort(const SortArgs &a, cudaStream_t s);
-fsdp_status launch_fill(const FillArgs &a, cudaStream_t s);
 fsdp_status launch_sums(const SumArgs &a, int dtype, bool vec, bool add, cudaStream_t s);
 
 }  // namespace embed

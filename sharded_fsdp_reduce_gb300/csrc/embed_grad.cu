@@ -37,7 +37,9 @@ struct SortShared {
     uint2 total[kDigits / 2];                 // of two digits over the CTA (its peers read them)
     uint32_t base[kDigits];                   // where its next entry with a digit goes
     uint32_t sums[kSortWarps];
-    uint2 entry[kTile];                       // {key, position} between passes, of few entries
+    uint32_t local[kDigits];                  // where the tile's entries with a digit are in `staged`
+    uint2 staged[kTile];                      // the tile's entries {key, position} by digit
+    uint2 entry[kTile];                       // the CTA's entries between passes, of few entries
 };
 
 __device__ __forceinline__ uint2 load_peer(const uint2 *p, uint32_t rank) {
@@ -77,6 +79,7 @@ __device__ __forceinline__ uint32_t before_all(uint32_t x, uint32_t *sums) {
         if (lane >= o) all += y;
     }
     const uint32_t warps_before = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
+    __syncthreads();
     return sum - x + (warp > 0 ? warps_before : 0u);
 }
 
@@ -157,18 +160,21 @@ __device__ __forceinline__ uint2 rank_tile(SortShared &s, SortTile &t, int shift
     __syncthreads();
     uint32_t sum = 0;  // two counts in one word: neither passes 16 bits
     if (2 * threadIdx.x < digits) {
+        uint32_t x[kSortWarps];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) x[w] = s.count[w][threadIdx.x];
 #pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t x = s.count[w][threadIdx.x];
             s.count[w][threadIdx.x] = sum;
-            sum += x;
+            sum += x[w];
         }
     }
     return make_uint2(sum & 0xffffu, sum >> 16);
 }
 
 // A stable radix sort by digits of up to 10 bits. Each CTA has a stretch of the
-// entries; the CTAs' counts of every digit tell where its entries go. Entries
+// entries; the CTAs' counts of every digit tell where its entries go, which it
+// puts in that order first, so that neighbours go out together. Entries
 // that are no token have the key `vocab` and come last. Up to eight tiles of
 // entries stay in the cluster's shared memory until the last pass. Bound by
 // latency (two passes: 1021 tokens 8 us, 8192 11, 32768 22; through memory and
@@ -202,14 +208,18 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_kernel(const __grid_cons
         tc::cluster_sync();  // (and everyone has its entries in registers)
         uint2 all = make_uint2(0, 0), before = make_uint2(0, 0);
         if (2 * threadIdx.x < digits) {
+            for (uint32_t c0 = 0; c0 < ctas; c0 += 4) {
+                uint2 x[4];  // (together: a peer's memory is far)
 #pragma unroll
-            for (uint32_t c = 0; c < kMostCtas; ++c) {
-                if (c >= ctas) break;
-                const uint2 x = load_peer(&s.total[threadIdx.x], c);
-                all.x += x.x;
-                all.y += x.y;
-                before.x += c < rank ? x.x : 0u;
-                before.y += c < rank ? x.y : 0u;
+                for (uint32_t u = 0; u < 4; ++u) x[u] = load_peer(&s.total[threadIdx.x], min(c0 + u, ctas - 1));
+#pragma unroll
+                for (uint32_t u = 0; u < 4; ++u) {
+                    const uint32_t c = c0 + u;
+                    all.x += c < ctas ? x[u].x : 0u;
+                    all.y += c < ctas ? x[u].y : 0u;
+                    before.x += c < rank ? x[u].x : 0u;
+                    before.y += c < rank ? x[u].y : 0u;
+                }
             }
         }
         const uint32_t start = before_all(all.x + all.y, s.sums);
@@ -217,25 +227,36 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_kernel(const __grid_cons
             s.base[2 * threadIdx.x] = start + before.x;
             s.base[2 * threadIdx.x + 1] = start + all.x + before.y;
         }
-        __syncthreads();
         for (uint32_t at = begin; at < end; at += kTile) {
-            uint2 here = make_uint2(0, 0);
+            uint2 here = total;
             if constexpr (LARGE) {
                 load_tile<LARGE>(a, s, pass, at, min(at + kTile, end), t);
                 here = rank_tile(s, t, shift, a.bits);
-                __syncthreads();
             }
+            const uint32_t local = before_all(here.x + here.y, s.sums);
+            if (2 * threadIdx.x < digits) {
+                s.local[2 * threadIdx.x] = local;
+                s.local[2 * threadIdx.x + 1] = local + here.x;
+            }
+            __syncthreads();
             const uint16_t *count = reinterpret_cast<const uint16_t *>(s.count[threadIdx.x / 32]);
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
                 if (i >= t.items || t.first + 32 * i >= t.end) continue;
                 const uint32_t digit = t.spot[i] >> 16;
-                const uint32_t to = s.base[digit] + count[digit] + (t.spot[i] & 0xffffu);
+                s.staged[s.local[digit] + count[digit] + (t.spot[i] & 0xffffu)] = make_uint2(t.key[i], t.pos[i]);
+            }
+            __syncthreads();
+            const uint32_t entries = min(kTile, end - at);
+#pragma unroll 2
+            for (uint32_t i = threadIdx.x; i < entries; i += kSortThreads) {
+                const uint2 e = s.staged[i];
+                const uint32_t digit = (e.x >> shift) & (digits - 1), to = s.base[digit] + i - s.local[digit];
                 if (LARGE || last) {
-                    a.key[pass % 2][to] = t.key[i];
-                    a.pos[pass % 2][to] = t.pos[i];
+                    a.key[pass % 2][to] = e.x;
+                    a.pos[pass % 2][to] = e.y;
                 } else {
-                    store_peer(&s.entry[to & (each - 1)], to >> each_log, make_uint2(t.key[i], t.pos[i]));
+                    store_peer(&s.entry[to & (each - 1)], to >> each_log, e);
                 }
             }
             if constexpr (LARGE) {
@@ -252,14 +273,66 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_kernel(const __grid_cons
     }
 }
 
+// ---------------------------------------------------------------- few tokens: their order by counting
+
+// Up to 4096 tokens below 2^20 (or none: key `vocab`) are sorted by all CTAs at
+// once: an entry's place is the number of smaller ones, a token and its position
+// in one 32-bit word, which a warp counts in shared memory. 1024 entries take
+// 3.7 us (the radix sort's waits 8), 4096 8, 8192 14 (11).
+constexpr uint32_t kPlaceBits = 12, kPlaceMost = 1u << kPlaceBits;
+static_assert(kPlaceMost * sizeof(uint32_t) <= 116 << 10, "the entries fit");
+constexpr int64_t kPlaceVocab = int64_t(1) << (32 - kPlaceBits);
+constexpr int kPlaceThreads = 1024;
+// More than half of an SM's shared memory, so that no SM gets two CTAs while the
+// kernel before is still on others (4096 tokens: 14 us in all against 17).
+constexpr int kPlaceShared = 116 << 10;
+
+__global__ void __launch_bounds__(kPlaceThreads, 1) place_kernel(const __grid_constant__ SortArgs a) {
+    extern __shared__ __align__(16) uint32_t entry[];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint32_t padded = (a.n + 127) / 128 * 128;
+    wait_previous();
+    allow_next();
+    for (uint32_t i = blockIdx.x * kPlaceThreads + threadIdx.x; i < a.n_tickets; i += gridDim.x * kPlaceThreads)
+        a.tickets[i] = 0;
+    for (uint32_t i = threadIdx.x; i < padded; i += kPlaceThreads) {
+        uint32_t e = 0xffffffffu;
+        if (i < a.n) {
+            const int64_t token = a.tokens[i];
+            const bool none = token == a.ignore || token < 0 || token >= a.vocab;
+            e = (none ? a.vocab : static_cast<uint32_t>(token)) << kPlaceBits | i;
+        }
+        entry[i] = e;
+    }
+    __syncthreads();
+    for (uint32_t i = blockIdx.x + gridDim.x * warp; i < a.n; i += 2 * kPlaceThreads / 32 * gridDim.x) {
+        const uint32_t other = i + kPlaceThreads / 32 * gridDim.x;  // two entries at a time
+        const uint32_t x = entry[i], y = other < a.n ? entry[other] : 0u;
+        uint32_t below_x = 0, below_y = 0;
+        for (uint32_t j = 4 * lane; j < padded; j += 128) {
+            const uint4 e = *reinterpret_cast<const uint4 *>(entry + j);
+            below_x += (e.x < x) + (e.y < x) + (e.z < x) + (e.w < x);
+            below_y += (e.x < y) + (e.y < y) + (e.z < y) + (e.w < y);
+        }
+        below_x = __reduce_add_sync(0xffffffffu, below_x);
+        below_y = __reduce_add_sync(0xffffffffu, below_y);
+        if (lane == 0) {
+            a.key[0][below_x] = x >> kPlaceBits;
+            a.pos[0][below_x] = i;
+            if (other < a.n) {
+                a.key[0][below_y] = y >> kPlaceBits;
+                a.pos[0][below_y] = other;
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- rows that no token uses
 
-constexpr int kFillThreads = 1024;
-constexpr int64_t kWindow = 16384;  // rows whose use is known at a time
-// More than half of an SM's shared memory, and less than the sort leaves: an SM
-// has room for one CTA of this kernel, beside the sort's or not. (Two on one
-// took twice as long: 32768 tokens, 128000 x 8192 bf16, 600 us in all against 490.)
-constexpr int kFillShared = 120 << 10;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+static_assert(kWarps == kSumWarps, "the host cuts the entries for as many warps");
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int64_t kWindow = 65536;  // rows whose use is known at a time, a bit each
 
 __device__ __forceinline__ void zero_row(uint8_t *row, int64_t bytes, int size, int lane) {
     // up to 16-byte alignment element by element, as at the end
@@ -281,120 +354,42 @@ __device__ __forceinline__ void zero_row(uint8_t *row, int64_t bytes, int size, 
     }
 }
 
-// Set a row's bit.
-__device__ __forceinline__ void mark(uint32_t *used, int64_t row) {
-    const uint32_t bit = 1u << (row % 32);
-    if (!(*static_cast<volatile uint32_t *>(used + row / 32) & bit)) atomicOr(used + row / 32, bit);
-}
-
-// A CTA per SM, each with a stretch of the table: it marks the rows that the
-// tokens use and writes zeros to the others. Follows the sort on the stream but
-// needs nothing of it, so it waits for it last: when this kernel has ended, the
-// sort has too.
-__global__ void __launch_bounds__(kFillThreads, 2) fill_kernel(const __grid_constant__ FillArgs a) {
-    __shared__ uint32_t used[kWindow / 32];
+// The first CTAs of the sums' grid have a stretch of the table each: they mark
+// the rows that the tokens use and write zeros to the others. They need nothing
+// of the sort before them on the stream and wait for it last, so they run
+// beside it, and the sums beside them as soon as it has ended (32768 tokens,
+// 128000 x 8192 bf16: 394 us where zeros, then sums took 425).
+__device__ __forceinline__ void fill_rows(const SumArgs &a, uint32_t *used) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t each = (a.vocab + gridDim.x - 1) / gridDim.x;
-    const int64_t begin = blockIdx.x * each, end = min(begin + each, a.vocab);
+    const int64_t vocab = a.vocab, each = (vocab + a.fill_ctas - 1) / a.fill_ctas;
+    const int64_t begin = min(blockIdx.x * each, vocab), end = min(begin + each, vocab);
     if (a.n == 0) wait_previous();  // (no sort: the kernel before is the caller's)
     for (int64_t row0 = begin; row0 < end; row0 += kWindow) {
         const int64_t rows = min(kWindow, end - row0);
-        for (int i = threadIdx.x; i < kWindow / 32; i += kFillThreads) used[i] = 0;
+        for (int i = threadIdx.x; i < (rows + 31) / 32; i += kThreads) used[i] = 0;
         __syncthreads();
 #pragma unroll 8
-        for (int64_t i = threadIdx.x; i < a.n; i += kFillThreads) {
+        for (int64_t i = threadIdx.x; i < a.n; i += kThreads) {
             const int64_t token = a.tokens[i], at = token - row0;
-            if (at >= 0 && at < rows && token != a.ignore) mark(used, at);
+            if (at < 0 || at >= rows || token == a.ignore) continue;
+            const uint32_t bit = 1u << (at % 32);
+            if (!(*static_cast<volatile uint32_t *>(used + at / 32) & bit)) atomicOr(used + at / 32, bit);
         }
         __syncthreads();
-        for (int64_t r = warp; r < rows; r += kFillThreads / 32)
+        for (int64_t r = warp; r < rows; r += kWarps)
             if (!(used[r / 32] >> (r % 32) & 1u))
-                zero_row(a.d_weight + (row0 + r) * a.row_bytes, a.dim * a.size, a.size, lane);
+                zero_row(a.d_weight + (row0 + r) * a.weight_bytes, a.dim * a.size, a.size, lane);
         __syncthreads();
     }
     wait_previous();
     allow_next();
-}
-
-// ---------------------------------------------------------------- few tokens: their order by counting, and the zeros
-
-// Up to 4096 tokens below 2^20 (or none: key `vocab`) are sorted by all CTAs at
-// once: an entry's place is the number of smaller ones, a token and its position
-// in one 32-bit word, which a warp counts in shared memory. 1024 entries take
-// 3.7 us (the radix sort's waits 8), 4096 8, 8192 14 (11).
-// Warps that have no entry to place fill rows with zeros meanwhile.
-constexpr uint32_t kPlaceBits = 12, kPlaceMost = 1u << kPlaceBits;
-constexpr int64_t kPlaceVocab = int64_t(1) << (32 - kPlaceBits);
-
-__global__ void __launch_bounds__(kFillThreads, 1)
-    place_kernel(const __grid_constant__ SortArgs a, const __grid_constant__ FillArgs f, bool fill) {
-    __shared__ __align__(16) uint32_t entry[kPlaceMost];
-    __shared__ uint32_t used[kWindow / 32];
-    __shared__ uint32_t next_row;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const uint32_t vocab = a.vocab, each = (vocab + gridDim.x - 1) / gridDim.x;
-    const uint32_t row0 = min(blockIdx.x * each, vocab), rows = min(each, vocab - row0);  // (within a window)
-    const uint32_t padded = (a.n + 127) / 128 * 128;
-    if (fill)
-        for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += kFillThreads) used[i] = 0;
-    if (threadIdx.x == 0) next_row = 0;
-    wait_previous();
-    allow_next();
-    for (uint32_t i = blockIdx.x * kFillThreads + threadIdx.x; i < a.n_tickets; i += gridDim.x * kFillThreads)
-        a.tickets[i] = 0;
-    __syncthreads();
-    for (uint32_t i = threadIdx.x; i < padded; i += kFillThreads) {
-        uint32_t e = 0xffffffffu;
-        if (i < a.n) {
-            const int64_t token = a.tokens[i];
-            const bool none = token == a.ignore || token < 0 || token >= vocab;
-            const uint32_t key = none ? vocab : static_cast<uint32_t>(token);
-            if (fill && key - row0 < rows) mark(used, key - row0);
-            e = key << kPlaceBits | i;
-        }
-        entry[i] = e;
-    }
-    __syncthreads();
-    for (uint32_t i = blockIdx.x + gridDim.x * warp; i < a.n; i += 2 * kFillThreads / 32 * gridDim.x) {
-        const uint32_t other = i + kFillThreads / 32 * gridDim.x;  // two entries at a time
-        const uint32_t x = entry[i], y = other < a.n ? entry[other] : 0u;
-        uint32_t below_x = 0, below_y = 0;
-        for (uint32_t j = 4 * lane; j < padded; j += 128) {
-            const uint4 e = *reinterpret_cast<const uint4 *>(entry + j);
-            below_x += (e.x < x) + (e.y < x) + (e.z < x) + (e.w < x);
-            below_y += (e.x < y) + (e.y < y) + (e.z < y) + (e.w < y);
-        }
-        below_x = __reduce_add_sync(0xffffffffu, below_x);
-        below_y = __reduce_add_sync(0xffffffffu, below_y);
-        if (lane == 0) {
-            a.key[0][below_x] = x >> kPlaceBits;
-            a.pos[0][below_x] = i;
-            if (other < a.n) {
-                a.key[0][below_y] = y >> kPlaceBits;
-                a.pos[0][below_y] = other;
-            }
-        }
-    }
-    if (!fill) return;
-    const int64_t bytes = f.dim * f.size;
-    const uint32_t batch = bytes >= 4096 ? 1 : static_cast<uint32_t>(4096 / bytes);
-    for (;;) {
-        uint32_t r = 0;
-        if (lane == 0) r = atomicAdd(&next_row, batch);
-        r = __shfl_sync(0xffffffffu, r, 0);
-        if (r >= rows) break;
-        for (const uint32_t last = min(r + batch, rows); r < last; ++r)
-            if (!(used[r / 32] >> (r % 32) & 1u)) zero_row(f.d_weight + int64_t(row0 + r) * f.row_bytes, bytes, f.size, lane);
-    }
 }
 
 // ---------------------------------------------------------------- sums
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-static_assert(kWarps == kSumWarps, "the host cuts the entries for as many warps");
-// Rows of a warp on their way; fewer where the rows they are added to are too.
-constexpr int slots(bool add) { return add ? 3 : 4; }
-constexpr uint32_t kAll = 0xffffffffu;
+// Rows of a warp on their way, and rows that sums are added to: three CTAs of an
+// SM have room for them.
+constexpr int kSlots = 4, kThere = 3;
 
 // A warp's slice of a row: 1 KB, in words of a lane of 16 bytes, or of one
 // element where rows are not 16-byte aligned (then with up to 16 bytes more, as
@@ -413,12 +408,11 @@ template <int DT, bool VEC> struct SumSlice {
 // come by then.
 template <int DT, bool VEC, bool ADD> struct WarpShared {
     using S = SumSlice<DT, VEC>;
-    static constexpr int kSlots = slots(ADD);
     union {
         uint4 rows[kSlots][S::kBytes / 16];
         float tail[S::kWords][S::kElems][32];
     };
-    uint4 there[ADD ? kSlots : 1][S::kBytes / 16];
+    uint4 there[ADD ? kThere : 1][S::kBytes / 16];
     float head[S::kWords][S::kElems][32];
     __device__ WarpShared() {}
 };
@@ -509,31 +503,20 @@ struct Columns {
     int count, words;  // words of a lane (the same for all slices)
 };
 
-// This run's part of block b to memory; true, with the whole run's sum, for
-// the warp that brings its last part.
+// Sum of the parts of a run in the blocks first, first + step, ... before
+// `end`. A run's part is the second one in the block it begins in, else the
+// first.
 template <int DT, bool VEC>
-__device__ __forceinline__ bool join_parts(const SumArgs &a, uint32_t b, uint32_t slice, const Columns &c, bool head,
-                                           uint32_t from, uint32_t to, typename SumSlice<DT, VEC>::Sum &sum) {
+__device__ __forceinline__ void add_parts(const SumArgs &a, const Columns &c, uint32_t from, uint32_t first, uint32_t end,
+                                          uint32_t step, typename SumSlice<DT, VEC>::Sum &sum) {
     using S = SumSlice<DT, VEC>;
     const int lane = threadIdx.x % 32;
-    float *mine = a.part + (int64_t(b) * 2 + (head ? 0 : 1)) * a.ld_part + c.first;
-#pragma unroll
-    for (int j = 0; j < S::kWords; ++j) {
-        const int col = (j * 32 + lane) * S::kElems;
-        if (col < c.count) store_floats<S::kElems>(mine + col, sum[j]);
-    }
-    __threadfence();
-    __syncwarp();
-    uint32_t there = 0;
-    if (lane == 0) there = atomicAdd(a.tickets + uint64_t(from) * a.slices + slice, 1u);
-    if (__shfl_sync(kAll, there, 0) != to - from) return false;
-    __threadfence();
 #pragma unroll
     for (int j = 0; j < S::kWords; ++j)
 #pragma unroll
         for (int e = 0; e < S::kElems; ++e) sum[j][e] = 0.0f;
 #pragma unroll 4
-    for (uint32_t i = from; i <= to; ++i) {
+    for (uint32_t i = first; i < end; i += step) {
         const float *part = a.part + (int64_t(i) * 2 + (i == from ? 1 : 0)) * a.ld_part + c.first;
 #pragma unroll
         for (int j = 0; j < S::kWords; ++j) {
@@ -541,7 +524,46 @@ __device__ __forceinline__ bool join_parts(const SumArgs &a, uint32_t b, uint32_
             if (col < c.count) add_floats<S::kElems>(part + col, sum[j]);
         }
     }
-    return true;
+}
+
+// This run's part of block b, of its blocks from .. to, to memory; true, with
+// the whole run's sum, for the warp that brings the last one. A run over many
+// blocks is added up in two steps, by the last warps of a few groups and then
+// by the last of those: one warp took 20 us for the parts of 102 blocks.
+template <int DT, bool VEC>
+__device__ __forceinline__ bool join_parts(const SumArgs &a, uint32_t b, uint32_t slice, const Columns &c, uint32_t from,
+                                           uint32_t to, typename SumSlice<DT, VEC>::Sum &sum) {
+    using S = SumSlice<DT, VEC>;
+    const int lane = threadIdx.x % 32;
+    const uint32_t blocks = to - from + 1;
+    uint32_t group = 16;
+    while (group * group < blocks) group *= 2;
+    uint32_t first = b - (b - from) % group, end = min(first + group, to + 1), step = 1, at = b;
+    // (a block may have a run's later group and another run's first one)
+    uint32_t *ticket = a.tickets + ((first == from ? 0 : 2 * uint64_t(a.blocks)) + first) * a.slices + slice;
+#pragma unroll 1
+    for (;;) {
+        float *mine = a.part + (int64_t(at) * 2 + (at == from ? 1 : 0)) * a.ld_part + c.first;
+#pragma unroll
+        for (int j = 0; j < S::kWords; ++j) {
+            const int col = (j * 32 + lane) * S::kElems;
+            if (col < c.count) store_floats<S::kElems>(mine + col, sum[j]);
+        }
+        __threadfence();
+        __syncwarp();
+        uint32_t there = 0;
+        if (lane == 0) there = atomicAdd(ticket, 1u) + 1;
+        if (__shfl_sync(kAll, there, 0) != (end - first + step - 1) / step) return false;
+        __threadfence();
+        add_parts<DT, VEC>(a, c, from, first, end, step, sum);
+        if (step > 1 || blocks <= group) return true;
+        // the group's sum, in its first part's place
+        at = first;
+        first = from;
+        end = to + 1;
+        step = group;
+        ticket = a.tickets + (uint64_t(a.blocks) + from) * a.slices + slice;
+    }
 }
 
 // A block of sorted entries, for one slice of the columns; each warp has 4 to 16
@@ -556,13 +578,19 @@ template <int DT, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kThreads, ADD ? 3 : 4) sum_kernel(const __grid_constant__ SumArgs a) {
     using S = SumSlice<DT, VEC>;
     using Shared = WarpShared<DT, VEC, ADD>;
-    constexpr int kSlots = slots(ADD);
     extern __shared__ __align__(16) uint8_t raw[];
     Shared *shared = reinterpret_cast<Shared *>(raw);
     __shared__ bool through[kWarps];    // a run from before the warp's entries goes on after them
     __shared__ uint32_t back, ahead;    // blocks that runs from before and after the block go over, beside the next one
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, each = a.block / kWarps;
-    const uint32_t slice = blockIdx.x % a.slices, b = blockIdx.x / a.slices;
+    if constexpr (!ADD) {
+        static_assert(kWarps * sizeof(Shared) >= kWindow / 8, "a bit for each row of a window");
+        if (blockIdx.x < a.fill_ctas) {
+            fill_rows(a, reinterpret_cast<uint32_t *>(raw));
+            return;
+        }
+    }
+    const uint32_t cta = blockIdx.x - a.fill_ctas, slice = cta % a.slices, b = cta / a.slices;
     Columns c;
     c.words = a.words;
     c.first = int64_t(slice) * 32 * c.words * S::kElems;
@@ -585,12 +613,12 @@ __global__ void __launch_bounds__(kThreads, ADD ? 3 : 4) sum_kernel(const __grid
     auto row_of = [&](int i) { return a.d_out + int64_t(__shfl_sync(kAll, pos, i)) * a.out_bytes + first_byte; };
     auto to_of = [&](int i) { return a.d_weight + int64_t(__shfl_sync(kAll, key, i)) * a.weight_bytes + first_byte; };
     auto shift_of = [](const uint8_t *p) { return VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15); };
-    auto issue = [&](int i) {  // row i to its slot, and the row that its run's sum is added to
-        if (i < count) {
-            copy_row<DT, VEC>(mine.rows[i % kSlots], row_of(i), c.count * S::kSize);
-            if constexpr (ADD) {
-                if (ends >> i & 1u) copy_row<DT, VEC>(mine.there[i % kSlots], to_of(i), c.count * S::kSize);
-            }
+    // row i to its slot, and the row that the run's sum of the entry before is added to
+    auto issue = [&](int i) {
+        if (i < count) copy_row<DT, VEC>(mine.rows[i % kSlots], row_of(i), c.count * S::kSize);
+        if constexpr (ADD) {
+            if (i > 0 && i <= count && (ends >> (i - 1) & 1u))
+                copy_row<DT, VEC>(mine.there[(i - 1) % kThere], to_of(i - 1), c.count * S::kSize);
         }
         copy_commit();
     };
@@ -626,11 +654,23 @@ __global__ void __launch_bounds__(kThreads, ADD ? 3 : 4) sum_kernel(const __grid
             Word<DT, VEC>::store(to, col, f);
         }
     };
+    auto add_there = [&](const uint8_t *to) {  // (a row that nothing has been copied of)
+        if constexpr (ADD) {
+            __syncwarp();
+            copy_row<DT, VEC>(mine.there[0], to, c.count * S::kSize);
+            copy_commit();
+            copy_wait<0>();
+            __syncwarp();
+        }
+    };
     clear();
     bool first = true;
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
-        copy_wait<kSlots - 1>();
+        if (ADD && (ends >> i & 1u))
+            copy_wait<kSlots - 2>();
+        else
+            copy_wait<kSlots - 1>();
         if constexpr (!VEC) __syncwarp();  // (other lanes' granules)
         const int shift = VEC ? 0 : shift_of(row_of(i));
 #pragma unroll
@@ -648,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, ADD ? 3 : 4) sum_kernel(const __grid
 #pragma unroll
                     for (int e = 0; e < S::kElems; ++e) mine.head[j][e][lane] = sum[j][e];
             } else {
-                write_row(to_of(i), mine.there[ADD ? i % kSlots : 0]);
+                write_row(to_of(i), mine.there[ADD ? i % kThere : 0]);
             }
             first = false;
             clear();
@@ -687,19 +727,13 @@ __global__ void __launch_bounds__(kThreads, ADD ? 3 : 4) sum_kernel(const __grid
                 for (int e = 0; e < S::kElems; ++e) sum[j][e] += shared[other].head[j][e][lane];
             goes = through[other];
         }
+        const int entry = which == 0 ? 0 : each - 1;
         if (which == 0 || goes) {
             const uint32_t from = which == 0 ? b - 1 - back : b, to = goes ? b + 1 + ahead : b;
-            if (!join_parts<DT, VEC>(a, b, slice, c, which == 0, from, to, sum)) continue;
+            if (!join_parts<DT, VEC>(a, b, slice, c, from, to, sum)) continue;
         }
-        uint8_t *to = to_of(which == 0 ? 0 : each - 1);
-        if constexpr (ADD) {
-            __syncwarp();
-            copy_row<DT, VEC>(mine.there[0], to, c.count * S::kSize);
-            copy_commit();
-            copy_wait<0>();
-            __syncwarp();
-        }
-        write_row(to, mine.there[0]);
+        add_there(to_of(entry));
+        write_row(to_of(entry), mine.there[0]);
     }
 }
 
@@ -714,7 +748,7 @@ template <int DT, bool VEC, bool ADD> fsdp_status launch_type(const SumArgs &a, 
         once.mark(dev);
     }
     // (the blocks times the slices are below 2^31: a workspace of that many tickets)
-    return launch_chained(sum_kernel<DT, VEC, ADD>, a.blocks * a.slices, kThreads, kShared, s, a);
+    return launch_chained(sum_kernel<DT, VEC, ADD>, a.fill_ctas + a.blocks * a.slices, kThreads, kShared, s, a);
 }
 
 template <int DT> fsdp_status launch_form(const SumArgs &a, bool vec, bool add, cudaStream_t s) {
@@ -760,26 +794,16 @@ fsdp_status launch_sort(const SortArgs &a, cudaStream_t s) {
 
 bool can_place(int64_t n, int64_t vocab) { return n > 0 && n <= kPlaceMost && vocab < kPlaceVocab; }
 
-fsdp_status launch_place(const SortArgs &a, const FillArgs &f, bool fill, cudaStream_t s) {
-    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
-    const int64_t rows = fill ? (f.vocab + 31) / 32 : 0, entries = (int64_t(a.n) + 1) / 2;
-    int64_t grid = rows > entries ? rows : entries;
-    grid = grid < sms ? grid : sms;
-    const int64_t windows = (f.vocab + kWindow - 1) / kWindow;  // (a device of few SMs)
-    grid = fill && grid < windows ? windows : grid;
-    return launch_chained(place_kernel, static_cast<unsigned>(grid), kFillThreads, 0, s, a, f, fill);
-}
-
-fsdp_status launch_fill(const FillArgs &a, cudaStream_t s) {
-    const int64_t sms = sm_count() > 0 ? sm_count() : 1, most = (a.vocab + 31) / 32;
+fsdp_status launch_place(const SortArgs &a, cudaStream_t s) {
     static PerDeviceOnce once;
     const int dev = current_device();
     if (!once.is_done(dev)) {
-        const cudaError_t e = cudaFuncSetAttribute(fill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFillShared);
+        const cudaError_t e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlaceShared);
         if (e != cudaSuccess) return cuda_status(e);
         once.mark(dev);
     }
-    return launch_chained(fill_kernel, static_cast<unsigned>(sms < most ? sms : most), kFillThreads, kFillShared, s, a);
+    const uint32_t sms = sm_count() > 0 ? sm_count() : 1, pairs = (a.n + 1) / 2;
+    return launch_chained(place_kernel, pairs < sms ? pairs : sms, kPlaceThreads, kPlaceShared, s, a);
 }
 
 fsdp_status launch_sums(const SumArgs &a, int dtype, bool vec, bool add, cudaStream_t s) {
