@@ -97,19 +97,44 @@ __device__ __forceinline__ void join(float &top, float &sum, float other_top, fl
     top = most;
 }
 
+// A lane's first entries of a row, and their logits.
+struct SoftEntries {
+    static constexpr int kEntries = 2;
+    int32_t id[kEntries];
+    float2 p[kEntries];
+    float logit[kEntries];
+    __device__ __forceinline__ void load(const RowArgs &a, int64_t row) {
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) {
+            const int64_t k = 32 * i + threadIdx.x % 32;
+            id[i] = k < a.top ? a.ids[row * a.top + k] : kNoEntry;
+            p[i] = k < a.top ? a.prob[row * a.top + k] : make_float2(0.0f, 0.0f);
+        }
+    }
+    __device__ __forceinline__ static float logit_of(const RowArgs &a, int64_t row, int64_t k, int32_t id) {
+        return a.at != nullptr ? a.at[row * a.top + k] : a.logits[row * a.ld_logits + id];
+    }
+    __device__ __forceinline__ void load_logits(const RowArgs &a, int64_t row) {
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i)
+            logit[i] = id[i] != kNoEntry ? logit_of(a, row, 32 * i + threadIdx.x % 32, id[i]) : 0.0f;
+    }
+};
+
 // What a row of SOFT loses: temperature^2 times the sum of p (log p - log q)
 // over the teacher's entries, by a warp. Differences first: each is as small
 // as the two distributions are close.
-__device__ __forceinline__ float soft_loss(const RowArgs &a, int64_t row, float top, float sum) {
-    const int lane = threadIdx.x % 32;
+__device__ __forceinline__ float soft_loss(const RowArgs &a, int64_t row, const SoftEntries &first, float top, float sum) {
     const float log_sum = logf(sum);
     float t = 0.0f;
-    for (int64_t k = lane; k < a.top; k += 32) {
+    auto add = [&](float2 p, float logit) { t += p.x * (p.y - ((logit - top) * a.inverse - log_sum)); };
+#pragma unroll
+    for (int i = 0; i < SoftEntries::kEntries; ++i)
+        if (first.id[i] != kNoEntry) add(first.p[i], first.logit[i]);
+    for (int64_t k = 32 * SoftEntries::kEntries + threadIdx.x % 32; k < a.top; k += 32) {
         const int32_t id = a.ids[row * a.top + k];
         if (id == kNoEntry) break;
-        const float2 p = a.prob[row * a.top + k];
-        const float logit = a.at != nullptr ? a.at[row * a.top + k] : a.logits[row * a.ld_logits + id];
-        t += p.x * (p.y - ((logit - top) * a.inverse - log_sum));
+        add(a.prob[row * a.top + k], SoftEntries::logit_of(a, row, k, id));
     }
     return a.temperature * a.temperature * warp_sum(t);
 }
@@ -120,15 +145,20 @@ __device__ __forceinline__ void write_loss(const RowArgs &a, double sum, long lo
     *a.scale = static_cast<float>(a.grad_scale / by);
 }
 
-constexpr int kRows = 16;     // of a block
+// Rows of a block: eight while that leaves a block for each SM at most (a
+// teacher's entries and 1021 rows of 50257 columns 10.7 us, with sixteen 13.5;
+// 2048 of 32000 15.5 and 12.3; 4096 of 50257 33 and 22). The cross entropy
+// keeps its sums' order.
+constexpr int64_t kEightRows = 1216;
+inline int block_rows(bool soft, int64_t tokens) { return soft && tokens <= kEightRows ? 8 : 16; }
 constexpr int kRowLoads = 8;  // spans a thread reads at once
 
-// 16 rows per block of 1024 threads: a warp reads two spans of the 16 rows at
-// a time (the statistics lie span by span), the 64 readers of a row share its
-// spans. Latency-bound: 2 x 4 bytes per span and row, eight loads in flight
+// 16 (or 8) rows per block of 1024 threads: a warp reads two (four) spans of
+// them at a time (the statistics lie span by span), the 64 (128) readers of a
+// row share its spans. Latency-bound: 2 x 4 bytes per span and row, eight loads in flight
 // per thread. The loss adds up per block, then over the blocks in one fixed
 // order, in fp64.
-template <bool SOFT> __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowArgs a) {
+template <bool SOFT, int kRows> __global__ void __launch_bounds__(1024) rows_kernel(const __grid_constant__ RowArgs a) {
     const float log2e = SOFT ? a.log2e : kLog2e;
     __shared__ float tops[32][kRows + 1], sums[32][kRows + 1];
     __shared__ double total[32];
@@ -137,6 +167,11 @@ template <bool SOFT> __global__ void __launch_bounds__(1024) rows_kernel(const _
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     wait_previous();
     allow_next();
+    SoftEntries entries;  // (a warp per row: on their way with the statistics)
+    if constexpr (SOFT) {
+        const int64_t row = int64_t(blockIdx.x) * kRows + warp;
+        if (warp < kRows && row < a.rows) entries.load(a, row);
+    }
     {
         const int64_t row = int64_t(blockIdx.x) * kRows + lane % kRows;
         float top = -INFINITY, sum = 0.0f;
@@ -159,7 +194,13 @@ template <bool SOFT> __global__ void __launch_bounds__(1024) rows_kernel(const _
                 top = most;
             }
         }
-        join(top, sum, __shfl_xor_sync(0xffffffffu, top, kRows), __shfl_xor_sync(0xffffffffu, sum, kRows), log2e);
+        if constexpr (SOFT) {
+            const int64_t own = int64_t(blockIdx.x) * kRows + warp;
+            if (warp < kRows && own < a.rows) entries.load_logits(a, own);
+        }
+#pragma unroll
+        for (int o = kRows; o < 32; o *= 2)
+            join(top, sum, __shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o), log2e);
         if (lane < kRows) {
             tops[warp][lane] = top;
             sums[warp][lane] = sum;
@@ -174,7 +215,7 @@ template <bool SOFT> __global__ void __launch_bounds__(1024) rows_kernel(const _
             join(top, sum, __shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o), log2e);
         float soft = 0.0f;
         if constexpr (SOFT) {
-            if (row < a.rows && a.targets[row] == 0) soft = soft_loss(a, row, top, sum);
+            if (row < a.rows && a.targets[row] == 0) soft = soft_loss(a, row, entries, top, sum);
         }
         if (lane == 0) {
             float t = 0.0f;
@@ -273,11 +314,10 @@ struct GradArgs {
     int64_t ignore;
     uint32_t row_blocks;
     // against a teacher's distribution
-    const uint16_t *first;   // [rows][ld_first]
     const int32_t *ids;      // [rows][top]
     const float2 *prob;
     const float *at;
-    int64_t ld_first, top, spans;
+    int64_t top;
     float log2e;
 };
 
@@ -299,12 +339,32 @@ __device__ __forceinline__ void split3(float x, float &hi, float &mid, float &lo
 }
 
 constexpr int kGradCols = 512, kGradRows = 64;
+constexpr int kGradStep = 256 / (kGradCols / 8);  // rows that the block's threads have at a time
+constexpr int grad_ahead(int dtype) { return dtype == FSDP_F32 ? 2 : 4; }  // of a thread, loaded together
+
+// Eight exponentials.
+template <int DT> struct GradWord {
+    uint4 x;
+    __device__ __forceinline__ void load(const void *e, int64_t at) {
+        x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e) + at);
+    }
+    __device__ __forceinline__ void widen(float *v) const { unpack8<FSDP_F16>(x, v); }
+};
+template <> struct GradWord<FSDP_F32> {
+    float4 x, y;
+    __device__ __forceinline__ void load(const void *e, int64_t at) {
+        x = *reinterpret_cast<const float4 *>(static_cast<const float *>(e) + at);
+        y = *reinterpret_cast<const float4 *>(static_cast<const float *>(e) + at + 4);
+    }
+    __device__ __forceinline__ void widen(float *v) const {
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    }
+};
 
 // 64 rows x 512 columns per block, 8 columns per thread and row. Bound by HBM
 // (or L2, where the band fits): 4 bytes moved per element in 16-bit types.
-//
-// SOFT: the block then writes the teacher's entries among its columns, from
-// their fp32 logits, as the target's is.
+// SOFT: q alone, whose exponentials are over the temperature; the teacher's
+// entries follow (entries_kernel).
 template <int DT, bool SOFT> __global__ void __launch_bounds__(256) grad_kernel(const __grid_constant__ GradArgs a) {
     __shared__ float factor[kGradCols / kSpan][kGradRows];
     __shared__ int32_t hit[kGradRows];  // the target's column in this block, or -1; -2: no gradient
@@ -318,6 +378,19 @@ template <int DT, bool SOFT> __global__ void __launch_bounds__(256) grad_kernel(
     const float log2e = SOFT ? a.log2e : kLog2e;
     wait_previous();
     allow_next();
+    // the first rows are on their way while the factors are formed
+    const int c = threadIdx.x % (kGradCols / 8) * 8;
+    const int64_t col = col0 + c;
+    const int rows = col >= a.vocab ? 0 : static_cast<int>(min(int64_t(kGradRows), a.rows - row0));
+    const int first_row = threadIdx.x / (kGradCols / 8);
+    constexpr int kGradAhead = grad_ahead(DT);
+    GradWord<DT> ahead[kGradAhead];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < kGradAhead; ++u)
+            if (r0 + u * kGradStep < rows) ahead[u].load(a.e, (row0 + r0 + u * kGradStep) * a.ld + col);
+    };
+    load(first_row);
     for (int i = threadIdx.x; i < kGradRows * (kGradCols / kSpan); i += 256) {
         const int r = i % kGradRows, s = i / kGradRows;
         const int64_t row = row0 + r, span = col0 / kSpan + s;
@@ -340,72 +413,68 @@ template <int DT, bool SOFT> __global__ void __launch_bounds__(256) grad_kernel(
         }
     }
     __syncthreads();
-    const int c = threadIdx.x % (kGradCols / 8) * 8;
-    const int64_t col = col0 + c;
-    if (!SOFT && col >= a.vocab) return;
-    const int rows = SOFT && col >= a.vocab ? 0 : static_cast<int>(min(int64_t(kGradRows), a.rows - row0));
-#pragma unroll 4
-    for (int r = threadIdx.x / (kGradCols / 8); r < rows; r += 256 / (kGradCols / 8)) {
-        const int64_t at = (row0 + r) * a.ld + col;
-        const float f = factor[c / kSpan][r];
-        const int h = hit[r] - c;
-        float v[8];
-        if constexpr (DT == FSDP_F32) {
-            const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.e) + at);
-            const float4 y = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.e) + at + 4);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-        } else {
-            unpack8<FSDP_F16>(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.e) + at), v);
-        }
+    for (int r0 = first_row; r0 < rows; r0 += kGradAhead * kGradStep) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] = h == j ? at_target[r] : v[j] * f;
-        }
-        if (hit[r] == -2) {
+        for (int u = 0; u < kGradAhead; ++u) {
+            const int r = r0 + u * kGradStep;
+            if (r >= rows) break;
+            const int64_t at = (row0 + r) * a.ld + col;
+            const float f = factor[c / kSpan][r];
+            const int h = hit[r] - c;
+            float v[8];
+            ahead[u].widen(v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        }
-        if constexpr (DT == FSDP_F32) {
-            float p[3][8];
+            for (int j = 0; j < 8; ++j) {
+                v[j] = h == j ? at_target[r] : v[j] * f;
+            }
+            if (hit[r] == -2) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) split3(v[j], p[0][j], p[1][j], p[2][j]);
-#pragma unroll
-            for (int z = 0; z < 3; ++z)
-                *reinterpret_cast<uint4 *>(a.planes[z] + at) =
-                    make_uint4(pack2<FSDP_BF16>(p[z][0], p[z][1]), pack2<FSDP_BF16>(p[z][2], p[z][3]),
-                               pack2<FSDP_BF16>(p[z][4], p[z][5]), pack2<FSDP_BF16>(p[z][6], p[z][7]));
-        } else {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.e) + at) =
-                make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
-        }
-    }
-    if constexpr (SOFT) {
-        __syncthreads();
-        constexpr int kShare = 256 / kGradRows;  // threads of a row
-        const int64_t row = row0 + threadIdx.x / kShare;
-        if (row >= a.rows) return;
-        const uint16_t *first = a.first + row * a.ld_first + col0 / kSpan;
-        const int end = first[min(int64_t(kGradCols / kSpan), a.spans - col0 / kSpan)];
-        const int32_t *ids = a.ids + row * a.top;
-        const float2 state = a.row_state[row];
-        for (int k = first[0] + threadIdx.x % kShare; k < end; k += kShare) {
-            // (a token that the teacher names twice has both probabilities)
-            const int32_t id = ids[k];
-            if (k > 0 && ids[k - 1] == id) continue;
-            float p = a.prob[row * a.top + k].x;
-            for (int more = k + 1; more < a.top && ids[more] == id; ++more) p += a.prob[row * a.top + more].x;
-            const float x = kGain * (exp_of(a.at[row * a.top + k] - state.x, log2e) / state.y - p);
-            const int64_t at = row * a.ld + id;
+                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+            }
             if constexpr (DT == FSDP_F32) {
-                float hi, mid, lo;
-                split3(x, hi, mid, lo);
-                Dtype<FSDP_BF16>::store(a.planes[0], at, hi);
-                Dtype<FSDP_BF16>::store(a.planes[1], at, mid);
-                Dtype<FSDP_BF16>::store(a.planes[2], at, lo);
+                float p[3][8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) split3(v[j], p[0][j], p[1][j], p[2][j]);
+#pragma unroll
+                for (int z = 0; z < 3; ++z)
+                    *reinterpret_cast<uint4 *>(a.planes[z] + at) =
+                        make_uint4(pack2<FSDP_BF16>(p[z][0], p[z][1]), pack2<FSDP_BF16>(p[z][2], p[z][3]),
+                                   pack2<FSDP_BF16>(p[z][4], p[z][5]), pack2<FSDP_BF16>(p[z][6], p[z][7]));
             } else {
-                Dtype<DT>::store(a.e, at, x);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.e) + at) =
+                    make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
             }
         }
+        load(r0 + kGradAhead * kGradStep);
+    }
+}
+
+// A teacher's entries of d, a thread each, from their fp32 logits as the target
+// is. (Within the pass over d they took 18 us of 4096 x 50257 x 1280 with 101
+// entries a row.)
+template <int DT> __global__ void __launch_bounds__(256) entries_kernel(const __grid_constant__ GradArgs a) {
+    constexpr float kGain = DT == FSDP_F16 ? kHalfGain : 1.0f;
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, row = i / a.top;
+    const int k = static_cast<int>(i - row * a.top);
+    wait_previous();
+    allow_next();
+    if (row >= a.rows) return;
+    const int32_t id = a.ids[i];
+    // (a token that the teacher names twice has both probabilities)
+    if (id == kNoEntry || (k > 0 && a.ids[i - 1] == id)) return;
+    const float2 state = a.row_state[row];
+    float p = a.prob[i].x;
+    for (int more = 1; k + more < a.top && a.ids[i + more] == id; ++more) p += a.prob[i + more].x;
+    const float x = kGain * (exp_of(a.at[i] - state.x, a.log2e) / state.y - p);
+    const int64_t at = row * a.ld + id;
+    if constexpr (DT == FSDP_F32) {
+        float hi, mid, lo;
+        split3(x, hi, mid, lo);
+        Dtype<FSDP_BF16>::store(a.planes[0], at, hi);
+        Dtype<FSDP_BF16>::store(a.planes[1], at, mid);
+        Dtype<FSDP_BF16>::store(a.planes[2], at, lo);
+    } else {
+        Dtype<DT>::store(a.e, at, x);
     }
 }
 
@@ -580,7 +649,7 @@ Plan choose(const fsdp_head_loss_args &a, int64_t top) {
     p.blocks = 0;
     for (int64_t b = 0; b < p.bands; ++b) {
         const int64_t rows = a.tokens - b * p.band < p.band ? a.tokens - b * p.band : p.band;
-        p.blocks += ceil_div(rows, kRows);
+        p.blocks += ceil_div(rows, block_rows(p.top > 0, a.tokens));
     }
     p.splits_x = p.splits_w = 1;
     if (a.d_hidden) p.splits_x = p.few ? static_cast<int>(few_parts(a.vocab, a.dim)) : hidden_splits(a, p.band);
@@ -634,6 +703,11 @@ Room room_up_to(const fsdp_head_loss_args &a, int64_t top) {
         r.stats = larger(r.stats, f.stats);
         r.e = larger(r.e, f.e);
         r.part = larger(r.part, f.part);
+    }
+    if (top > 0 && a.tokens > kEightRows) {
+        // (shorter ones have blocks of half as many rows; a band ends a block)
+        const int64_t each = a.band > 0 ? a.band : kTileM;
+        r.blocks = larger(r.blocks, ceil_div(kEightRows, 8) + ceil_div(kEightRows, each) + 1);
     }
     // the longest band of these calls: they are as long as their tokens up to
     // what was asked for or what the budget allows
@@ -929,7 +1003,7 @@ fsdp_status run_rows(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, i
     r.scale = reinterpret_cast<float *>(ws + p.scale);
     r.grad_scale = a.grad_scale;
     r.mean = a.reduction == FSDP_LOSS_MEAN;
-    const unsigned blocks = static_cast<unsigned>(ceil_div(rows, kRows));
+    const unsigned blocks = static_cast<unsigned>(ceil_div(rows, block_rows(soft != nullptr, a.tokens)));
     block += blocks;
     if (soft) {
         r.ids = soft->ids;
@@ -941,9 +1015,9 @@ fsdp_status run_rows(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, i
         r.temperature = soft->temperature;
         r.inverse = soft->inverse;
         r.log2e = soft->log2e;
-        return launch_chained(rows_kernel<true>, blocks, 1024, 0, s, r);
+        return launch_chained(block_rows(true, a.tokens) == 8 ? rows_kernel<true, 8> : rows_kernel<true, 16>, blocks, 1024, 0, s, r);
     }
-    return launch_chained(rows_kernel<false>, blocks, 1024, 0, s, r);
+    return launch_chained(rows_kernel<false, 16>, blocks, 1024, 0, s, r);
 }
 
 // soft: against a teacher's distribution (a.targets are then the workspace's,
@@ -1059,19 +1133,25 @@ fsdp_status run(const fsdp_head_loss_args &a, const Plan &p, uint8_t *ws, SoftAr
                     : a.dtype == FSDP_F16 ? grad_kernel<FSDP_F16, false>
                                           : grad_kernel<FSDP_F32, false>;
         if (soft) {
-            d.first = soft->first;
-            d.ld_first = soft->ld_first;
             d.ids = soft->ids;
             d.prob = soft->prob;
             d.at = g.at;
             d.top = soft->top;
-            d.spans = soft->spans;
             d.log2e = soft->log2e;
             grad = a.dtype == FSDP_BF16  ? grad_kernel<FSDP_BF16, true>
                    : a.dtype == FSDP_F16 ? grad_kernel<FSDP_F16, true>
                                          : grad_kernel<FSDP_F32, true>;
         }
         if ((st = launch_chained(grad, dgrid, 256, 0, s, d)) != FSDP_OK) return st;
+        if (soft) {
+            const int64_t entry_blocks = ceil_div(rows * d.top, 256);
+            if (entry_blocks > 0x7fffffff) return FSDP_ERR_INVALID_ARG;
+            auto entries = a.dtype == FSDP_BF16  ? entries_kernel<FSDP_BF16>
+                           : a.dtype == FSDP_F16 ? entries_kernel<FSDP_F16>
+                                                 : entries_kernel<FSDP_F32>;
+            st = launch_chained(entries, static_cast<unsigned>(entry_blocks), 256, 0, s, d);
+            if (st != FSDP_OK) return st;
+        }
         if (a.d_hidden) {
             CUtensorMap d_k;
             st = make_map(&d_k, t16, ws + p.d, V, rows, planes, p.ldv, plane, 128);
