@@ -235,12 +235,13 @@ fsdp_status check(const fsdp_head_distill_args *d) {
     if (d->id_bits != 32 && d->id_bits != 64) return FSDP_ERR_UNSUPPORTED_DTYPE;
     if (d->top < 1 || d->top > kMostTop || !(d->temperature >= 1e-3f && d->temperature <= 1e3f))
         return FSDP_ERR_INVALID_ARG;
-    constexpr int64_t kMostLd = int64_t(1) << 34;
+    constexpr int64_t kMostLd = int64_t(1) << 34, kMostArea = int64_t(1) << 50;  // (products of sizes stay inside 64 bits)
     if (d->tokens < 0 || d->ld_teacher_logits < d->top || d->ld_teacher_logits > kMostLd || d->ld_teacher_ids < d->top ||
-        d->ld_teacher_ids > kMostLd || !isfinite(d->grad_scale * d->temperature))
+        d->ld_teacher_ids > kMostLd || d->tokens > kMostArea / d->ld_teacher_logits ||
+        d->tokens > kMostArea / d->ld_teacher_ids || !isfinite(d->grad_scale * d->temperature))
         return FSDP_ERR_INVALID_ARG;
     const size_t entry = d->teacher_dtype == FSDP_F32 ? 4 : 2, token = d->id_bits / 8;
-    const int64_t rows = d->tokens < (int64_t(1) << 30) ? d->tokens : 0;  // (more are refused below)
+    const int64_t rows = d->tokens;
     const void *in[2] = {d->teacher_logits, d->teacher_ids};
     const size_t nin[2] = {rows > 0 ? ((rows - 1) * d->ld_teacher_logits + d->top) * entry : 0,
                            rows > 0 ? ((rows - 1) * d->ld_teacher_ids + d->top) * token : 0};

@@ -7,56 +7,6 @@
 namespace fsdp {
 namespace embed {
 
-// What the lookup's warp copies of a row: 32 lanes times this many words of 16
-// bytes, or of one element where rows are not 16-byte aligned.
-template <int DT, bool VEC> struct Slice {
-    static constexpr int kSize = Dtype<DT>::kSize;
-    static constexpr int kElems = VEC ? 16 / kSize : 1;  // of a word
-    static constexpr int kWords = VEC ? 4 : 16;          // of a lane
-    static constexpr int kCols = 32 * kWords * kElems;
-};
-
-// kElems consecutive values as fp32, and back (rounded once).
-template <int DT, bool VEC> struct Word;
-template <int DT> struct Word<DT, true> {
-    uint4 raw;
-    __device__ __forceinline__ void load(const uint8_t *row, int64_t col) {
-        raw = ld_stream(row + col * Dtype<DT>::kSize);
-    }
-    __device__ __forceinline__ void load_cached(const uint8_t *row, int64_t col) {
-        raw = __ldg(reinterpret_cast<const uint4 *>(row + col * Dtype<DT>::kSize));
-    }
-    __device__ __forceinline__ void load_coherent(const uint8_t *row, int64_t col) {
-        raw = *reinterpret_cast<const uint4 *>(row + col * Dtype<DT>::kSize);
-    }
-    __device__ __forceinline__ void widen(float *f) const {
-        if constexpr (DT == FSDP_F32) {
-            f[0] = __uint_as_float(raw.x), f[1] = __uint_as_float(raw.y);
-            f[2] = __uint_as_float(raw.z), f[3] = __uint_as_float(raw.w);
-        } else {
-            unpack8<DT>(raw, f);
-        }
-    }
-    __device__ __forceinline__ static void store(uint8_t *row, int64_t col, const float *f) {
-        uint4 w;
-        if constexpr (DT == FSDP_F32)
-            w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-        else
-            w = make_uint4(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]), pack2<DT>(f[4], f[5]), pack2<DT>(f[6], f[7]));
-        st_stream(row + col * Dtype<DT>::kSize, w);
-    }
-};
-template <int DT> struct Word<DT, false> {
-    float x;
-    __device__ __forceinline__ void load(const uint8_t *row, int64_t col) { x = Dtype<DT>::load(row, col); }
-    __device__ __forceinline__ void load_cached(const uint8_t *row, int64_t col) { load(row, col); }
-    __device__ __forceinline__ void load_coherent(const uint8_t *row, int64_t col) { load(row, col); }
-    __device__ __forceinline__ void widen(float *f) const { f[0] = x; }
-    __device__ __forceinline__ static void store(uint8_t *row, int64_t col, const float *f) {
-        Dtype<DT>::store(row, col, f[0]);
-    }
-};
-
 struct LookupArgs {
     const int64_t *tokens;
     int64_t n, vocab, dim, ignore;
@@ -64,6 +14,7 @@ struct LookupArgs {
     uint8_t *out;
     int64_t weight_bytes, out_bytes;  // from one row to the next
     int64_t slices;                   // warps of a row
+    int32_t lanes_log;                // or lanes of a short one, a power of two
     float scale;
 };
 

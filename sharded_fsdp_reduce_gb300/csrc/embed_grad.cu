@@ -4,17 +4,19 @@
 //
 // written to the whole table, or added to the rows in use.
 //
-// The tokens are sorted first (one launch: a cluster of up to eight CTAs, a
-// stable radix sort), so that a row's summands lie side by side and add up in
-// one fixed order: the same bits every time, whatever order the warps run in.
-// Rows that no token uses are filled with zeros beside the sort, which keeps
-// only a few SMs busy. Then a CTA adds up 32 to 128 sorted entries for a slice
-// of the columns; what begins and ends within them is written at once, a run
-// that crosses to other CTAs' entries leaves fp32 parts, which the last of
-// them adds in order.
+// The tokens are put in order first, in one launch (few by counting, more by a
+// stable radix sort in a cluster), so that a row's summands lie side by side and
+// add up in one fixed order: the same bits every time, whatever order the warps
+// run in. A second launch has the sums, 32 to 128 sorted entries and 1 KB of
+// their rows to a CTA: what begins and ends within them is written at once, a
+// run that crosses to other CTAs' entries leaves fp32 parts, which the last of
+// them adds in order. The first CTAs of that launch fill the rows that no token
+// uses with zeros; they run beside the sort as well.
 //
-// Bound by HBM: dY is read once, the table written once. 32768 tokens of a
-// 128000 x 8192 bf16 table: 439 us, 5.9 TB/s (zeros 300, sums 131).
+// Bound by HBM for large tables and long batches: dY is read once, the table
+// written once. 32768 tokens of a 128000 x 8192 bf16 table: 387 us, 6.7 TB/s.
+// Bound by the two launches' latency for a few tokens added to a table (1021 of
+// 50257 x 768: 9 us; 8192: 18).
 #include "embed.cuh"
 #include "tcgen.cuh"
 
@@ -24,8 +26,8 @@ namespace {
 
 // ---------------------------------------------------------------- sort
 
-// 512 threads of at most 64 registers: beside a CTA of the fill kernel, an SM
-// holds one of these.
+// 512 threads of at most 64 registers: an SM has room for CTAs of the zeros
+// beside one of these.
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32, kItems = 8;
 constexpr uint32_t kTile = kSortThreads * kItems;  // entries of a CTA in one go
 constexpr int kMostCtas = 16;                      // of the cluster (eight are portable)
@@ -175,10 +177,10 @@ __device__ __forceinline__ uint2 rank_tile(SortShared &s, SortTile &t, int shift
 // A stable radix sort by digits of up to 10 bits. Each CTA has a stretch of the
 // entries; the CTAs' counts of every digit tell where its entries go, which it
 // puts in that order first, so that neighbours go out together. Entries
-// that are no token have the key `vocab` and come last. Up to eight tiles of
-// entries stay in the cluster's shared memory until the last pass. Bound by
-// latency (two passes: 1021 tokens 8 us, 8192 11, 32768 22; through memory and
-// with 1024 threads 14, 16 and 28).
+// that are no token have the key `vocab` and come last. Up to sixteen tiles of
+// entries stay in the cluster's shared memory until the last pass (LARGE: more,
+// through memory). Bound by latency: two passes over 8192 entries take 11 us,
+// over 32768 19, over 65536 22.
 template <bool LARGE>
 __global__ void __launch_bounds__(kSortThreads, 2) sort_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
@@ -460,6 +462,17 @@ template <int DT, bool VEC> __device__ __forceinline__ void read_word(const uint
     }
 }
 
+// A word of a row, rounded.
+template <int DT, bool VEC> __device__ __forceinline__ void store_word(uint8_t *row, int col, const float *f) {
+    if constexpr (!VEC)
+        Dtype<DT>::store(row, col, f[0]);
+    else if constexpr (DT == FSDP_F32)
+        st_state(reinterpret_cast<float *>(row) + col, make_float4(f[0], f[1], f[2], f[3]));
+    else
+        st_stream(row + col * 2, make_uint4(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]), pack2<DT>(f[4], f[5]),
+                                            pack2<DT>(f[6], f[7])));
+}
+
 template <int N> __device__ __forceinline__ void store_floats(float *p, const float *f) {
     if constexpr (N % 4 == 0) {
 #pragma unroll
@@ -651,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, ADD ? 3 : 4) sum_kernel(const __grid
             if constexpr (ADD) read_word<DT, VEC>(there, shift_of(to), j, f);
 #pragma unroll
             for (int e = 0; e < S::kElems; ++e) f[e] = ADD ? fmaf(sum[j][e], a.scale, f[e]) : sum[j][e] * a.scale;
-            Word<DT, VEC>::store(to, col, f);
+            store_word<DT, VEC>(to, col, f);
         }
     };
     auto add_there = [&](const uint8_t *to) {  // (a row that nothing has been copied of)

@@ -88,6 +88,7 @@ def test_refusals(lib, L):
         (dict(teacher_ids=None), bad), (dict(loss=None), bad),
         (dict(ld_hidden=63), bad), (dict(ld_weight=0), bad), (dict(ld_teacher_logits=19), bad),
         (dict(ld_teacher_ids=19), bad), (dict(ld_teacher_ids=1 << 50), bad),
+        (dict(tokens=1 << 30, ld_teacher_ids=1 << 34), bad), (dict(tokens=1 << 29, ld_teacher_logits=1 << 33), bad),
         (dict(hidden=BASE + 1), off), (dict(teacher_logits=BASE + 2 * STEP + 2), off),
         (dict(teacher_ids=BASE + 3 * STEP + 4), off), (dict(loss=BASE + 4 * STEP + 2), off),
         (dict(wait_timeouts=BASE + 2), off),
