@@ -120,20 +120,18 @@ class Embedding:
         self._ws = Workspace(need, self.device) if grad else None
         self._ws_at, self._ws_bytes = (self._ws.buf.data_ptr(), need) if grad else (0, 0)
 
-    def _check(self, tokens, table, name: str) -> None:
+    def _check(self, tokens) -> None:
         if not isinstance(tokens, torch.Tensor) or tokens.numel() > self.max_tokens:
             raise ValueError(f"tokens must hold at most {self.max_tokens}")
-        if not isinstance(table, torch.Tensor) or table.dtype != self.dtype or table.shape != (self.vocab, self.dim):
-            raise ValueError(f"{name} must be [{self.vocab}, {self.dim}] of {self.dtype}")
 
     def forward(self, tokens: torch.Tensor, weight: torch.Tensor, out: Optional[torch.Tensor] = None,
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """scale * weight[tokens], [T, dim]: written to out, or to a new tensor."""
-        self._check(tokens, weight, "weight")
+        self._check(tokens)
         device = torch.cuda.current_device()
         if out is None:
             with torch.cuda.stream(stream):  # a new result belongs to the call's stream
-                out = torch.empty(tokens.numel(), self.dim, dtype=self.dtype, device=weight.device)
+                out = torch.empty(tokens.numel(), self.dim, dtype=self.dtype, device=tokens.device)
         a = _lib.FsdpEmbedArgs.from_buffer_copy(self._lookup)
         _fill(a, tokens, weight, out, self.dtype, device)
         _check(_lib.load().fsdp_embed(ctypes.byref(a), raw_stream(stream, device)), "fsdp_embed")
@@ -144,7 +142,7 @@ class Embedding:
         """The table's gradient from its rows' ([T, dim]), written to d_weight
         whole (zeros where no token points), or added to what it holds
         (accumulate: a table tied to the head, after the head's gradient)."""
-        self._check(tokens, d_weight, "d_weight")
+        self._check(tokens)
         if self._ws is None:
             raise ValueError("this Embedding was made without gradients (grad=False)")
         device = torch.cuda.current_device()
