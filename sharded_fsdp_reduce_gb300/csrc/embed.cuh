@@ -20,7 +20,7 @@ struct LookupArgs {
 
 fsdp_status launch_lookup(const LookupArgs &a, int dtype, cudaStream_t s);
 
-// Largest digit of a sorting pass, and the most passes (30-bit tokens).
+// Bits of a sorting pass's digit, at most.
 constexpr int kMostBits = 10;
 
 struct SortArgs {
@@ -28,12 +28,13 @@ struct SortArgs {
     int64_t ignore;
     uint32_t n, vocab;
     int32_t passes, bits;
-    uint32_t *key[2], *pos[2];  // a pass writes the p % 2-th (few entries: the last pass alone)
+    uint32_t *key[2], *pos[2];  // pass p writes the p % 2-th (up to 65536 entries: the last pass alone)
     uint32_t *tickets;          // cleared for the sums
     uint32_t n_tickets;
 };
 
 constexpr int kSliceBytes = 1024;  // of a row, for a CTA
+// Sorted entries whose sums a CTA forms: 4, 8 or 16 for each of its warps.
 constexpr int kSumWarps = 8, kLeastBlock = 4 * kSumWarps, kMostBlock = 16 * kSumWarps;
 
 struct SumArgs {

@@ -653,8 +653,8 @@ __global__ void __launch_bounds__(kThreads, ADD ? 3 : 4) sum_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < S::kElems; ++e) sum[j][e] = 0.0f;
     };
-    // a lane's columns of a row's sum to the gradient: times scale, and added to
-    // what is there, if `there` is not NULL
+    // a lane's columns of a row's sum to the gradient: times scale, and (ADD) added
+    // to what is there
     auto write_row = [&](uint8_t *to, const uint4 *there) {
 #pragma unroll
         for (int j = 0; j < S::kWords; ++j) {

@@ -149,7 +149,7 @@ class HeadDistill(Head):
     def _run(self, hidden, weight, teacher_logits, teacher_ids, d_hidden, d_weight, grad_scale, loss, token_loss, stream,
              wait_timeouts):
         self._check_operands(hidden, weight)
-        if teacher_ids.dim() != 2 or teacher_ids.shape[1] > self.top:
+        if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 2 or teacher_ids.shape[1] > self.top:
             raise ValueError(f"teacher_ids must be [{hidden.shape[0]}, at most {self.top}]")
         loss, token_loss = self._results(hidden, loss, token_loss, stream)
         a = _lib.FsdpHeadDistillArgs.from_buffer_copy(self._blank)

@@ -13,7 +13,8 @@ roundoff; A = max_v sum_k |x_k w_k| of a row; s a row's entries):
 * a token's loss: the sum over its entries of p times both errors, and of p's
   error times the term; its own sum (s / 32 + 8) 2^-24 of the magnitudes.
 * a gradient element: sums of errors of d times |w| (or |x|): q's error and p's;
-  for 16-bit types d's rounding u and the exponential's 2^-11; 10 % for
+  for 16-bit types d's rounding u and the exponential's 2^-11, but 2^-40 of the
+  largest of its 64 columns where it is small against that; 10 % for
   second-order terms; and the output's own rounding. fp32 heads: the split
   products and sums 4 sqrt(K) 2^-23, the output 2^-23.
 """
@@ -63,6 +64,7 @@ def inputs(T, V, D, K, dt, seed=0, std=0.05, kind="some", teacher=torch.float32,
 
 def reference(x, w, a, i, tau=1.0, reduction="mean", grad_scale=1.0):
     """Loss, row losses, gradients and their error bounds' parts, in fp64."""
+    stored16 = x.dtype != torch.float32
     x, w, i = x.double(), w.double(), i.long()
     T, K = i.shape
     live = (i != -1) & (a.double() != -INF)
@@ -89,7 +91,11 @@ def reference(x, w, a, i, tau=1.0, reduction="mean", grad_scale=1.0):
     tol += tau * tau * (K / 32 + 8) * 2.0 ** -24 * (p * size).sum(1)
     q = torch.exp(logq)
     d = q.clone().scatter_add_(1, torch.where(live, i, 0), -p)
-    ed = (q * (dq[:, None] + 2.0 ** -20)).scatter_add_(1, torch.where(live, i, 0), p * dp)
+    # 16-bit heads: an exponential is an fp16 number times 2^-15 of the largest
+    # of its 64 columns, at half a subnormal step 2^-25 2^-15 off
+    least = torch.nn.functional.pad(q, (0, -q.shape[1] % 64)).view(T, -1, 64).amax(2).repeat_interleave(64, 1)
+    least = least[:, :q.shape[1]] * (2.0 ** -40 if stored16 else 0.0)
+    ed = (q * (dq[:, None] + 2.0 ** -20) + least).scatter_add_(1, torch.where(live, i, 0), p * dp)
     d *= valid[:, None]
     ed *= valid[:, None]
     out = dict(loss=tok.sum() / n, tok=tok, tol=tol * valid + 1e-38, n=n, valid=valid)
@@ -187,6 +193,17 @@ def test_temperatures(F, T, tau, dt):
     check(ref, dt, (1500, T), loss, tok, dx, dw)
     loss, tok, _, _ = run(F, x, w, a, i, tau=tau, grad=False)
     check(ref, dt, (1500, T), loss, tok)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,tau", [(4, 0.5), (4, 0.05), (150, 0.5), (150, 0.05)])
+def test_probabilities_far_apart(F, T, tau, dt):
+    # logits over the temperature up to 100 apart: columns at 2^-40 of their
+    # neighbours and less
+    x, w, a, i = inputs(T, 3001, 264, 5, dt, seed=8, std=0.15 if tau == 0.5 else 0.05, kind="all")
+    ref = reference(x, w, a, i, tau)
+    loss, tok, dx, dw = run(F, x, w, a, i, tau=tau)
+    check(ref, dt, (3001, T), loss, tok, dx, dw)
 
 
 @pytest.mark.parametrize("teacher", ["bf16", "f16", "f32"])
@@ -513,6 +530,7 @@ def test_refusals(F):
         lambda: head.forward_backward(x, w, a, i, dx, dw[:99]),
         lambda: head.forward(x, w, a, i, loss=torch.empty(2, device=DEV)),
         lambda: F.HeadDistill(100, 64, torch.bfloat16, 20, 5, reduction="none"),
+        lambda: head.forward(x, w, a, None),
         lambda: F.HeadDistill(100, 64, torch.float64, 20, 5),
     ):
         with pytest.raises((ValueError, TypeError)):
