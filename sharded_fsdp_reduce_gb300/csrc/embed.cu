@@ -29,12 +29,13 @@ template <int DT, bool VEC, int ROWS> struct Lookup {
     static constexpr int kWords = (VEC ? 4 : 8) / ROWS;
 };
 
-// Two 16-bit elements at a 2-byte boundary, by the aligned words that hold them.
+// Two 16-bit elements at a 2-byte boundary: one aligned word, or each by itself.
+// (Both aligned words around them would reach two bytes before and behind: past
+// the end of a table that ends there.)
 __device__ __forceinline__ uint32_t load_pair(const uint8_t *p) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const uint32_t *word = reinterpret_cast<const uint32_t *>(at & ~uintptr_t(3));
-    const uint32_t low = __ldg(word);
-    return at & 2 ? __byte_perm(low, __ldg(word + 1), 0x5432) : low;
+    if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) return __ldg(reinterpret_cast<const uint32_t *>(p));
+    const uint16_t *half = reinterpret_cast<const uint16_t *>(p);
+    return __ldg(half) | static_cast<uint32_t>(__ldg(half + 1)) << 16;
 }
 
 // The word at p, of the elements first .. of a row of dim; one that the row has
