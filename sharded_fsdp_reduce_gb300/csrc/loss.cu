@@ -149,8 +149,8 @@ __device__ __forceinline__ void write_loss(const RowArgs &a, double sum, long lo
 // teacher's entries and 1021 rows of 50257 columns 10.7 us, with sixteen 13.5;
 // 2048 of 32000 15.5 and 12.3; 4096 of 50257 33 and 22). The cross entropy
 // keeps its sums' order.
-constexpr int64_t kEightRows = 1216;
-inline int block_rows(bool soft, int64_t tokens) { return soft && tokens <= kEightRows ? 8 : 16; }
+inline int64_t eight_rows() { return int64_t(8) * sm_count(); }
+inline int block_rows(bool soft, int64_t tokens) { return soft && tokens <= eight_rows() ? 8 : 16; }
 constexpr int kRowLoads = 8;  // spans a thread reads at once
 
 // 16 (or 8) rows per block of 1024 threads: a warp reads two (four) spans of
@@ -704,10 +704,10 @@ Room room_up_to(const fsdp_head_loss_args &a, int64_t top) {
         r.e = larger(r.e, f.e);
         r.part = larger(r.part, f.part);
     }
-    if (top > 0 && a.tokens > kEightRows) {
+    if (const int64_t eight = eight_rows(); top > 0 && a.tokens > eight) {
         // (shorter ones have blocks of half as many rows; a band ends a block)
         const int64_t each = a.band > 0 ? a.band : kTileM;
-        r.blocks = larger(r.blocks, ceil_div(kEightRows, 8) + ceil_div(kEightRows, each) + 1);
+        r.blocks = larger(r.blocks, ceil_div(eight, 8) + ceil_div(eight, each) + 1);
     }
     // the longest band of these calls: they are as long as their tokens up to
     // what was asked for or what the budget allows
