@@ -499,12 +499,13 @@ fsdp_status fsdp_step_plan_destroy(fsdp_step_plan *plan);
  * Precision: every sum and statistic is fp32 or wider. bf16 and fp16 heads:
  * d is rounded once to the head's type (fp16: times 2^14) for the gradient
  * products, the exponentials are held in fp16 relative to the largest of 64
- * columns before that (off by 2^-40 of it where they are below 2^-29 of it), but for the target's entry, which comes from its fp32
- * logit: p - 1 is good to a few 2^-24 beside the logit's own error. A p that
- * differs from 1 by less than that shows as 1. fp32 heads: every operand as three bf16 parts, the
- * products as exact as fp32's. Infinities and NaN come out as fp32 arithmetic
- * has them, in every type and at any number of tokens. A few tokens (4, or 24 of an fp32 head, for losses alone; 8
- * of an fp32 head with gradients) are plain fp32 dot products.
+ * columns before that (off by 2^-40 of it where they are below 2^-29 of it), but
+ * for the target's entry, which comes from its fp32 logit: p - 1 is good to a few
+ * 2^-24 beside the logit's own error. A p that differs from 1 by less than that
+ * shows as 1. fp32 heads: every operand as three bf16 parts, the products as exact
+ * as fp32's. Infinities and NaN come out as fp32 arithmetic has them, in every
+ * type and at any number of tokens. A few tokens (4, or 24 of an fp32 head, for
+ * losses alone; 8 of an fp32 head with gradients) are plain fp32 dot products.
  *   hidden       device, tokens rows of dim elements at stride ld_hidden.
  *   weight       device, vocab rows of dim elements at stride ld_weight.
  *                Rows that are not 16-byte aligned are packed into the
@@ -581,6 +582,9 @@ fsdp_status fsdp_head_loss(const fsdp_head_loss_args *args, void *workspace, int
  *   hidden, weight, dtype, band, reduction, grad_scale, loss, token_loss, d_*,
  *   wait_timeouts, the precision of it all, the few rows that are plain dot
  *   products, and the workspace's rules: as fsdp_head_loss.
+ * A token loss is off by a few tau^2 2^-24 (1 + |log p| + |log q|), weighted with
+ * p, beside the logits' own errors: at a high temperature that is more than what
+ * a student loses that all but agrees with a teacher of the whole vocabulary.
  *   teacher_logits  device, tokens rows of top values of teacher_dtype at
  *                stride ld_teacher_logits, in any order.
  *   teacher_ids  device, tokens rows of top int32 or int64 (id_bits 32 or 64)
@@ -662,7 +666,10 @@ fsdp_status fsdp_embed(const fsdp_embed_args *args, void *stream);
  *                d_weight holds, rows that no token uses stay as they are: a
  *                table tied to the head, whose gradient is there already, or
  *                another micro-batch.
- *   d_out        device, count rows of dim elements at stride ld_d_out.
+ *   d_out        device, count rows of dim elements at stride ld_d_out. Rows that
+ *                are not 16-byte aligned are read from the last such boundary on
+ *                (so are d_weight's that are added to): what lies between it and
+ *                the row has no effect.
  *   d_weight     device, vocab rows of dim elements at stride ld_d_weight, such
  *                as a parameter's view of a flat gradient buffer; overlaps no
  *                input.

@@ -9,7 +9,7 @@
 // 16384 tokens of a 128000 x 8192 bf16 table 59 us, 6.4 TB/s; of 768 columns
 // 5.2; 65536 of 64 columns 3.5 (9.8 with a warp for each row). Rows of 16-bit
 // elements that are not aligned go in pairs, bound by instructions: 65536 of
-// 771 columns 53 us.
+// 771 columns 50 us.
 #include <math.h>
 
 #include "embed.cuh"
@@ -285,7 +285,7 @@ fsdp_status run_grad(const fsdp_embed_grad_args &a, const Plan &p, uint8_t *ws, 
     r.block = p.block;
     r.words = p.words;
     // three on an SM leave a place for the sums (32768 tokens, 128000 x 8192 bf16:
-    // one 426 us, two 401, three 394, four 391; 1021, 50257 x 768: 29, 17.7, 15.9, 17.1)
+    // one 402 us, two 396, three 389, four 387; 1021, 50257 x 768: 31, 17.6, 15.8, 17.4)
     const int64_t fill = int64_t(sm_count() > 0 ? sm_count() : 1) * 3, most = (a.vocab + 31) / 32;
     r.fill_ctas = a.accumulate ? 0 : static_cast<uint32_t>(fill < most ? fill : most);
     r.tokens = a.tokens;

@@ -14,9 +14,9 @@
 // uses with zeros; they run beside the sort as well.
 //
 // Bound by HBM for large tables and long batches: dY is read once, the table
-// written once. 32768 tokens of a 128000 x 8192 bf16 table: 387 us, 6.7 TB/s.
+// written once. 32768 tokens of a 128000 x 8192 bf16 table: 388 us, 6.7 TB/s.
 // Bound by the two launches' latency for a few tokens added to a table (1021 of
-// 50257 x 768: 9 us; 8192: 18).
+// 50257 x 768: 8 us; 8192: 20).
 #include "embed.cuh"
 #include "tcgen.cuh"
 
@@ -179,8 +179,8 @@ __device__ __forceinline__ uint2 rank_tile(SortShared &s, SortTile &t, int shift
 // puts in that order first, so that neighbours go out together. Entries
 // that are no token have the key `vocab` and come last. Up to sixteen tiles of
 // entries stay in the cluster's shared memory until the last pass (LARGE: more,
-// through memory). Bound by latency: two passes over 8192 entries take 11 us,
-// over 32768 19, over 65536 22.
+// through memory). Bound by latency: two passes over 8192 entries take 9 us,
+// over 32768 16, over 65536 18; through memory over 131072 45, over a million 308.
 template <bool LARGE>
 __global__ void __launch_bounds__(kSortThreads, 2) sort_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
@@ -280,14 +280,14 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_kernel(const __grid_cons
 // Up to 4096 tokens below 2^20 (or none: key `vocab`) are sorted by all CTAs at
 // once: an entry's place is the number of smaller ones, a token and its position
 // in one 32-bit word, which a warp counts in shared memory. In a graph of such
-// launches 1024 entries take 1.6 us (the radix sort with its waits 7.5), 4096 3.5
+// launches 1021 entries take 1.8 us (the radix sort with its waits 7.8), 4096 3.6
 // (8.4).
 constexpr uint32_t kPlaceBits = 12, kPlaceMost = 1u << kPlaceBits;
 static_assert(kPlaceMost * sizeof(uint32_t) <= 116 << 10, "the entries fit");
 constexpr int64_t kPlaceVocab = int64_t(1) << (32 - kPlaceBits);
 constexpr int kPlaceThreads = 1024;
 // More than half of an SM's shared memory, so that no SM gets two CTAs while the
-// kernel before is still on others (4096 tokens: 14 us in all against 17).
+// kernel before is still on others (4096 tokens added: 11.5 us in all, else 13.6).
 constexpr int kPlaceShared = 116 << 10;
 
 __global__ void __launch_bounds__(kPlaceThreads, 1) place_kernel(const __grid_constant__ SortArgs a) {
@@ -353,8 +353,8 @@ __device__ __forceinline__ void zero_row(uint8_t *row, int64_t bytes, int size, 
 // The first CTAs of the sums' grid have a stretch of the table each: they mark
 // the rows that the tokens use and write zeros to the others. They need nothing
 // of the sort before them on the stream and wait for it last, so they run
-// beside it, and the sums beside them as soon as it has ended (32768 tokens,
-// 128000 x 8192 bf16: 394 us where zeros, then sums took 425).
+// beside it, and the sums beside them as soon as it has ended: zeros, then sums
+// took 31 us more for 32768 tokens of 128000 x 8192 bf16.
 __device__ __forceinline__ void fill_rows(const SumArgs &a, uint32_t *used) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t vocab = a.vocab, each = (vocab + a.fill_ctas - 1) / a.fill_ctas;

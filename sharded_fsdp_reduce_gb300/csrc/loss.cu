@@ -26,7 +26,10 @@
 // Against a teacher's top logits (fsdp_head_distill, distill.cu) the same
 // kernels run with the exponentials of the logits over a temperature; the
 // logits of the teacher's entries leave the product in fp32, and take the place
-// of the target's in the row kernel and in d.
+// of the target's in the row kernel and in d. More than one column of a row then
+// is not small, and the gradients are what one rounding of d and one of the result
+// leave: 2.3e-3 for bf16 and 2.9e-4 for fp16 (the same shapes; d formed in 64 bits,
+// rounded to the type and multiplied in 64 bits leaves the same).
 #include <math.h>
 #include <string.h>
 
@@ -363,6 +366,9 @@ template <> struct GradWord<FSDP_F32> {
 
 // 64 rows x 512 columns per block, 8 columns per thread and row. Bound by HBM
 // (or L2, where the band fits): 4 bytes moved per element in 16-bit types.
+// Rows loaded together, the first ones ahead of the factors: the cross entropy's
+// calls take what they took with a row at a time (1021 x 50257 x 768 bf16 210 us,
+// 4096 x 50257 x 1280 fp16 1.17 ms in a loop).
 // SOFT: q alone, whose exponentials are over the temperature; the teacher's
 // entries follow (entries_kernel).
 template <int DT, bool SOFT> __global__ void __launch_bounds__(256) grad_kernel(const __grid_constant__ GradArgs a) {
